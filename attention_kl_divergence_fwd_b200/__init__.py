@@ -16,6 +16,9 @@ The ``*_gqa`` variants take K tensors with fewer heads than Q (grouped-query att
 The ``*_varlen`` variants take packed sequences: q_* [total_q, H, d], k_* [total_k, H_kv, d],
 int32 offsets cu_seqlens_q / cu_seqlens_k [B+1] on the device, row statistics and g
 [H, total_q]; gradients keep the packed shapes of Q and K.
+
+``sparse`` holds what the trained map is used for: block masses, block selection and
+attention over the selected blocks (forward, backward, single tokens).
 """
 from __future__ import annotations
 
@@ -33,6 +36,8 @@ EXPORTS = ("streamkl_fwd", "streamkl_bwd", "streamkl_bwd_teacher", "streamkl_fwd
            "streamkl_bwd_varlen", "streamkl_bwd_teacher_varlen", "streamkl_fwd_partial",
            "streamkl_merge_partial", "streamkl_bwd_shard", "streamkl_bwd_teacher_shard",
            "streamkl_watchdog_selftest", "streamkl_exp2_eval", "streamkl_sm_clock_probe",
+           "streamkl_block_mass", "streamkl_block_select", "streamkl_sparse_attn_workspace",
+           "streamkl_sparse_attn_fwd", "streamkl_sparse_attn_bwd",
            "streamkl_status_string",
            "streamkl_device_status", "streamkl_version")
 
@@ -92,6 +97,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.streamkl_bwd_shard.restype = i
     lib.streamkl_bwd_teacher_shard.argtypes = shead + [vp, vp, vp, vp, vp, vp, vp]
     lib.streamkl_bwd_teacher_shard.restype = i
+    # block-sparse attention (sparse.py)
+    ll = ctypes.c_longlong
+    lib.streamkl_block_mass.argtypes = [vp] * 3 + [i] * 6 + [f, i, vp, vp, ll, vp, vp]
+    lib.streamkl_block_mass.restype = i
+    lib.streamkl_block_select.argtypes = [vp, vp] + [i] * 8 + [vp, vp]
+    lib.streamkl_block_select.restype = i
+    lib.streamkl_sparse_attn_workspace.argtypes = [i] * 9
+    lib.streamkl_sparse_attn_workspace.restype = ll
+    lib.streamkl_sparse_attn_fwd.argtypes = [vp] * 5 + [i] * 8 + [f, i, vp, ll, vp, vp, vp]
+    lib.streamkl_sparse_attn_fwd.restype = i
+    lib.streamkl_sparse_attn_bwd.argtypes = [vp] * 8 + [i] * 8 + [f, i, vp, ll, vp, vp, vp, vp]
+    lib.streamkl_sparse_attn_bwd.restype = i
     lib.streamkl_exp2_eval.argtypes = [vp, vp, vp, ctypes.c_longlong, vp]
     lib.streamkl_exp2_eval.restype = i
     lib.streamkl_sm_clock_probe.argtypes = [vp, ctypes.c_longlong, vp]

@@ -1,0 +1,334 @@
+// block_mass.cuh - probability mass of an attention map on blocks of 64 keys (tcgen05 + TMA).
+//
+//   mass[i, c] = 1/G sum_{g < G} sum_{j in block c, j allowed} exp(scale <q_gi, k_j> - LSE_gi)
+// over the G query heads that share a K head. The map itself is never stored.
+//
+// CTA = one 128-row tile of packed query heads (sparse_common.cuh) and a range of blocks. K
+// streams through a ring in pairs of blocks; per pair one N = 128 product into one of two TMEM
+// score buffers; one thread per row reduces each block's 64 scores to one number. The row
+// numbers of 32 blocks are staged in shared memory, summed over the heads of the group and
+// written as 128 contiguous bytes per query.
+// With the LSEs at hand (the divergence's forward has them) that is the result. Without them
+// (NORM = false) the kernel writes per head the block's base-2 log-sum-exp, and a second kernel
+// sums those to the row's LSE: the scores of a block need no running maximum across blocks,
+// so the keys of one query can be spread over as many CTAs as there are pairs of blocks.
+// Bound by the exponential unit (one exponential per pair) for many queries, by reading K for
+// few. Two CTAs per SM.
+//
+// Warps: 0-3 rows, 4 TMA producer, 5 MMA + TMEM.
+#pragma once
+
+#include "sparse_common.cuh"
+
+namespace skl {
+
+struct MassArgs {
+  SparseArgs s;         // P = K heads of the map, G = query heads per K head
+  int bpc;              // blocks per CTA (a multiple of 2), n_chunks = ceil(NB / bpc)
+  int n_chunks;
+  const float* row_lse; // [B, H, N_Q] (NORM)
+  float* mass;          // [B, P, N_Q, NB] (NORM)
+  float* blse;          // [B, H, N_Q, NB] base-2 log-sum-exp of each visible block (!NORM)
+};
+
+template <int D>
+struct MassCfg {
+  static constexpr int BM = 128;
+  static constexpr int QBYTES = BM * D * 2;
+  static constexpr int KBYTES = 128 * D * 2;
+  static constexpr int NST = D == 128 ? 2 : 4;
+  static constexpr int OFF_K = QBYTES;
+  static constexpr int OFF_STG = OFF_K + NST * KBYTES;  // [128 rows][33] floats
+  static constexpr int OFF_BAR = OFF_STG + 128 * 33 * 4;
+  static constexpr int SMEM = OFF_BAR + 256;
+  static constexpr int TM_COLS = 256;
+  static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
+};
+
+struct MassBars {
+  uint64_t q_full;
+  uint64_t k_full[4], k_empty[4];
+  uint64_t s_full[2], s_free[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(MassBars) <= 256, "barrier block");
+
+constexpr int kMassThreads = 192;
+
+// Row value of one block: sum 2^(s c - lse2) (NORM) or log2 sum 2^(s c).
+template <bool NORM>
+__device__ __forceinline__ float mass_block(const uint32_t (&v)[64], float c, float nl, int lim) {
+  float bias = nl;
+  if (!NORM) {
+    float mx = -INFINITY;
+    if (lim >= 63) {
+      mx = fmaxf(max_tree32<false>(v, 0, 31), max_tree32<false>(v, 32, 31));
+    } else {
+      mx = fmaxf(max_tree32<true>(v, 0, lim), max_tree32<true>(v, 32, lim - 32));
+    }
+    if (mx == -INFINITY) return -INFINITY;
+    bias = -mx * c;
+  }
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  if (lim >= 63) {
+#pragma unroll
+    for (int k = 0; k < 64; k += 4) {
+      s0 += ex2_approx(fmaf(__uint_as_float(v[k]), c, bias));
+      s1 += ex2_approx(fmaf(__uint_as_float(v[k + 1]), c, bias));
+      s2 += ex2_approx(fmaf(__uint_as_float(v[k + 2]), c, bias));
+      s3 += ex2_approx(fmaf(__uint_as_float(v[k + 3]), c, bias));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 64; ++k) {
+      const float e = ex2_approx(fmaf(__uint_as_float(v[k]), c, bias));
+      s0 += k <= lim ? e : 0.f;
+    }
+  }
+  const float s = (s0 + s1) + (s2 + s3);
+  return NORM ? s : log2f(s) - bias;
+}
+
+template <int D, bool NORM>
+__global__ void __launch_bounds__(kMassThreads, 2)
+streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
+                           const __grid_constant__ CUtensorMap map_k, const MassArgs ma,
+                           const uint32_t idesc) {
+  using C = MassCfg<D>;
+  const SparseArgs& a = ma.s;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_skl_error, 4u);
+    return;
+  }
+  MassBars* bars = reinterpret_cast<MassBars*>(smem + C::OFF_BAR);
+  float* stage = reinterpret_cast<float*>(smem + C::OFF_STG);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int chunk = blockIdx.x % ma.n_chunks, unit = blockIdx.x / ma.n_chunks;
+  const int bp = unit / a.n_tiles, tile = a.n_tiles - 1 - unit % a.n_tiles;
+  const int b = bp / a.P, p = bp - b * a.P;
+  const int q0 = tile * a.Qn, h0 = b * a.H + p * a.G;
+  const int nk = sp_len(a.lens, b, a.N_K);
+  const int c_begin = chunk * ma.bpc, c_end = min(a.NB, c_begin + ma.bpc);
+  // Blocks that the tile's last query sees; the rest of the range is only written as 0.
+  const int last_tile = sp_last(min(q0 + a.Qn, a.N_Q) - 1, nk, a.N_Q, a.causal);
+  const int n_vis = min(c_end, last_tile / kSpBlock + (last_tile >= 0 ? 1 : 0)) - c_begin;
+  const int steps = n_vis > 0 ? (n_vis + 1) / 2 : 0;
+  if (!NORM && steps == 0) return;
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bars->q_full), 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(smem_u32(&bars->k_full[s]), 1);
+      mbar_init(smem_u32(&bars->k_empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&bars->s_full[s]), 1);
+      mbar_init(smem_u32(&bars->s_free[s]), 4);
+    }
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp < 4) {
+    const int r = warp * 32 + lane;
+    const int g = r / a.Qn, qi = r - g * a.Qn, i = q0 + qi;
+    const bool valid = g < a.G && i < a.N_Q;
+    const int last = valid ? sp_last(i, nk, a.N_Q, a.causal) : -1;
+    const bool warp_live = __any_sync(0xffffffffu, valid);
+    const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16);
+    const float c = a.c;
+    float nl = 0.f;
+    bool row_on = valid;
+    if (NORM && valid) {
+      const float l = __ldg(ma.row_lse + (size_t)(h0 + g) * a.N_Q + i);
+      row_on = l != -INFINITY;
+      nl = row_on ? -l * 1.4426950408889634f : 0.f;
+    }
+    // Queries of this tile that exist; rows are written for those only.
+    const int nq = min(a.Qn, a.N_Q - q0);
+    const float inv_g = 1.f / (float)a.G;
+    // Writes the staged values of blocks cg .. cg + n - 1.
+    auto flush = [&](int cg, int n) {
+      named_bar_sync(1, 128);
+      if (NORM) {
+        float* dst = ma.mass + ((size_t)bp * a.N_Q + q0) * a.NB + cg;
+        for (int q = warp; q < nq; q += 4) {
+          float s = 0.f;
+          for (int h = 0; h < a.G; ++h) s += stage[(h * a.Qn + q) * 33 + lane];
+          if (lane < n) dst[(size_t)q * a.NB + lane] = s * inv_g;
+        }
+      } else {
+        float* dst = ma.blse + ((size_t)h0 * a.N_Q + q0) * a.NB + cg;
+        for (int h = 0; h < a.G; ++h)
+          for (int q = warp; q < nq; q += 4)
+            if (lane < n) dst[((size_t)h * a.N_Q + q) * a.NB + lane] = stage[(h * a.Qn + q) * 33 + lane];
+      }
+      named_bar_sync(1, 128);
+    };
+    bool ok = true;
+    const int n_blocks = c_end - c_begin;
+    for (int s = 0; s < steps; ++s) {
+      // After a wait that ran out the warp still takes part in every named barrier.
+      if (ok && !mbar_wait(smem_u32(&bars->s_full[s & 1]), (s >> 1) & 1)) ok = false;
+      tc_fence_after();
+      const int cb = 2 * s;  // first block of the pair, from c_begin
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = NORM ? 0.f : -INFINITY;
+        if (warp_live) {
+          uint32_t v[64];
+          tmem_ld_2x32_wait(ts + (s & 1) * 128 + 64 * h, ts + (s & 1) * 128 + 64 * h + 32, v);
+          const int lim = row_on ? last - (c_begin + cb + h) * kSpBlock : -1;
+          if (__all_sync(0xffffffffu, lim >= 63)) {
+            x = mass_block<NORM>(v, c, nl, 63);
+          } else if (__any_sync(0xffffffffu, lim >= 0)) {
+            const float y = mass_block<NORM>(v, c, nl, min(lim, 62));
+            const float z = mass_block<NORM>(v, c, nl, 63);
+            x = lim >= 63 ? z : (lim >= 0 ? y : x);
+          }
+        }
+        stage[r * 33 + ((cb + h) & 31)] = x;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[s & 1]));
+      if (((cb + 2) & 31) == 0 || s == steps - 1) {
+        const int cg = cb & ~31;
+        flush(c_begin + cg, min(cb + 2, n_blocks) - cg);
+      }
+    }
+    if (!ok) {
+      atomicOr(&g_skl_error, 1u);
+      *abort_flag = 1;
+    }
+    if (NORM) {  // blocks that no query of the tile sees
+      const int z0 = c_begin + min(2 * steps, n_blocks);
+      float* dst = ma.mass + ((size_t)bp * a.N_Q + q0) * a.NB;
+      for (int q = warp; q < nq; q += 4)
+        for (int cc = z0 + lane; cc < c_end; cc += 32) dst[(size_t)q * a.NB + cc] = 0.f;
+    }
+  } else if (warp == 4) {
+    if (lane == 0 && steps > 0) {
+      tma_prefetch_desc(&map_q);
+      tma_prefetch_desc(&map_k);
+      const uint64_t keep = l2_policy_evict_last();
+      const uint32_t qb = smem_u32(&bars->q_full);
+      mbar_arrive_expect_tx(qb, a.Qn * a.G * D * 2);
+      for (int blk = 0; blk < D / 64; ++blk)
+        tma_load_3d(sb + blk * (C::BM * 128), &map_q, qb, blk * 64, q0, h0, keep);
+      int issued = 0;
+      for (int s = 0; s < steps; ++s) {
+        const int st = s % C::NST;
+        if (!mbar_wait(smem_u32(&bars->k_empty[st]), ((s / C::NST) & 1) ^ 1)) {
+          atomicOr(&g_skl_error, 1u);
+          *abort_flag = 1;
+          break;
+        }
+        const uint32_t kf = smem_u32(&bars->k_full[st]);
+        mbar_arrive_expect_tx(kf, C::KBYTES);
+        for (int blk = 0; blk < D / 64; ++blk)
+          tma_load_3d(sb + C::OFF_K + st * C::KBYTES + blk * (128 * 128), &map_k, kf, blk * 64,
+                      (c_begin + 2 * s) * kSpBlock, bp, keep);
+        issued = s + 1;
+      }
+      if (*abort_flag) {
+        mbar_wait(qb, 0);
+        for (int j = max(0, issued - C::NST); j < issued; ++j)
+          mbar_wait(smem_u32(&bars->k_full[j % C::NST]), (j / C::NST) & 1);
+      }
+    }
+  } else if (steps > 0 && elect_one()) {
+    bool ok = mbar_wait(smem_u32(&bars->q_full), 0);
+    for (int s = 0; ok && s < steps; ++s) {
+      const int st = s % C::NST;
+      ok = mbar_wait(smem_u32(&bars->k_full[st]), (s / C::NST) & 1) &&
+           mbar_wait(smem_u32(&bars->s_free[s & 1]), ((s >> 1) & 1) ^ 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sk = sb + C::OFF_K + st * C::KBYTES;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+        umma_bf16_ss(tmem + (s & 1) * 128, sdesc_sw128(sb + off, 16, 1024),
+                     sdesc_sw128(sk + off, 16, 1024), idesc, kk > 0);
+      }
+      umma_commit(smem_u32(&bars->k_empty[st]));
+      umma_commit(smem_u32(&bars->s_full[s & 1]));
+    }
+    umma_commit(smem_u32(&bars->drain));
+    if (!ok) {
+      atomicOr(&g_skl_error, 1u);
+      *abort_flag = 1;
+    }
+    mbar_wait(smem_u32(&bars->drain), 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+// Second kernel of the form without LSEs: mass[c] = 1/G sum_g 2^(x_gc - L_g), with
+// L_g = log2 sum_c 2^(x_gc) over the row's visible blocks. One CTA per (K head, query).
+__global__ void __launch_bounds__(256) streamkl_block_norm_kernel(const MassArgs ma) {
+  const SparseArgs& a = ma.s;
+  __shared__ float red[8];
+  const int bp = blockIdx.x / a.N_Q, i = blockIdx.x - bp * a.N_Q, b = bp / a.P, p = bp - b * a.P;
+  const int nk = sp_len(a.lens, b, a.N_K);
+  const int last = sp_last(i, nk, a.N_Q, a.causal);
+  const int n = last < 0 ? 0 : last / kSpBlock + 1;
+  float* dst = ma.mass + ((size_t)bp * a.N_Q + i) * a.NB;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float inv_g = 1.f / (float)a.G;
+  if (n == 0) {
+    for (int c = threadIdx.x; c < a.NB; c += blockDim.x) dst[c] = 0.f;
+    return;
+  }
+  for (int g = 0; g < a.G; ++g) {
+    const float* x = ma.blse + ((size_t)(b * a.H + p * a.G + g) * a.N_Q + i) * a.NB;
+    float mx = -INFINITY;
+    for (int c = threadIdx.x; c < n; c += blockDim.x) mx = fmaxf(mx, x[c]);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    if (lane == 0) red[warp] = mx;
+    __syncthreads();
+    mx = red[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) mx = fmaxf(mx, red[k]);
+    __syncthreads();
+    float sum = 0.f;
+    for (int c = threadIdx.x; c < n; c += blockDim.x) sum += exp2f(x[c] - mx);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();
+    sum = red[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) sum += red[k];
+    __syncthreads();
+    const float f = inv_g / sum;
+    for (int c = threadIdx.x; c < a.NB; c += blockDim.x) {
+      const float y = c < n ? exp2f(x[c] - mx) * f : 0.f;
+      dst[c] = g == 0 ? y : dst[c] + y;  // the same thread wrote it
+    }
+  }
+}
+
+}  // namespace skl

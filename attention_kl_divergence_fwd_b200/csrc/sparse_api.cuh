@@ -1,0 +1,318 @@
+// sparse_api.cuh - argument checks and launch planner of the block-sparse attention entry
+// points (include/streamkl.h states the contract). Part of streamkl_api.cu.
+#pragma once
+
+namespace {
+
+// Tensor map over [heads, rows, d] bf16 with a box of 64 columns x box_rows x box_heads.
+bool make_map_heads(CUtensorMap* m, const void* base, int d, long long rows, long long heads,
+                    int box_rows, int box_heads) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)rows * d * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_heads};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+constexpr int kMaxTopk = 1 << 20;
+
+// Sizes common to every block-sparse entry point, and the packing of rows into tiles.
+streamkl_status sparse_problem(skl::SparseArgs& a, const int* lens, int B, int H, int Hkv,
+                               int Hsel, int N_Q, int N_K, int d, float scale, int causal) {
+  if (B < 1 || H < 1 || N_Q < 1 || N_K < 1 || !std::isfinite(scale))
+    return STREAMKL_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return STREAMKL_ERR_UNSUPPORTED;
+  if (Hkv < 1 || Hsel < 1 || H % Hkv != 0 || H % Hsel != 0) return STREAMKL_ERR_UNSUPPORTED;
+  const int P = Hkv > Hsel ? Hkv : Hsel;
+  if (P % Hkv != 0 || P % Hsel != 0 || H / P > 128) return STREAMKL_ERR_UNSUPPORTED;
+  const long long bh = (long long)B * H, nmax = N_Q > N_K ? N_Q : N_K;
+  if (bh >= (1ll << 24) || bh * nmax >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
+  if (misaligned4(lens)) return STREAMKL_ERR_MISALIGNED;
+  a.B = B;
+  a.H = H;
+  a.N_Q = N_Q;
+  a.N_K = N_K;
+  a.NB = (N_K + skl::kSpBlock - 1) / skl::kSpBlock;
+  a.P = P;
+  a.G = H / P;
+  a.Hkv = Hkv;
+  a.Hsel = Hsel;
+  a.Qn = 1;
+  while (a.Qn * 2 * a.G <= 128 && a.Qn < N_Q) a.Qn *= 2;
+  a.n_tiles = (N_Q + a.Qn - 1) / a.Qn;
+  a.causal = causal ? 1 : 0;
+  a.splits = 1;
+  // A scale of 0 keeps a positive factor (masked scores are -inf, and -inf * 0 is NaN); it is
+  // far below what the scores' products with it can show in fp32.
+  a.c = scale == 0.f ? 1e-30f : std::fabs(scale) * kLog2e;
+  a.scale = scale;
+  a.lens = lens;
+  return STREAMKL_OK;
+}
+
+long long round256(long long n) { return (n + 255) / 256 * 256; }
+
+long long mask_bytes(const skl::SparseArgs& a) {
+  return round256(4ll * a.B * a.Hsel * ((a.N_Q + 31) / 32) * a.NB);
+}
+
+// CTAs that share a tile's list: with fewer tiles than about two waves of CTAs (two per SM) the
+// lists are dealt out, down to one pair of blocks per CTA.
+int sparse_splits(const skl::SparseArgs& a) {
+  const long long ctas = (long long)a.B * a.P * a.n_tiles, want = 4ll * sm_count();
+  long long blocks = (long long)a.Qn * a.topk;
+  if (blocks > a.NB) blocks = a.NB;
+  long long s = (want + ctas - 1) / ctas;
+  if (s > (blocks + 1) / 2) s = (blocks + 1) / 2;
+  return (int)(s < 1 ? 1 : (s > 32 ? 32 : s));
+}
+
+bool sparse_direct(const skl::SparseArgs& a) {
+  return a.N_Q == 1 && a.G <= 64 && a.NB <= 65536;
+}
+
+long long fwd_ws_bytes(const skl::SparseArgs& a, int d) {
+  const long long rows = (long long)a.B * a.H * a.N_Q;
+  const int s = sparse_splits(a);
+  return (sparse_direct(a) ? 0 : mask_bytes(a)) +
+         (s > 1 ? round256(4ll * s * rows * d) + round256(4ll * s * rows) : 0);
+}
+
+long long bwd_ws_bytes(const skl::SparseArgs& a) {
+  return mask_bytes(a) + round256(8ll * a.B * a.H * a.N_Q);
+}
+
+streamkl_status ok_launch() {
+  return cudaGetLastError() == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_LAUNCH;
+}
+
+streamkl_status launch_mask(skl::SparseArgs& a, void* ws, cudaStream_t stream) {
+  const long long grid = (long long)((a.N_Q + 31) / 32) * a.B * a.Hsel;
+  uint32_t* mask = static_cast<uint32_t*>(ws);
+  skl::streamkl_sparse_mask_kernel<<<(unsigned)grid, 128, 0, stream>>>(a, mask);
+  a.mask = mask;
+  return ok_launch();
+}
+
+template <int D>
+streamkl_status launch_sparse_fwd(const skl::SparseArgs& a, const void* q, const void* k,
+                                  const void* v, cudaStream_t stream) {
+  using C = skl::SpFwdCfg<D>;
+  CUtensorMap mq, mk, mv;
+  if (!make_map_heads(&mq, q, D, a.N_Q, (long long)a.B * a.H, a.Qn, a.G) ||
+      !make_map_heads(&mk, k, D, a.N_K, (long long)a.B * a.Hkv, 64, 1) ||
+      !make_map_heads(&mv, v, D, a.N_K, (long long)a.B * a.Hkv, 64, 1))
+    return STREAMKL_ERR_LAUNCH;
+  auto kern = skl::streamkl_sparse_fwd_kernel<D>;
+  if (!set_smem(kern, C::SMEM)) return STREAMKL_ERR_LAUNCH;
+  const bool neg = a.scale < 0.f;
+  const long long grid = (long long)a.B * a.P * a.n_tiles * a.splits;
+  kern<<<(unsigned)grid, skl::kSpThreads, C::SMEM, stream>>>(
+      mq, mk, mv, a, skl::idesc_bf16_f32(128, 128, false, false, neg),
+      skl::idesc_bf16_f32(128, 64, false, false, neg), skl::idesc_bf16_f32(128, D, false, true));
+  if (a.splits > 1) {
+    const long long rows = (long long)a.B * a.H * a.N_Q;
+    skl::streamkl_sparse_merge_kernel<D><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(a);
+  }
+  return ok_launch();
+}
+
+template <int D>
+streamkl_status launch_sparse_bwd(const skl::SparseArgs& a, const void* q, const void* k,
+                                  const void* v, const void* out, const float* lse,
+                                  const void* dout, cudaStream_t stream) {
+  using CQ = skl::SpDqCfg<D>;
+  using CK = skl::SpDkvCfg<D>;
+  CUtensorMap mq, mdo, mk, mv;
+  if (!make_map_heads(&mq, q, D, a.N_Q, (long long)a.B * a.H, a.Qn, a.G) ||
+      !make_map_heads(&mdo, dout, D, a.N_Q, (long long)a.B * a.H, a.Qn, a.G) ||
+      !make_map_heads(&mk, k, D, a.N_K, (long long)a.B * a.Hkv, 64, 1) ||
+      !make_map_heads(&mv, v, D, a.N_K, (long long)a.B * a.Hkv, 64, 1))
+    return STREAMKL_ERR_LAUNCH;
+  auto kq = skl::streamkl_sparse_dq_kernel<D>;
+  auto kk = skl::streamkl_sparse_dkv_kernel<D>;
+  if (!set_smem(kq, CQ::SMEM) || !set_smem(kk, CK::SMEM)) return STREAMKL_ERR_LAUNCH;
+  const bool neg = a.scale < 0.f;
+  const uint32_t i_s = skl::idesc_bf16_f32(128, 64, false, false, neg);
+  const uint32_t i_dp = skl::idesc_bf16_f32(128, 64, false, false);
+  const long long rows = (long long)a.B * a.H * a.N_Q;
+  skl::streamkl_sparse_rows_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout), lse, rows,
+      a.rows);
+  kk<<<(unsigned)((long long)a.B * a.Hkv * a.NB), skl::kSpDkvThreads, CK::SMEM, stream>>>(
+      mq, mdo, mk, mv, a, i_s, i_dp, skl::idesc_bf16_f32(128, 64, true, true));
+  kq<<<(unsigned)((long long)a.B * a.P * a.n_tiles), skl::kSpThreads, CQ::SMEM, stream>>>(
+      mq, mdo, mk, mv, a, i_s, i_dp, skl::idesc_bf16_f32(128, D, false, true));
+  return ok_launch();
+}
+
+template <int D, bool NORM>
+streamkl_status launch_mass(const skl::MassArgs& ma, const void* q, const void* k,
+                            cudaStream_t stream) {
+  using C = skl::MassCfg<D>;
+  const skl::SparseArgs& a = ma.s;
+  CUtensorMap mq, mk;
+  if (!make_map_heads(&mq, q, D, a.N_Q, (long long)a.B * a.H, a.Qn, a.G) ||
+      !make_map_heads(&mk, k, D, a.N_K, (long long)a.B * a.P, 128, 1))
+    return STREAMKL_ERR_LAUNCH;
+  auto kern = skl::streamkl_block_mass_kernel<D, NORM>;
+  if (!set_smem(kern, C::SMEM)) return STREAMKL_ERR_LAUNCH;
+  const long long grid = (long long)a.B * a.P * a.n_tiles * ma.n_chunks;
+  if (grid >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
+  kern<<<(unsigned)grid, skl::kMassThreads, C::SMEM, stream>>>(
+      mq, mk, ma, skl::idesc_bf16_f32(128, 128, false, false, a.scale < 0.f));
+  if (!NORM)
+    skl::streamkl_block_norm_kernel<<<(unsigned)((long long)a.B * a.P * a.N_Q), 256, 0, stream>>>(
+        ma);
+  return ok_launch();
+}
+
+}  // namespace
+
+extern "C" {
+
+long long streamkl_sparse_attn_workspace(int B, int H, int H_kv, int H_sel, int N_Q, int N_K,
+                                         int d, int topk, int backward) {
+  skl::SparseArgs a{};
+  if (topk < 1 || topk > kMaxTopk ||
+      sparse_problem(a, nullptr, B, H, H_kv, H_sel, N_Q, N_K, d, 1.f, 0) != STREAMKL_OK)
+    return -1;
+  a.topk = topk;
+  return backward ? bwd_ws_bytes(a) : fwd_ws_bytes(a, d);
+}
+
+streamkl_status streamkl_sparse_attn_fwd(const void* q, const void* k, const void* v,
+                                         const int* block_idx, const int* seqlens_k, int B, int H,
+                                         int H_kv, int H_sel, int N_Q, int N_K, int d, int topk,
+                                         float scale, int causal, void* workspace,
+                                         long long workspace_bytes, void* out, float* lse,
+                                         cudaStream_t stream) {
+  skl::SparseArgs a{};
+  const streamkl_status st =
+      sparse_problem(a, seqlens_k, B, H, H_kv, H_sel, N_Q, N_K, d, scale, causal);
+  if (st != STREAMKL_OK) return st;
+  if (topk < 1 || !q || !k || !v || !block_idx || !out || !lse) return STREAMKL_ERR_INVALID_ARG;
+  if (topk > kMaxTopk) return STREAMKL_ERR_UNSUPPORTED;
+  a.topk = topk;
+  const long long need = fwd_ws_bytes(a, d);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return STREAMKL_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse) ||
+      !aligned16(workspace) || misaligned4(block_idx))
+    return STREAMKL_ERR_MISALIGNED;
+  a.idx = block_idx;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.splits = sparse_splits(a);
+  a.direct = sparse_direct(a) ? 1 : 0;
+  char* ws = static_cast<char*>(workspace);
+  if (!a.direct) {
+    const streamkl_status sm = launch_mask(a, ws, stream);
+    if (sm != STREAMKL_OK) return sm;
+    ws += mask_bytes(a);
+  }
+  if (a.splits > 1) {
+    const long long rows = (long long)B * H * N_Q;
+    a.part_o = reinterpret_cast<float*>(ws);
+    a.part_l = reinterpret_cast<float*>(ws + round256(4ll * a.splits * rows * d));
+  }
+  return d == 128 ? launch_sparse_fwd<128>(a, q, k, v, stream)
+                  : launch_sparse_fwd<64>(a, q, k, v, stream);
+}
+
+streamkl_status streamkl_sparse_attn_bwd(const void* q, const void* k, const void* v,
+                                         const void* out, const float* lse, const void* dout,
+                                         const int* block_idx, const int* seqlens_k, int B, int H,
+                                         int H_kv, int H_sel, int N_Q, int N_K, int d, int topk,
+                                         float scale, int causal, void* workspace,
+                                         long long workspace_bytes, void* dq, void* dk, void* dv,
+                                         cudaStream_t stream) {
+  skl::SparseArgs a{};
+  const streamkl_status st =
+      sparse_problem(a, seqlens_k, B, H, H_kv, H_sel, N_Q, N_K, d, scale, causal);
+  if (st != STREAMKL_OK) return st;
+  if (topk < 1 || !q || !k || !v || !out || !lse || !dout || !block_idx || !dq || !dk || !dv)
+    return STREAMKL_ERR_INVALID_ARG;
+  if (topk > kMaxTopk) return STREAMKL_ERR_UNSUPPORTED;
+  a.topk = topk;
+  if (!workspace || workspace_bytes < bwd_ws_bytes(a)) return STREAMKL_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse) ||
+      !aligned16(dout) || !aligned16(workspace) || !aligned16(dq) || !aligned16(dk) ||
+      !aligned16(dv) || misaligned4(block_idx))
+    return STREAMKL_ERR_MISALIGNED;
+  a.idx = block_idx;
+  a.dq = static_cast<__nv_bfloat16*>(dq);
+  a.dk = static_cast<__nv_bfloat16*>(dk);
+  a.dv = static_cast<__nv_bfloat16*>(dv);
+  char* ws = static_cast<char*>(workspace);
+  a.rows = reinterpret_cast<float2*>(ws + mask_bytes(a));
+  const streamkl_status sm = launch_mask(a, ws, stream);
+  if (sm != STREAMKL_OK) return sm;
+  return d == 128 ? launch_sparse_bwd<128>(a, q, k, v, out, lse, dout, stream)
+                  : launch_sparse_bwd<64>(a, q, k, v, out, lse, dout, stream);
+}
+
+streamkl_status streamkl_block_mass(const void* q, const void* k, const int* seqlens_k, int B,
+                                    int H, int H_kv, int N_Q, int N_K, int d, float scale,
+                                    int causal, const float* lse, void* workspace,
+                                    long long workspace_bytes, float* mass, cudaStream_t stream) {
+  skl::MassArgs ma{};
+  const streamkl_status st =
+      sparse_problem(ma.s, seqlens_k, B, H, H_kv, H_kv, N_Q, N_K, d, scale, causal);
+  if (st != STREAMKL_OK) return st;
+  const skl::SparseArgs& a = ma.s;
+  if (!q || !k || !mass) return STREAMKL_ERR_INVALID_ARG;
+  if (!lse && (!workspace || workspace_bytes < 4ll * B * H * N_Q * a.NB))
+    return STREAMKL_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(mass) || !aligned16(lse) ||
+      !aligned16(workspace))
+    return STREAMKL_ERR_MISALIGNED;
+  ma.row_lse = lse;
+  ma.mass = mass;
+  ma.blse = lse ? nullptr : static_cast<float*>(workspace);
+  // A tile's blocks are spread over CTAs while there are fewer than about two waves of them
+  // (two per SM); a CTA takes at least one pair.
+  const long long tiles = (long long)a.B * a.P * a.n_tiles, want = 4ll * sm_count();
+  long long chunks = (want + tiles - 1) / tiles;
+  long long bpc = (a.NB + chunks - 1) / chunks;
+  bpc = (bpc + 1) / 2 * 2;
+  ma.bpc = (int)bpc;
+  ma.n_chunks = (int)((a.NB + bpc - 1) / bpc);
+  if (d == 128)
+    return lse ? launch_mass<128, true>(ma, q, k, stream) : launch_mass<128, false>(ma, q, k, stream);
+  return lse ? launch_mass<64, true>(ma, q, k, stream) : launch_mass<64, false>(ma, q, k, stream);
+}
+
+streamkl_status streamkl_block_select(const float* mass, const int* seqlens_k, int B, int H_sel,
+                                      int N_Q, int N_K, int causal, int topk, int n_first,
+                                      int n_last, int* block_idx, cudaStream_t stream) {
+  if (!mass || !block_idx || B < 1 || H_sel < 1 || N_Q < 1 || N_K < 1 || topk < 1 ||
+      n_first < 0 || n_last < 0 || n_first > topk || n_last > topk - n_first)
+    return STREAMKL_ERR_INVALID_ARG;
+  const long long rows = (long long)B * H_sel * N_Q;
+  const int nb = (N_K + skl::kSpBlock - 1) / skl::kSpBlock;
+  if (topk > kMaxTopk || (long long)B * H_sel >= (1ll << 24) || rows >= (1ll << 31) || nb > 8192)
+    return STREAMKL_ERR_UNSUPPORTED;
+  if (!aligned16(mass) || !aligned16(block_idx) || misaligned4(seqlens_k))
+    return STREAMKL_ERR_MISALIGNED;
+  const skl::SelectArgs a{mass, seqlens_k, block_idx, rows,   H_sel,   N_Q,
+                          N_K,  nb,        causal ? 1 : 0, topk, n_first, n_last};
+  const unsigned warp_grid = (unsigned)((rows + 3) / 4), cta_grid = (unsigned)rows;
+  if (nb <= 64)
+    skl::streamkl_block_select_kernel<2, 1><<<warp_grid, 128, 0, stream>>>(a);
+  else if (nb <= 256)
+    skl::streamkl_block_select_kernel<8, 1><<<warp_grid, 128, 0, stream>>>(a);
+  else if (nb <= 1024)
+    skl::streamkl_block_select_kernel<32, 1><<<warp_grid, 128, 0, stream>>>(a);
+  else
+    skl::streamkl_block_select_kernel<32, 8><<<cta_grid, 256, 0, stream>>>(a);
+  return ok_launch();
+}
+
+}  // extern "C"

@@ -1,0 +1,647 @@
+// sparse_bwd.cuh - attention over selected key blocks, backward (tcgen05 + TMEM + TMA).
+//
+// With p_ij = exp(s_ij - LSE_i) recomputed tile by tile, D_i = sum_d out_i dout_i and
+//   dP_ij = <dout_i, v_j>,  dS_ij = p_ij (dP_ij - D_i):
+//   dV_j = sum_i p_ij dout_i,  dK_j = scale sum_i dS_ij q_i,  dQ_i = scale sum_j dS_ij k_j.
+// Two kernels, one per direction of the bit matrix, so that every sum has one owner: no
+// atomics, the same bits every time, and K heads shared by a group of query heads are summed
+// inside one CTA (a tile's rows are the whole group). Recomputing S and dP in both costs 7
+// products per tile pair instead of 5; adding dQ parts (or dK and dV parts) through L2 instead
+// would move 64 KB of fp32 per (tile, block) pair, more time than the two extra products.
+// P and dS are rounded to bf16 for the tensor core; every accumulator is fp32, and each
+// gradient is rounded once, to bf16.
+#pragma once
+
+#include "sparse_fwd.cuh"
+
+namespace skl {
+
+// rows[r] = {LSE * log2(e), sum_d out * dout}: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(256)
+streamkl_sparse_rows_kernel(const __nv_bfloat16* out, const __nv_bfloat16* dout, const float* lse,
+                            long long rows, float2* dst) {
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  float acc = 0.f;
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) {
+    const size_t at = (size_t)row * D + k * 64 + lane * 2;
+    const __nv_bfloat162 o = *reinterpret_cast<const __nv_bfloat162*>(out + at);
+    const __nv_bfloat162 g = *reinterpret_cast<const __nv_bfloat162*>(dout + at);
+    acc = fmaf(__low2float(o), __low2float(g), acc);
+    acc = fmaf(__high2float(o), __high2float(g), acc);
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
+  if (lane == 0) dst[row] = make_float2(lse[row] * 1.4426950408889634f, acc);
+}
+
+// ------------------------------------------------------------------ dQ, query-major
+//
+// CTA = one 128-row tile, as in the forward; key tiles are single blocks. Per block:
+// S = Q K^T and dP = dO V^T into TMEM, one thread per row forms dS and writes it over S as
+// bf16, dQ += dS K. 256 TMEM columns and 113 KB: two CTAs per SM.
+template <int D>
+struct SpDqCfg {
+  static constexpr int BM = 128;
+  static constexpr int QBYTES = BM * D * 2;
+  static constexpr int SLOT = 64 * D * 2;
+  static constexpr int NK = 2;                      // K slots
+  static constexpr int NV = D == 128 ? 1 : 2;       // V slots
+  static constexpr int OFF_DO = QBYTES;
+  static constexpr int OFF_K = 2 * QBYTES;
+  static constexpr int OFF_V = OFF_K + NK * SLOT;
+  static constexpr int OFF_BAR = OFF_V + NV * SLOT;
+  static constexpr int SMEM = OFF_BAR + 1024;
+  static constexpr int TM_S = 0, TM_DP = 64, TM_DQ = 128, TM_COLS = 256;
+  static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
+};
+
+struct SpBlockInfo {
+  int c;  // block, -1 = end
+  uint32_t w[4];
+};
+
+struct SpDqBars {
+  uint64_t q_full;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t info_full[4];
+  uint64_t s_full, ds_full, dq_full;
+  uint32_t tmem_base;
+  int abort_flag;
+  SpBlockInfo info[4];
+};
+static_assert(sizeof(SpDqBars) <= 1024, "barrier block");
+
+template <int D>
+__global__ void __launch_bounds__(kSpThreads, 2)
+streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
+                          const __grid_constant__ CUtensorMap map_do,
+                          const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_v, const SparseArgs a,
+                          const uint32_t idesc_s, const uint32_t idesc_dp,
+                          const uint32_t idesc_dq) {
+  using C = SpDqCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_skl_error, 4u);
+    return;
+  }
+  SpDqBars* bars = reinterpret_cast<SpDqBars*>(smem + C::OFF_BAR);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bp = blockIdx.x / a.n_tiles;
+  const SpTile t = sp_tile(a, bp, a.n_tiles - 1 - blockIdx.x % a.n_tiles);
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bars->q_full), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&bars->k_full[s]), 1);
+      mbar_init(smem_u32(&bars->k_empty[s]), 1);
+      mbar_init(smem_u32(&bars->v_full[s]), 1);
+      mbar_init(smem_u32(&bars->v_empty[s]), 1);
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
+    mbar_init(smem_u32(&bars->s_full), 1);
+    mbar_init(smem_u32(&bars->ds_full), 4);
+    mbar_init(smem_u32(&bars->dq_full), 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp < 4) {
+    const int r = warp * 32 + lane;
+    const int g = r / a.Qn, qi = r - g * a.Qn, i = t.q0 + qi;
+    const bool valid = g < a.G && i < a.N_Q;
+    const int last = valid ? sp_last(i, t.nk, a.N_Q, a.causal) : -1;
+    const int wi = qi >> 5, bi = a.Qn >= 32 ? (qi & 31) : t.bit0 + qi;
+    const size_t row = (size_t)(t.h0 + g) * a.N_Q + i;
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t ts = tmem + lane_off + C::TM_S, tp = tmem + lane_off + C::TM_DP;
+    const uint32_t tq = tmem + lane_off + C::TM_DQ;
+    const float2 rv = valid ? __ldg(a.rows + row) : make_float2(0.f, 0.f);
+    const float nl = -rv.x, nd = -rv.y, c = a.c;
+    bool ok = true;
+    int n = 0;
+    for (;; ++n) {
+      if (!mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1)) { ok = false; break; }
+      const SpBlockInfo& f = bars->info[n & 3];
+      if (f.c < 0) break;
+      const bool on = (f.w[wi & 3] >> bi) & 1u;
+      const int lim = on ? last - f.c * kSpBlock : -1;
+      const int tail = t.nk & (kSpBlock - 1);
+      const bool at_end = tail != 0 && t.nk < a.N_K && f.c == t.nk / kSpBlock;
+      if (!mbar_wait(smem_u32(&bars->s_full), n & 1)) { ok = false; break; }
+      tc_fence_after();
+      if (at_end) {  // S is complete: K may lose its rows past nk before dQ += dS K
+        uint8_t* kb = smem + C::OFF_K + (n % C::NK) * C::SLOT;
+        const int per = (kSpBlock - tail) * 8;
+        for (int e = threadIdx.x; e < per * (D / 64); e += 128)
+          *reinterpret_cast<uint4*>(kb + (e / per) * (64 * 128) + tail * 128 + (e % per) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        fence_async_smem();
+      }
+      uint32_t p[32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[64];  // 32 scores, 32 dP
+        tmem_ld_2x32_wait(ts + 32 * h, tp + 32 * h, v);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float d0 = ex2_approx(fmaf(__uint_as_float(v[k]), c, nl)) * (__uint_as_float(v[32 + k]) + nd);
+          float d1 = ex2_approx(fmaf(__uint_as_float(v[k + 1]), c, nl)) *
+                     (__uint_as_float(v[33 + k]) + nd);
+          d0 = 32 * h + k <= lim ? d0 : 0.f;
+          d1 = 32 * h + k + 1 <= lim ? d1 : 0.f;
+          p[16 * h + (k >> 1)] = pack_bf16x2(d0, d1);
+        }
+      }
+      tmem_st_32(ts, p);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
+    }
+    if (ok && !mbar_wait(smem_u32(&bars->dq_full), 0)) ok = false;
+    if (!ok) {
+      atomicOr(&g_skl_error, 2u);
+      *abort_flag = 1;
+    }
+    tc_fence_after();
+    if (ok) {
+#pragma unroll
+      for (int k = 0; k < D; k += 32) {
+        uint32_t o[32];
+        if (n > 0) tmem_ld_32_wait(tq + k, o);
+        if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>(a.dq + row * D + k);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = n > 0 ? __uint_as_float(o[e + q]) * a.scale : 0.f;
+            dst[e >> 3] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                     pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+          }
+        }
+      }
+    }
+  } else if (warp == 4) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_q);
+      tma_prefetch_desc(&map_do);
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+      const uint32_t qb = smem_u32(&bars->q_full);
+      mbar_arrive_expect_tx(qb, 2 * a.Qn * a.G * D * 2);
+      for (int blk = 0; blk < D / 64; ++blk) {
+        tma_load_3d(sb + blk * (C::BM * 128), &map_q, qb, blk * 64, t.q0, t.h0,
+                    l2_policy_evict_first());
+        tma_load_3d(sb + C::OFF_DO + blk * (C::BM * 128), &map_do, qb, blk * 64, t.q0, t.h0,
+                    l2_policy_evict_first());
+      }
+    }
+    const uint64_t keep = l2_policy_evict_last();
+    int n = 0;
+    auto push = [&](int c, const uint32_t (&u)[4]) -> bool {
+      bool fine = true;
+      if (lane == 0) {
+        SpBlockInfo& f = bars->info[n & 3];
+        f.c = c;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f.w[k] = u[k];
+        mbar_arrive(smem_u32(&bars->info_full[n & 3]));
+        if (c >= 0) {
+          const int ks = n % C::NK, vs = n % C::NV;
+          const uint32_t kf = smem_u32(&bars->k_full[ks]), vf = smem_u32(&bars->v_full[vs]);
+          fine = mbar_wait(smem_u32(&bars->k_empty[ks]), ((n / C::NK) & 1) ^ 1);
+          if (fine) {
+            mbar_arrive_expect_tx(kf, C::SLOT);
+            for (int blk = 0; blk < D / 64; ++blk)
+              tma_load_3d(sb + C::OFF_K + ks * C::SLOT + blk * (64 * 128), &map_k, kf, blk * 64,
+                          c * kSpBlock, t.kv, keep);
+            fine = mbar_wait(smem_u32(&bars->v_empty[vs]), ((n / C::NV) & 1) ^ 1);
+          }
+          if (fine) {
+            mbar_arrive_expect_tx(vf, C::SLOT);
+            for (int blk = 0; blk < D / 64; ++blk)
+              tma_load_3d(sb + C::OFF_V + vs * C::SLOT + blk * (64 * 128), &map_v, vf, blk * 64,
+                          c * kSpBlock, t.kv, keep);
+          }
+        }
+      }
+      fine = __shfl_sync(0xffffffffu, fine ? 1 : 0, 0) != 0;
+      if (c >= 0) ++n;
+      return fine;
+    };
+    bool ok = sp_scan(a, t, lane, push);
+    const uint32_t none[4] = {0u, 0u, 0u, 0u};
+    if (ok) ok = push(-1, none);
+    if (!ok && lane == 0) {
+      atomicOr(&g_skl_error, 2u);
+      *abort_flag = 1;
+      mbar_wait(smem_u32(&bars->q_full), 0);
+      for (int j = max(0, n - C::NK); j < n; ++j)
+        mbar_wait(smem_u32(&bars->k_full[j % C::NK]), (j / C::NK) & 1);
+      for (int j = max(0, n - C::NV); j < n; ++j)
+        mbar_wait(smem_u32(&bars->v_full[j % C::NV]), (j / C::NV) & 1);
+    }
+    if (lane == 0 && n == 0) mbar_wait(smem_u32(&bars->q_full), 0);
+  } else if (elect_one()) {
+    bool ok = mbar_wait(smem_u32(&bars->q_full), 0);
+    for (int n = 0; ok; ++n) {
+      if (!(ok = mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1))) break;
+      if (bars->info[n & 3].c < 0) break;
+      const int ks = n % C::NK, vs = n % C::NV;
+      const uint32_t sk = sb + C::OFF_K + ks * C::SLOT, sv = sb + C::OFF_V + vs * C::SLOT;
+      if (!(ok = mbar_wait(smem_u32(&bars->k_full[ks]), (n / C::NK) & 1))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t qa = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+        const uint32_t ka = (kk >> 2) * (64 * 128) + (kk & 3) * 32;
+        umma_bf16_ss(tmem + C::TM_S, sdesc_sw128(sb + qa, 16, 1024), sdesc_sw128(sk + ka, 16, 1024),
+                     idesc_s, kk > 0);
+      }
+      if (!(ok = mbar_wait(smem_u32(&bars->v_full[vs]), (n / C::NV) & 1))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t qa = C::OFF_DO + (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+        const uint32_t ka = (kk >> 2) * (64 * 128) + (kk & 3) * 32;
+        umma_bf16_ss(tmem + C::TM_DP, sdesc_sw128(sb + qa, 16, 1024),
+                     sdesc_sw128(sv + ka, 16, 1024), idesc_dp, kk > 0);
+      }
+      umma_commit(smem_u32(&bars->v_empty[vs]));
+      umma_commit(smem_u32(&bars->s_full));
+      if (!(ok = mbar_wait(smem_u32(&bars->ds_full), n & 1))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        umma_bf16_ts(tmem + C::TM_DQ, tmem + C::TM_S + kk * 8,
+                     sdesc_sw128(sk + kk * 2048, 64 * 128, 1024), idesc_dq,
+                     (n > 0 || kk > 0) ? 1u : 0u);
+      umma_commit(smem_u32(&bars->k_empty[ks]));
+    }
+    umma_commit(smem_u32(&bars->dq_full));
+    if (!ok) {
+      atomicOr(&g_skl_error, 2u);
+      *abort_flag = 1;
+    }
+    mbar_wait(smem_u32(&bars->dq_full), 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------ dK, dV, key-major
+//
+// CTA = one block of 64 keys of one K head; it walks the tiles (of every pack that reads this
+// K head) whose word column lists the block. Per tile: S = Q K^T and dP = dO V^T (rows on the
+// lanes, 64 key columns), one thread per row writes P and dS as bf16 into shared memory, then
+//   dV^T += dO^T P  and  dK^T += Q^T dS   (d on the lanes, keys on the columns).
+// For d = 64 both products take the stacked operand [dO | Q] (128 lanes) and keep the half
+// they need: an M of 64 would run at the same speed.
+// Warps: 0-3 tiles of even steps, 4-7 of odd steps, 8 producer, 9 MMA + TMEM.
+constexpr int kSpDkvThreads = 320;
+
+template <int D>
+struct SpDkvCfg {
+  static constexpr int SLOT = 64 * D * 2;
+  static constexpr int QBYTES = 128 * D * 2;
+  static constexpr int STAGE = 2 * QBYTES;          // {dO, Q}
+  static constexpr int PT = 128 * 128;              // bf16 [128 rows][64 keys]
+  static constexpr int OFF_V = SLOT;                // K first
+  static constexpr int OFF_Q = 2 * SLOT;            // two stages
+  static constexpr int OFF_P = OFF_Q + 2 * STAGE;   // two buffers {P, dS}
+  static constexpr int OFF_BAR = OFF_P + 4 * PT;
+  static constexpr int SMEM = OFF_BAR + 1024;
+  static constexpr int TM_S = 0;                    // buffer b: S at 128 b, dP at 128 b + 64
+  static constexpr int TM_DV = 256, TM_DK = 320, TM_COLS = 512;
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+struct SpTileInfo {
+  int tile;  // tile of pack p, -1 = end
+  int p;
+  uint32_t w[4];
+};
+
+struct SpDkvBars {
+  uint64_t k_full;
+  uint64_t q_full[2], q_empty[2];
+  uint64_t info_full[4];
+  uint64_t s_full[2], s_free[2], ds_full[2], ds_empty[2];
+  uint64_t acc_full;
+  uint32_t tmem_base;
+  int abort_flag;
+  SpTileInfo info[4];
+};
+static_assert(sizeof(SpDkvBars) <= 1024, "barrier block");
+
+template <int D>
+__global__ void __launch_bounds__(kSpDkvThreads, 1)
+streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
+                           const __grid_constant__ CUtensorMap map_do,
+                           const __grid_constant__ CUtensorMap map_k,
+                           const __grid_constant__ CUtensorMap map_v, const SparseArgs a,
+                           const uint32_t idesc_s, const uint32_t idesc_dp,
+                           const uint32_t idesc_acc) {
+  using C = SpDkvCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_skl_error, 4u);
+    return;
+  }
+  SpDkvBars* bars = reinterpret_cast<SpDkvBars*>(smem + C::OFF_BAR);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Block 0 of every head first: causal maps list the early blocks most.
+  const int kv = blockIdx.x % (a.B * a.Hkv), blk0 = blockIdx.x / (a.B * a.Hkv);
+  const int b = kv / a.Hkv;
+  const int nk = sp_len(a.lens, b, a.N_K);
+  const int ppk = a.P / a.Hkv;               // packs that read this K head
+  const int p0 = (kv - b * a.Hkv) * ppk;
+  const int rows = a.Qn * a.G;               // rows of a tile that TMA writes
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bars->k_full), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&bars->q_full[s]), 1);
+      mbar_init(smem_u32(&bars->q_empty[s]), 1);
+      mbar_init(smem_u32(&bars->s_full[s]), 1);
+      mbar_init(smem_u32(&bars->s_free[s]), 4);
+      mbar_init(smem_u32(&bars->ds_full[s]), 4);
+      mbar_init(smem_u32(&bars->ds_empty[s]), 1);
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
+    mbar_init(smem_u32(&bars->acc_full), 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
+    tmem_relinquish();
+  }
+  // Rows of the Q and dO buffers that no copy writes enter the row sums of dV and dK with a
+  // factor of 0 and must be finite: zero them once.
+  if (rows < 128) {
+    const int per = (128 - rows) * 8;
+    for (int e = threadIdx.x; e < per * 4 * (D / 64); e += kSpDkvThreads)
+      *reinterpret_cast<uint4*>(smem + C::OFF_Q + (e / per) * (128 * 128) + rows * 128 +
+                                (e % per) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp < 8) {
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const int g = r / a.Qn, qi = r - g * a.Qn;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t ts = tmem + lane_off + C::TM_S + 128 * wg;
+    const uint32_t prow = sb + C::OFF_P + wg * 2 * C::PT + r * 128;
+    const float c = a.c;
+    bool ok = true;
+    int n = 0;
+    for (;; ++n) {
+      if (!mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1)) { ok = false; break; }
+      const SpTileInfo& f = bars->info[n & 3];
+      if (f.tile < 0) break;
+      if ((n & 1) != wg) continue;
+      const int i = f.tile * a.Qn + qi;
+      const bool valid = g < a.G && i < a.N_Q;
+      const int bit = a.Qn >= 32 ? (qi & 31) : ((f.tile * a.Qn) & 31) + qi;
+      const bool on = valid && ((f.w[(qi >> 5) & 3] >> bit) & 1u);
+      const int lim = on ? sp_last(i, nk, a.N_Q, a.causal) - blk0 * kSpBlock : -1;
+      const float2 rv =
+          on ? __ldg(a.rows + (size_t)(b * a.H + f.p * a.G + g) * a.N_Q + i) : make_float2(0.f, 0.f);
+      const float nl = -rv.x, nd = -rv.y;
+      const uint32_t ph = (n >> 1) & 1;
+      if (!mbar_wait(smem_u32(&bars->s_full[wg]), ph)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t p[32], d[32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[64];
+        tmem_ld_2x32_wait(ts + 32 * h, ts + 64 + 32 * h, v);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float e0 = ex2_approx(fmaf(__uint_as_float(v[k]), c, nl));
+          float e1 = ex2_approx(fmaf(__uint_as_float(v[k + 1]), c, nl));
+          float d0 = e0 * (__uint_as_float(v[32 + k]) + nd);
+          float d1 = e1 * (__uint_as_float(v[33 + k]) + nd);
+          const bool k0 = 32 * h + k <= lim, k1 = 32 * h + k + 1 <= lim;
+          p[16 * h + (k >> 1)] = pack_bf16x2(k0 ? e0 : 0.f, k1 ? e1 : 0.f);
+          d[16 * h + (k >> 1)] = pack_bf16x2(k0 ? d0 : 0.f, k1 ? d1 : 0.f);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[wg]));
+      if (!mbar_wait(smem_u32(&bars->ds_empty[wg]), ph ^ 1)) { ok = false; break; }
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) {
+        const uint32_t at = prow + ((ch ^ (r & 7)) << 4);
+        st_shared_v4(at, p[4 * ch], p[4 * ch + 1], p[4 * ch + 2], p[4 * ch + 3]);
+        st_shared_v4(at + C::PT, d[4 * ch], d[4 * ch + 1], d[4 * ch + 2], d[4 * ch + 3]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[wg]));
+    }
+    if (ok && !mbar_wait(smem_u32(&bars->acc_full), 0)) ok = false;
+    if (!ok) {
+      atomicOr(&g_skl_error, 2u);
+      *abort_flag = 1;
+    }
+    tc_fence_after();
+    // Warps 0-3 write dV, warps 4-7 dK: lane = d, columns = keys. For d = 64 dV is on lanes
+    // 0-63 and dK on lanes 64-127 of the stacked products.
+    const int col = D == 128 ? r : (wg == 0 ? r : r - 64);
+    const bool mine = D == 128 || (wg == 0 ? quarter < 2 : quarter >= 2);
+    if (ok && mine) {
+      const float f = wg == 0 ? 1.f : a.scale;
+      __nv_bfloat16* dst = wg == 0 ? a.dv : a.dk;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[32];
+        if (n > 0) tmem_ld_32_wait(tmem + lane_off + (wg == 0 ? C::TM_DV : C::TM_DK) + 32 * h, v);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int key = blk0 * kSpBlock + 32 * h + k;
+          if (key < a.N_K)
+            dst[((size_t)kv * a.N_K + key) * D + col] =
+                __float2bfloat16_rn(n > 0 ? __uint_as_float(v[k]) * f : 0.f);
+        }
+      }
+    }
+  } else if (warp == 8) {
+    const uint64_t keep = l2_policy_evict_last();
+    if (lane == 0) {
+      tma_prefetch_desc(&map_q);
+      tma_prefetch_desc(&map_do);
+      const uint32_t kf = smem_u32(&bars->k_full);
+      mbar_arrive_expect_tx(kf, 2 * C::SLOT);
+      for (int blk = 0; blk < D / 64; ++blk) {
+        tma_load_3d(sb + blk * (64 * 128), &map_k, kf, blk * 64, blk0 * kSpBlock, kv, keep);
+        tma_load_3d(sb + C::OFF_V + blk * (64 * 128), &map_v, kf, blk * 64, blk0 * kSpBlock, kv,
+                    keep);
+      }
+    }
+    int n = 0;
+    auto push = [&](int tile, int p, const uint32_t (&u)[4]) -> bool {
+      bool fine = true;
+      if (lane == 0) {
+        // Entry n & 3 was last read for step n - 4, whose P and dS were written before the
+        // products that freed step n - 2's stage (awaited below before step n - 1 was loaded).
+        SpTileInfo& f = bars->info[n & 3];
+        f.tile = tile;
+        f.p = p;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f.w[k] = u[k];
+        mbar_arrive(smem_u32(&bars->info_full[n & 3]));
+        if (tile >= 0) {
+          const int st = n & 1;
+          fine = mbar_wait(smem_u32(&bars->q_empty[st]), ((n >> 1) & 1) ^ 1);
+          if (fine) {
+            const uint32_t qf = smem_u32(&bars->q_full[st]);
+            const uint32_t base = sb + C::OFF_Q + st * C::STAGE;
+            mbar_arrive_expect_tx(qf, 2 * rows * D * 2);
+            for (int blk = 0; blk < D / 64; ++blk) {
+              tma_load_3d(base + blk * (128 * 128), &map_do, qf, blk * 64, tile * a.Qn,
+                          b * a.H + p * a.G, keep);
+              tma_load_3d(base + C::QBYTES + blk * (128 * 128), &map_q, qf, blk * 64,
+                          tile * a.Qn, b * a.H + p * a.G, keep);
+            }
+          }
+        }
+      }
+      fine = __shfl_sync(0xffffffffu, fine ? 1 : 0, 0) != 0;
+      if (tile >= 0) ++n;
+      return fine;
+    };
+    const int iws = (a.N_Q + 31) >> 5;
+    bool ok = true;
+    for (int p = p0; ok && p < p0 + ppk; ++p) {
+      const uint32_t* col =
+          a.mask + (size_t)(b * a.Hsel + p / (a.P / a.Hsel)) * iws * a.NB + blk0;
+      for (int base = 0; ok && base < a.n_tiles; base += 32) {
+        const int tile = base + lane, q0 = tile * a.Qn, iw = q0 >> 5;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (tile < a.n_tiles) {
+          const uint32_t tmask = a.Qn >= 32 ? 0xffffffffu : ((1u << a.Qn) - 1u) << (q0 & 31);
+          const int nw = a.Qn <= 32 ? 1 : min(a.Qn >> 5, iws - iw);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < nw) w[k] = __ldg(col + (size_t)(iw + k) * a.NB) & tmask;
+        }
+        uint32_t nz = __ballot_sync(0xffffffffu, (w[0] | w[1] | w[2] | w[3]) != 0u);
+        while (ok && nz) {
+          const int pos = __ffs(nz) - 1;
+          nz &= nz - 1;
+          uint32_t u[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) u[k] = __shfl_sync(0xffffffffu, w[k], pos);
+          ok = push(base + pos, p, u);
+        }
+      }
+    }
+    const uint32_t none[4] = {0u, 0u, 0u, 0u};
+    if (ok) ok = push(-1, 0, none);
+    if (lane == 0) mbar_wait(smem_u32(&bars->k_full), 0);
+    if (!ok && lane == 0) {
+      atomicOr(&g_skl_error, 2u);
+      *abort_flag = 1;
+      for (int j = max(0, n - 2); j < n; ++j)
+        mbar_wait(smem_u32(&bars->q_full[j & 1]), (j >> 1) & 1);
+    }
+  } else if (elect_one()) {
+    bool ok = mbar_wait(smem_u32(&bars->k_full), 0);
+    // Scores of step n, when there is one: 1, none left: 0, a wait ran out: -1.
+    auto scores = [&](int n) -> int {
+      if (!mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1)) return -1;
+      if (bars->info[n & 3].tile < 0) return 0;
+      const int st = n & 1;
+      const uint32_t ph = (n >> 1) & 1;
+      if (!mbar_wait(smem_u32(&bars->q_full[st]), ph)) return -1;
+      if (!mbar_wait(smem_u32(&bars->s_free[st]), ph ^ 1)) return -1;
+      tc_fence_after();
+      const uint32_t sdo = sb + C::OFF_Q + st * C::STAGE, sq = sdo + C::QBYTES;
+      const uint32_t ds = tmem + C::TM_S + 128 * st;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t qa = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+        const uint32_t ka = (kk >> 2) * (64 * 128) + (kk & 3) * 32;
+        umma_bf16_ss(ds, sdesc_sw128(sq + qa, 16, 1024), sdesc_sw128(sb + ka, 16, 1024), idesc_s,
+                     kk > 0);
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t qa = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+        const uint32_t ka = C::OFF_V + (kk >> 2) * (64 * 128) + (kk & 3) * 32;
+        umma_bf16_ss(ds + 64, sdesc_sw128(sdo + qa, 16, 1024), sdesc_sw128(sb + ka, 16, 1024),
+                     idesc_dp, kk > 0);
+      }
+      umma_commit(smem_u32(&bars->s_full[st]));
+      return 1;
+    };
+    int more = ok ? scores(0) : 0;
+    for (int n = 0; more > 0; ++n) {
+      more = scores(n + 1);
+      if (more < 0) break;
+      const int st = n & 1;
+      if (!mbar_wait(smem_u32(&bars->ds_full[st]), (n >> 1) & 1)) { more = -1; break; }
+      tc_fence_after();
+      const uint32_t sdo = sb + C::OFF_Q + st * C::STAGE;
+      const uint32_t sq = D == 128 ? sdo + C::QBYTES : sdo;  // d = 64: stacked [dO | Q]
+      const uint32_t sp = sb + C::OFF_P + st * 2 * C::PT;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)  // 16 rows a step; A and B are both row-contracted
+        umma_bf16_ss(tmem + C::TM_DV, sdesc_sw128(sdo + kk * 2048, 128 * 128, 1024),
+                     sdesc_sw128(sp + kk * 2048, 128 * 128, 1024), idesc_acc,
+                     (n > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        umma_bf16_ss(tmem + C::TM_DK, sdesc_sw128(sq + kk * 2048, 128 * 128, 1024),
+                     sdesc_sw128(sp + C::PT + kk * 2048, 128 * 128, 1024), idesc_acc,
+                     (n > 0 || kk > 0) ? 1u : 0u);
+      umma_commit(smem_u32(&bars->q_empty[st]));
+      umma_commit(smem_u32(&bars->ds_empty[st]));
+    }
+    if (more < 0) ok = false;
+    umma_commit(smem_u32(&bars->acc_full));
+    if (!ok) {
+      atomicOr(&g_skl_error, 2u);
+      *abort_flag = 1;
+    }
+    mbar_wait(smem_u32(&bars->acc_full), 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+}  // namespace skl

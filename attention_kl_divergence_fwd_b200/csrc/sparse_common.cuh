@@ -1,0 +1,119 @@
+// sparse_common.cuh - shared pieces of the block-sparse attention kernels: problem view,
+// packing of grouped query heads into 128-row tiles, the selection bit matrix.
+//
+// Keys are cut into blocks of 64. Every query of every selection head lists the blocks it
+// reads. The tensor core works on tiles of 128 rows, so rows that share a K head and a
+// selection are packed: a tile holds Qn queries (a power of two) of the G query heads of
+// one pack, row r = g * Qn + (query - q0). A tile reads the union of its queries' blocks and
+// each row drops the blocks that its own query did not list. For neighbouring queries, whose
+// lists largely agree, the union is little longer than one list; a gather per query instead
+// would move every block through L2 once per query (at 16384 tokens, 8 K heads and 16 blocks
+// of 64 x 256 bf16 that is 69 GB), and for unrelated lists the union ends at dense attention.
+//
+// The lists become a bit matrix first: word (iw, c) of a selection head holds, for queries
+// 32 iw .. 32 iw + 31, whether each reads block c. It turns lists in any order, with repeated
+// or negative entries, into sets; a tile scans its row of words (consecutive c), the
+// key-major backward scans a column.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace skl {
+
+constexpr int kSpBlock = 64;  // keys per block
+
+struct SparseArgs {
+  int B, H, N_Q, N_K, NB;  // NB = ceil(N_K / 64)
+  int P, G;                // packs of query heads per batch entry, heads per pack (H = P * G)
+  int Hkv, Hsel;           // K heads, selection heads (both divide P)
+  int Qn, n_tiles;         // queries per 128-row tile, tiles per pack
+  int causal, topk;
+  int splits;              // CTAs that share one tile's list (forward)
+  int direct;              // forward of one query: blocks straight from the list
+  float c, scale;          // |scale| * log2(e); signed scale
+  const int* idx;          // [B, Hsel, N_Q, topk]
+  const int* lens;         // [B] keys of each sequence, or null (N_K)
+  const uint32_t* mask;    // [B * Hsel, ceil(N_Q / 32), NB]
+  float2* rows;            // backward: {LSE * log2(e), sum_d out * dout} per row
+  __nv_bfloat16* out;      // forward
+  float* lse;
+  float* part_o;           // splits > 1: [splits, rows, d] normalised partial outputs
+  float* part_l;           //             [splits, rows] base-2 log-sum-exps
+  __nv_bfloat16* dq;       // backward
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+};
+
+// Keys of sequence b. A length outside 0 .. N_K is recorded and read as an empty sequence.
+__device__ __forceinline__ int sp_len(const int* lens, int b, int N_K) {
+  if (lens == nullptr) return N_K;
+  const int n = __ldg(lens + b);
+  if (n < 0 || n > N_K) {
+    if (threadIdx.x == 0) atomicOr(&g_skl_error, kErrBadOffsets);
+    return 0;
+  }
+  return n;
+}
+
+// Last key index that query i may read (bottom-right causal alignment), -1 for none.
+__device__ __forceinline__ int sp_last(int i, int nk, int N_Q, int causal) {
+  return causal ? max(-1, min(nk - 1, i + nk - N_Q)) : nk - 1;
+}
+
+// A tile of one pack: sequence, K head, selection head, first query and first row.
+struct SpTile {
+  int b, p, q0, nk;
+  int kv;        // head coordinate of K and V in the tensor maps
+  int h0;        // head coordinate of the pack's first query head
+  const uint32_t* words;  // row of the bit matrix that holds query q0
+  int bit0;      // bit of query q0 within its word (0 unless Qn < 32)
+  int nwords;    // words that cover the tile's queries (1, 2 or 4)
+};
+
+__device__ __forceinline__ SpTile sp_tile(const SparseArgs& a, int bp, int tile) {
+  SpTile t;
+  t.b = bp / a.P;
+  t.p = bp - t.b * a.P;
+  t.q0 = tile * a.Qn;
+  t.nk = sp_len(a.lens, t.b, a.N_K);
+  t.kv = t.b * a.Hkv + t.p / (a.P / a.Hkv);
+  t.h0 = t.b * a.H + t.p * a.G;
+  const int sel = t.b * a.Hsel + t.p / (a.P / a.Hsel);
+  const int iws = (a.N_Q + 31) >> 5;
+  t.words = a.mask + ((size_t)sel * iws + (t.q0 >> 5)) * a.NB;
+  t.bit0 = t.q0 & 31;
+  t.nwords = a.Qn <= 32 ? 1 : min(a.Qn >> 5, iws - (t.q0 >> 5));
+  return t;
+}
+
+// Builds the bit matrix: one CTA per 32 queries of a selection head. Entries that are
+// negative, beyond the last block, or of a block the query may not see set no bit.
+constexpr int kMaskChunk = 8192;  // blocks per pass (32 KB of shared memory)
+__global__ void __launch_bounds__(128)
+streamkl_sparse_mask_kernel(const SparseArgs a, uint32_t* mask) {
+  __shared__ uint32_t sm[kMaskChunk];
+  const int iws = (a.N_Q + 31) >> 5;
+  const int sel = blockIdx.x / iws, iw = blockIdx.x - sel * iws, b = sel / a.Hsel, i0 = iw * 32;
+  const int nk = sp_len(a.lens, b, a.N_K);
+  const int nq = min(32, a.N_Q - i0);
+  const int* idx = a.idx + ((size_t)sel * a.N_Q + i0) * a.topk;
+  uint32_t* dst = mask + ((size_t)sel * iws + iw) * a.NB;
+  for (int c0 = 0; c0 < a.NB; c0 += kMaskChunk) {
+    const int n = min(kMaskChunk, a.NB - c0);
+    for (int c = threadIdx.x; c < n; c += blockDim.x) sm[c] = 0u;
+    __syncthreads();
+    const int total = nq * a.topk;  // at most 32 * topk, topk < 2^24
+    for (int e = threadIdx.x; e < total; e += blockDim.x) {
+      const int c = __ldg(idx + e), q = e / a.topk;
+      const int last = sp_last(i0 + q, nk, a.N_Q, a.causal);
+      // c <= last / 64 keeps c * 64 from being formed for wild entries
+      if (last >= 0 && c >= 0 && c <= last / kSpBlock && c >= c0 && c - c0 < n)
+        atomicOr(&sm[c - c0], 1u << q);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < n; c += blockDim.x) dst[c0 + c] = sm[c];
+    __syncthreads();
+  }
+}
+
+}  // namespace skl

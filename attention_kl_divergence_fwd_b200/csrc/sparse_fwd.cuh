@@ -1,0 +1,490 @@
+// sparse_fwd.cuh - attention over selected key blocks, forward (tcgen05 + TMEM + TMA).
+//
+//   out[i] = sum_j p_ij v_j,  p_ij = exp(s_ij - LSE_i),  s_ij = scale <q_i, k_j>,
+//   LSE_i = log sum_j exp(s_ij),  j over the allowed keys of the blocks that i lists.
+//
+// CTA = one 128-row tile of packed query heads (sparse_common.cuh). Key tiles are pairs of
+// listed blocks (128 keys, gathered into one buffer by two TMA boxes). Per key tile:
+//   S = Q K^T into TMEM; one thread per row turns its 128 scores into probabilities against
+//   a running reference m (raised, with a rescale of O in TMEM, only when a score exceeds it
+//   by 2^8, so that most tiles leave O alone) and writes them back over the scores as bf16;
+//   O += P V with P read from TMEM.
+// P is rounded to bf16 for the tensor core (relative error at most 2^-8 each, the same as the
+// output's own rounding); the row sums, references and O stay in fp32.
+// A CTA keeps one score buffer: 256 TMEM columns and 97 KB of shared memory, so two CTAs share
+// an SM and one's MMAs run under the other's exponentials.
+// `splits` > 1: the tile's list is dealt to that many CTAs by rank, each writes a normalised
+// partial output and its log-sum-exp, and the merge kernel joins them.
+//
+// Warps: 0-3 softmax (row = TMEM lane), 4 producer (scans the bit matrix, TMA), 5 MMA + TMEM.
+#pragma once
+
+#include "sparse_common.cuh"
+
+namespace skl {
+
+constexpr int kSpThreads = 192;
+
+// One key tile as the producer announces it: how many blocks (0 = end), which, and which of
+// the tile's queries list them.
+struct SpInfo {
+  int nb;
+  int c[2];
+  uint32_t w[2][4];
+};
+
+template <int D>
+struct SpFwdCfg {
+  static constexpr int BM = 128;
+  static constexpr int QBYTES = BM * D * 2;
+  static constexpr int KVBYTES = 128 * D * 2;         // one pair of K (or V) blocks
+  static constexpr int NST = D == 128 ? 1 : 2;        // pair buffers each of K and V
+  static constexpr int OFF_K = QBYTES;
+  static constexpr int OFF_V = OFF_K + NST * KVBYTES;
+  static constexpr int OFF_BAR = OFF_V + NST * KVBYTES;
+  static constexpr int SMEM = OFF_BAR + 1024;
+  static constexpr int TM_S = 0;    // 128 columns of scores, P over the first 64
+  static constexpr int TM_O = 128;  // D columns
+  static constexpr int TM_COLS = 256;
+  static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
+};
+
+struct SpFwdBars {
+  uint64_t q_full;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t info_full[4];
+  uint64_t s_full, p_full, o_full;
+  uint32_t tmem_base;
+  int abort_flag;
+  SpInfo info[4];
+};
+static_assert(sizeof(SpFwdBars) <= 1024, "barrier block");
+
+// Sets the rows past nk of a [D/64][128][64] pair buffer's half to zero: with a padded cache
+// they hold whatever the cache held, and 0 * NaN would reach the products.
+template <int D>
+__device__ __forceinline__ void sp_zero_tail(uint8_t* buf, int half, int first, int tid,
+                                             int nthreads) {
+  const int n = (kSpBlock - first) * 8 * (D / 64);  // 16-byte pieces
+  for (int e = tid; e < n; e += nthreads) {
+    const int blk = e / ((kSpBlock - first) * 8), r = e % ((kSpBlock - first) * 8);
+    *reinterpret_cast<uint4*>(buf + blk * (128 * 128) + (half * 64 + first) * 128 + r * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// Producer's walk over the blocks of a tile's union, whole warp: emit(c, w0..w3) for each
+// (w in units of the tile's own bits), in ascending order.
+template <typename Emit>
+__device__ __forceinline__ bool sp_scan(const SparseArgs& a, const SpTile& t, int lane,
+                                        Emit&& emit) {
+  const uint32_t tmask = a.Qn >= 32 ? 0xffffffffu : ((1u << a.Qn) - 1u) << t.bit0;
+  for (int base = 0; base < a.NB; base += 32) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (base + lane < a.NB) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < t.nwords) w[k] = __ldg(t.words + (size_t)k * a.NB + base + lane) & tmask;
+    }
+    uint32_t nz = __ballot_sync(0xffffffffu, (w[0] | w[1] | w[2] | w[3]) != 0u);
+    while (nz) {
+      const int pos = __ffs(nz) - 1;
+      nz &= nz - 1;
+      uint32_t u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = __shfl_sync(0xffffffffu, w[k], pos);
+      if (!emit(base + pos, u)) return false;
+    }
+  }
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kSpThreads, 2)
+streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
+                           const __grid_constant__ CUtensorMap map_k,
+                           const __grid_constant__ CUtensorMap map_v, const SparseArgs a,
+                           const uint32_t idesc_s2, const uint32_t idesc_s1,
+                           const uint32_t idesc_o) {
+  using C = SpFwdCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_skl_error, 4u);
+    return;
+  }
+  SpFwdBars* bars = reinterpret_cast<SpFwdBars*>(smem + C::OFF_BAR);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // Tiles of one pack are neighbours in the grid (they share K and V in L2), last tile first
+  // (causal: the longest lists).
+  const int split = blockIdx.x % a.splits;
+  const int unit = blockIdx.x / a.splits;
+  const int bp = unit / a.n_tiles;
+  const SpTile t = sp_tile(a, bp, a.n_tiles - 1 - unit % a.n_tiles);
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bars->q_full), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&bars->k_full[s]), 1);
+      mbar_init(smem_u32(&bars->k_empty[s]), 1);
+      mbar_init(smem_u32(&bars->v_full[s]), 1);
+      mbar_init(smem_u32(&bars->v_empty[s]), 1);
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
+    mbar_init(smem_u32(&bars->s_full), 1);
+    mbar_init(smem_u32(&bars->p_full), 4);
+    mbar_init(smem_u32(&bars->o_full), 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------- softmax rows
+    const int r = warp * 32 + lane;
+    const int g = r / a.Qn, qi = r - g * a.Qn, i = t.q0 + qi;
+    const bool valid = g < a.G && i < a.N_Q;
+    const int last = valid ? sp_last(i, t.nk, a.N_Q, a.causal) : -1;
+    const int wi = qi >> 5, bi = a.Qn >= 32 ? (qi & 31) : t.bit0 + qi;
+    const bool warp_live = __any_sync(0xffffffffu, valid);
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t ts = tmem + lane_off + C::TM_S, to = tmem + lane_off + C::TM_O;
+    const float c = a.c;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    int n = 0;
+    for (;; ++n) {
+      if (!mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1)) { ok = false; break; }
+      const SpInfo& f = bars->info[n & 3];
+      const int nb = f.nb;
+      if (nb == 0) break;
+      int lim[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool on = h < nb && ((f.w[h][wi & 3] >> bi) & 1u);
+        lim[h] = on ? last - f.c[h] * kSpBlock : -1;
+      }
+      if (!mbar_wait(smem_u32(&bars->s_full), n & 1)) { ok = false; break; }
+      tc_fence_after();
+      // A padded cache's last block: rows past nk of V must not reach the product. S(n) is
+      // complete, so the products before it are too and v_full is in this tile's phase.
+      const int tail = t.nk & (kSpBlock - 1);
+      bool at_end = false;
+      if (tail != 0 && t.nk < a.N_K) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (h < nb && f.c[h] == t.nk / kSpBlock) {
+            const int st = n % C::NST;
+            if (!mbar_wait(smem_u32(&bars->v_full[st]), (n / C::NST) & 1)) ok = false;
+            sp_zero_tail<D>(smem + C::OFF_V + st * C::KVBYTES, h, tail, threadIdx.x, 128);
+            fence_async_smem();
+            at_end = true;
+          }
+      }
+      if (!ok) break;
+      if (warp_live) {
+        uint32_t v[128];
+        tmem_ld_4x32_wait(ts, ts + 32, ts + 64, ts + 96, v);
+        // Blocks are read whole or not at all except at the causal diagonal and the
+        // sequence's end; only those mask single scores (the end's scores may be NaN).
+        const bool partial = (lim[0] >= 0 && lim[0] < 63) || (lim[1] >= 0 && lim[1] < 63);
+        if (at_end || __any_sync(0xffffffffu, partial)) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if ((k & 63) > lim[k >> 6]) v[k] = 0xff800000u;  // -inf
+        }
+        const float mx0 = fmaxf(max_tree32<false>(v, 0, 31), max_tree32<false>(v, 32, 31));
+        const float mx1 = fmaxf(max_tree32<false>(v, 64, 31), max_tree32<false>(v, 96, 31));
+        const float mx = fmaxf(lim[0] >= 0 ? mx0 : -INFINITY, lim[1] >= 0 ? mx1 : -INFINITY);
+        const float ms = mx == -INFINITY ? -INFINITY : mx * c;
+        const bool raise = ms > m + 8.f || (m == -INFINITY && ms > -INFINITY);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f0 = raise ? ex2_approx(m - ms) : 1.f;  // m = -inf: 0
+          if (raise) m = ms;
+          l *= f0;
+          if (n > 0) {  // S(n) is complete, so O holds every earlier product
+#pragma unroll
+            for (int k = 0; k < D; k += 32) {
+              uint32_t o[32];
+              tmem_ld_32_wait(to + k, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+              tmem_st_32(to + k, o);
+            }
+          }
+        }
+        const float bias = m == -INFINITY ? 0.f : -m;
+        const float b0 = lim[0] >= 0 ? bias : -INFINITY, b1 = lim[1] >= 0 ? bias : -INFINITY;
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (q >= nb) break;  // a single block: the other half holds no scores
+          uint32_t p[32];
+          const float bq = q ? b1 : b0;
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float e0 = ex2_approx(fmaf(__uint_as_float(v[64 * q + 2 * k]), c, bq));
+            const float e1 = ex2_approx(fmaf(__uint_as_float(v[64 * q + 2 * k + 1]), c, bq));
+            const float e2 = ex2_approx(fmaf(__uint_as_float(v[64 * q + 2 * k + 2]), c, bq));
+            const float e3 = ex2_approx(fmaf(__uint_as_float(v[64 * q + 2 * k + 3]), c, bq));
+            s0 += e0;
+            s1 += e1;
+            s2 += e2;
+            s3 += e3;
+            p[k] = pack_bf16x2(e0, e1);
+            p[k + 1] = pack_bf16x2(e2, e3);
+          }
+          tmem_st_32(ts + 32 * q, p);
+        }
+        l += (s0 + s1) + (s2 + s3);
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
+    }
+    if (ok && !mbar_wait(smem_u32(&bars->o_full), 0)) ok = false;
+    if (!ok) {
+      atomicOr(&g_skl_error, 1u);
+      *abort_flag = 1;
+    }
+    tc_fence_after();
+    if (warp_live && ok) {
+      const size_t row = (size_t)(t.h0 + g) * a.N_Q + i;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool some = n > 0;  // else O was never written
+#pragma unroll
+      for (int k = 0; k < D; k += 32) {
+        uint32_t o[32];
+        if (some) tmem_ld_32_wait(to + k, o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          o[e] = some && l > 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+        if (!valid) {
+          // no row to write
+        } else if (a.splits == 1) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + k);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+            w.y = pack_bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+            w.z = pack_bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
+            w.w = pack_bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
+            dst[e >> 3] = w;
+          }
+        } else {
+          const size_t rows = (size_t)a.B * a.H * a.N_Q;
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + (split * rows + row) * D + k);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) dst[e >> 2] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (valid) {
+        const float l2 = l > 0.f ? m + log2f(l) : -INFINITY;
+        if (a.splits == 1)
+          a.lse[row] = l2 * 0.69314718055994530942f;
+        else
+          a.part_l[split * ((size_t)a.B * a.H * a.N_Q) + row] = l2;
+      }
+    }
+  } else if (warp == 4) {
+    // ---------------------------------------------------- producer (whole warp scans)
+    if (lane == 0) {
+      tma_prefetch_desc(&map_q);
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+      const uint32_t qb = smem_u32(&bars->q_full);
+      mbar_arrive_expect_tx(qb, a.Qn * a.G * D * 2);
+      for (int blk = 0; blk < D / 64; ++blk)
+        tma_load_3d(sb + blk * (C::BM * 128), &map_q, qb, blk * 64, t.q0, t.h0,
+                    l2_policy_evict_first());
+    }
+    const uint64_t keep = l2_policy_evict_last();
+    bool ok = true;
+    int n = 0, rank = 0, pend = 0;
+    int pc[2] = {0, 0};
+    uint32_t pw[2][4] = {};
+    // Announces the pending blocks as key tile n and loads them (nb = 0: the end).
+    auto push = [&](int nb) -> bool {
+      bool fine = true;
+      if (lane == 0) {
+        SpInfo& f = bars->info[n & 3];
+        f.nb = nb;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f.c[h] = pc[h];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f.w[h][k] = pw[h][k];
+        }
+        mbar_arrive(smem_u32(&bars->info_full[n & 3]));
+        if (nb > 0) {
+          const int st = n % C::NST;
+          const uint32_t ph = ((n / C::NST) & 1) ^ 1;
+          const uint32_t kf = smem_u32(&bars->k_full[st]), vf = smem_u32(&bars->v_full[st]);
+          fine = mbar_wait(smem_u32(&bars->k_empty[st]), ph);
+          if (fine) {
+            mbar_arrive_expect_tx(kf, nb * 64 * D * 2);
+            for (int h = 0; h < nb; ++h)
+              for (int blk = 0; blk < D / 64; ++blk)
+                tma_load_3d(sb + C::OFF_K + st * C::KVBYTES + blk * (128 * 128) + h * (64 * 128),
+                            &map_k, kf, blk * 64, pc[h] * kSpBlock, t.kv, keep);
+            fine = mbar_wait(smem_u32(&bars->v_empty[st]), ph);
+          }
+          if (fine) {
+            mbar_arrive_expect_tx(vf, nb * 64 * D * 2);
+            for (int h = 0; h < nb; ++h)
+              for (int blk = 0; blk < D / 64; ++blk)
+                tma_load_3d(sb + C::OFF_V + st * C::KVBYTES + blk * (128 * 128) + h * (64 * 128),
+                            &map_v, vf, blk * 64, pc[h] * kSpBlock, t.kv, keep);
+          }
+        }
+      }
+      fine = __shfl_sync(0xffffffffu, fine ? 1 : 0, 0) != 0;
+      ++n;
+      pend = 0;
+      return fine;
+    };
+    auto emit = [&](int c, const uint32_t (&u)[4]) -> bool {
+      if (rank++ % a.splits != split) return true;
+      pc[pend] = c;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pw[pend][k] = u[k];
+      return ++pend < 2 ? true : push(2);
+    };
+    if (a.direct) {
+      // One query: its list as a bitmap over the blocks, in the rows of the Q buffer that
+      // the pack's at most 64 rows leave unused.
+      uint32_t* bits = reinterpret_cast<uint32_t*>(smem + 64 * 128);
+      const int sel = t.b * a.Hsel + t.p / (a.P / a.Hsel);
+      const int* idx = a.idx + (size_t)sel * a.topk;
+      const int lastkey = sp_last(0, t.nk, 1, a.causal);
+      for (int w = lane; w < (a.NB + 31) / 32; w += 32) bits[w] = 0u;
+      __syncwarp();
+      for (int e = lane; e < a.topk; e += 32) {
+        const int c = __ldg(idx + e);
+        if (lastkey >= 0 && c >= 0 && c <= lastkey / kSpBlock) atomicOr(&bits[c >> 5], 1u << (c & 31));
+      }
+      __syncwarp();
+      const uint32_t one[4] = {1u, 0u, 0u, 0u};
+      for (int w0 = 0; ok && w0 < (a.NB + 31) / 32; w0 += 32) {
+        const uint32_t mine = w0 + lane < (a.NB + 31) / 32 ? bits[w0 + lane] : 0u;
+        uint32_t lanes = __ballot_sync(0xffffffffu, mine != 0u);
+        while (ok && lanes) {
+          const int src = __ffs(lanes) - 1;
+          lanes &= lanes - 1;
+          uint32_t w = __shfl_sync(0xffffffffu, mine, src);
+          while (ok && w) {
+            ok = emit((w0 + src) * 32 + __ffs(w) - 1, one);
+            w &= w - 1;
+          }
+        }
+      }
+    } else {
+      ok = sp_scan(a, t, lane, emit);
+    }
+    if (ok && pend) ok = push(1);
+    const int tiles = n;
+    if (ok) ok = push(0);
+    if (!ok && lane == 0) {
+      atomicOr(&g_skl_error, 1u);
+      *abort_flag = 1;
+      // Let the copies in flight land before the CTA can exit (each wait is bounded).
+      mbar_wait(smem_u32(&bars->q_full), 0);
+      for (int j = max(0, tiles - C::NST); j < tiles; ++j) {
+        mbar_wait(smem_u32(&bars->k_full[j % C::NST]), (j / C::NST) & 1);
+        mbar_wait(smem_u32(&bars->v_full[j % C::NST]), (j / C::NST) & 1);
+      }
+    }
+    // With no key tile nothing else waits for the Q copy.
+    if (lane == 0 && tiles == 0) mbar_wait(smem_u32(&bars->q_full), 0);
+  } else if (elect_one()) {
+    // ------------------------------------------------------------------ MMA issuer
+    bool ok = mbar_wait(smem_u32(&bars->q_full), 0);
+    for (int n = 0; ok; ++n) {
+      ok = mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1);
+      if (!ok) break;
+      const int nb = bars->info[n & 3].nb;
+      if (nb == 0) break;
+      const int st = n % C::NST;
+      const uint32_t ph = (n / C::NST) & 1;
+      const uint32_t sk = sb + C::OFF_K + st * C::KVBYTES, sv = sb + C::OFF_V + st * C::KVBYTES;
+      if (!(ok = mbar_wait(smem_u32(&bars->k_full[st]), ph))) break;
+      tc_fence_after();
+      const uint32_t id = nb == 2 ? idesc_s2 : idesc_s1;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+        umma_bf16_ss(tmem + C::TM_S, sdesc_sw128(sb + off, 16, 1024),
+                     sdesc_sw128(sk + off, 16, 1024), id, kk > 0);
+      }
+      umma_commit(smem_u32(&bars->k_empty[st]));
+      umma_commit(smem_u32(&bars->s_full));
+      if (!(ok = mbar_wait(smem_u32(&bars->v_full[st]), ph))) break;
+      if (!(ok = mbar_wait(smem_u32(&bars->p_full), n & 1))) break;
+      tc_fence_after();
+      // O += P V: A = P from TMEM, B = V [keys][d] MN-major, 16 keys per step.
+      for (int kk = 0; kk < 4 * nb; ++kk)
+        umma_bf16_ts(tmem + C::TM_O, tmem + C::TM_S + kk * 8,
+                     sdesc_sw128(sv + kk * 2048, 128 * 128, 1024), idesc_o,
+                     (n > 0 || kk > 0) ? 1u : 0u);
+      umma_commit(smem_u32(&bars->v_empty[st]));
+    }
+    umma_commit(smem_u32(&bars->o_full));
+    if (!ok) {
+      atomicOr(&g_skl_error, 1u);
+      *abort_flag = 1;
+    }
+    // Every MMA of this thread must be complete before TMEM is released.
+    mbar_wait(smem_u32(&bars->o_full), 0);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+// Joins the partial outputs of `splits` CTAs: out = sum_s 2^(l_s - L) o_s with
+// L = log2 sum_s 2^(l_s). One warp per row; each lane holds D / 32 columns.
+template <int D>
+__global__ void __launch_bounds__(128) streamkl_sparse_merge_kernel(const SparseArgs a) {
+  const size_t rows = (size_t)a.B * a.H * a.N_Q;
+  const size_t row = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  float mx = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, __ldg(a.part_l + s * rows + row));
+  float acc[D / 32], tot = 0.f;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
+  if (mx > -INFINITY) {
+    for (int s = 0; s < a.splits; ++s) {
+      const float w = exp2f(__ldg(a.part_l + s * rows + row) - mx);
+      tot += w;
+      const float* src = a.part_o + (s * rows + row) * D + lane * (D / 32);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) acc[k] += w * __ldg(src + k);
+    }
+  }
+  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+#pragma unroll
+  for (int k = 0; k < D / 32; k += 2)
+    *reinterpret_cast<uint32_t*>(a.out + row * D + lane * (D / 32) + k) =
+        pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
+  if (lane == 0)
+    a.lse[row] = tot > 0.f ? (mx + log2f(tot)) * 0.69314718055994530942f : -INFINITY;
+}
+
+}  // namespace skl

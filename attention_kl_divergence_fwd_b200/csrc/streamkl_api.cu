@@ -20,6 +20,10 @@
 #include "fwd_persistent.cuh"
 #include "bwd_kernel.cuh"
 #include "merge_kernel.cuh"
+#include "sparse_fwd.cuh"
+#include "sparse_bwd.cuh"
+#include "block_mass.cuh"
+#include "block_select.cuh"
 
 namespace {
 
@@ -626,3 +630,5 @@ streamkl_status streamkl_device_status(cudaStream_t stream) {
 int streamkl_version(void) { return 200; }
 
 }  // extern "C"
+
+#include "sparse_api.cuh"

@@ -1,0 +1,271 @@
+"""Block-sparse attention steered by a distilled attention map.
+
+The divergence of ``attention_kl`` trains a student map towards a teacher's. Cut into blocks of
+64 keys, the student map then says which keys full attention has to read:
+
+    kl, _, lse_s = streamkl_fwd(q_t, k_t, q_s, k_s, ...)            # training: the map's loss
+    mass = block_mass(q_s, k_s, causal=True, lse=lse_s)             # [B, H_kv, N_Q, NB] fp32
+    idx = select_blocks(mass, n_k, topk=16, causal=True)            # [B, H_kv, N_Q, 16] int32
+    out = sparse_attention(q, k, v, idx, causal=True)               # differentiable in q, k, v
+
+and, serving one token against a padded cache (``seqlens_k``: keys of each sequence), the same
+calls with ``N_Q = 1`` and without ``lse``; ``student_sparse_attention`` makes the three in a row.
+
+Tensors are bf16 [B, heads, N, d] on one CUDA device, d in {64, 128}; K heads may be shared by a
+group of query heads, and one selection may serve several K heads. Calls run on the current (or
+the given) stream and allocate outputs and workspace from PyTorch's allocator, which makes them
+safe to capture into a CUDA graph. The selection has no gradient.
+"""
+from __future__ import annotations
+
+import math
+from typing import Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import StreamKLError, _check, _on_device, _stream_ptr, load_library
+
+BLOCK = 64  # keys per block
+
+
+def num_blocks(n_k: int) -> int:
+    """Blocks that n_k keys make up."""
+    return (int(n_k) + BLOCK - 1) // BLOCK
+
+
+def _bf16(name, t, like=None):
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 4 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 4-D bf16 CUDA tensor [B, heads, N, d]")
+    if like is not None and t.shape != like:
+        raise ValueError(f"{name} must have shape {tuple(like)}, got {tuple(t.shape)}")
+
+
+def _typed(name, t, dtype, shape):
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+    return t
+
+
+def _lens(seqlens_k, B):
+    return 0 if seqlens_k is None else _typed("seqlens_k", seqlens_k, torch.int32, (B,)).data_ptr()
+
+
+def _workspace(nbytes, device, stream):
+    """Scratch of one call; on another stream than the current one it is kept until that
+    stream is past the call."""
+    if nbytes < 0:
+        raise StreamKLError(2, "streamkl_sparse_attn_workspace")
+    if nbytes == 0:
+        return None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws, ws.data_ptr()
+
+
+def _qk_shape(q, k):
+    _bf16("q", q)
+    _bf16("k", k)
+    B, H, n_q, d = q.shape
+    if k.shape[0] != B or k.shape[3] != d:
+        raise ValueError("inconsistent shapes of q and k")
+    return B, H, k.shape[1], n_q, k.shape[2], d
+
+
+def _qkv_shape(q, k, v, block_idx):
+    B, H, h_kv, n_q, n_k, d = _qk_shape(q, k)
+    _bf16("v", v, k.shape)
+    if block_idx.dim() != 4:
+        raise ValueError("block_idx must be [B, H_sel, N_Q, topk]")
+    h_sel, topk = block_idx.shape[1], block_idx.shape[3]
+    _typed("block_idx", block_idx, torch.int32, (B, h_sel, n_q, topk))
+    return B, H, h_kv, h_sel, n_q, n_k, d, topk
+
+
+@_on_device
+def streamkl_block_mass(q_s, k_s, scale_S: float, causal: bool, lse_s=None, seqlens_k=None,
+                        mass=None, stream=None):
+    """Mass of the map softmax(scale <q_s, k_s>) on every block of 64 keys, averaged over the
+    query heads of each K head: fp32 [B, H_kv, N_Q, ceil(N_K / 64)]."""
+    B, H, h_kv, n_q, n_k, d = _qk_shape(q_s, k_s)
+    nb = num_blocks(n_k)
+    if mass is None:
+        mass = torch.empty(B, h_kv, n_q, nb, device=q_s.device, dtype=torch.float32)
+    else:
+        _typed("mass", mass, torch.float32, (B, h_kv, n_q, nb))
+    nbytes = ws = lse = 0
+    keep = None
+    if lse_s is None:
+        nbytes = 4 * B * H * n_q * nb
+        keep, ws = _workspace(nbytes, q_s.device, stream)
+    else:
+        lse = _typed("lse_s", lse_s, torch.float32, (B, H, n_q)).data_ptr()
+    st = load_library().streamkl_block_mass(
+        q_s.data_ptr(), k_s.data_ptr(), _lens(seqlens_k, B), B, H, h_kv, n_q, n_k, d,
+        float(scale_S), int(bool(causal)), lse, ws, nbytes, mass.data_ptr(), _stream_ptr(stream))
+    _check(st, "streamkl_block_mass")
+    return mass
+
+
+@_on_device
+def streamkl_block_select(mass, n_k: int, causal: bool, topk: int, n_first: int = 1,
+                          n_last: int = 1, seqlens_k=None, block_idx=None, stream=None):
+    """The blocks each query reads: int32 [B, H_sel, N_Q, topk], ascending, -1 behind the last."""
+    if mass.dim() != 4:
+        raise ValueError("mass must be [B, H_sel, N_Q, NB]")
+    B, h_sel, n_q, nb = mass.shape
+    _typed("mass", mass, torch.float32, (B, h_sel, n_q, nb))
+    n_k, topk = int(n_k), int(topk)
+    if num_blocks(n_k) != nb:
+        raise ValueError(f"mass has {nb} blocks, n_k = {n_k} keys make {num_blocks(n_k)}")
+    if block_idx is None:
+        block_idx = torch.empty(B, h_sel, n_q, max(topk, 0), device=mass.device, dtype=torch.int32)
+    else:
+        _typed("block_idx", block_idx, torch.int32, (B, h_sel, n_q, topk))
+    st = load_library().streamkl_block_select(
+        mass.data_ptr(), _lens(seqlens_k, B), B, h_sel, n_q, n_k, int(bool(causal)), topk,
+        int(n_first), int(n_last), block_idx.data_ptr(), _stream_ptr(stream))
+    _check(st, "streamkl_block_select")
+    return block_idx
+
+
+@_on_device
+def streamkl_sparse_attn_fwd(q, k, v, block_idx, scale: float, causal: bool, seqlens_k=None,
+                             out=None, lse=None, stream=None):
+    """Attention of every query over its listed blocks: out bf16 [B, H, N_Q, d] and the
+    log-sum-exps fp32 [B, H, N_Q]."""
+    B, H, h_kv, h_sel, n_q, n_k, d, topk = _qkv_shape(q, k, v, block_idx)
+    lib = load_library()
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _bf16("out", out, q.shape)
+    if lse is None:
+        lse = torch.empty(B, H, n_q, device=q.device, dtype=torch.float32)
+    else:
+        _typed("lse", lse, torch.float32, (B, H, n_q))
+    nbytes = lib.streamkl_sparse_attn_workspace(B, H, h_kv, h_sel, n_q, n_k, d, topk, 0)
+    keep, ws = _workspace(max(nbytes, 0), q.device, stream)
+    st = lib.streamkl_sparse_attn_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), block_idx.data_ptr(), _lens(seqlens_k, B), B, H,
+        h_kv, h_sel, n_q, n_k, d, topk, float(scale), int(bool(causal)), ws, nbytes,
+        out.data_ptr(), lse.data_ptr(), _stream_ptr(stream))
+    _check(st, "streamkl_sparse_attn_fwd")
+    return out, lse
+
+
+@_on_device
+def streamkl_sparse_attn_bwd(q, k, v, out, lse, dout, block_idx, scale: float, causal: bool,
+                             seqlens_k=None, dq=None, dk=None, dv=None, stream=None):
+    """dQ, dK, dV (bf16, the shapes of q, k, v) from the forward's out and lse."""
+    B, H, h_kv, h_sel, n_q, n_k, d, topk = _qkv_shape(q, k, v, block_idx)
+    _bf16("out", out, q.shape)
+    _bf16("dout", dout, q.shape)
+    _typed("lse", lse, torch.float32, (B, H, n_q))
+    grads = []
+    for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if g is None:
+            g = torch.empty_like(like)
+        else:
+            _bf16(name, g, like.shape)
+        grads.append(g)
+    dq, dk, dv = grads
+    lib = load_library()
+    nbytes = lib.streamkl_sparse_attn_workspace(B, H, h_kv, h_sel, n_q, n_k, d, topk, 1)
+    keep, ws = _workspace(max(nbytes, 0), q.device, stream)
+    st = lib.streamkl_sparse_attn_bwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+        block_idx.data_ptr(), _lens(seqlens_k, B), B, H, h_kv, h_sel, n_q, n_k, d, topk,
+        float(scale), int(bool(causal)), ws, nbytes, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+        _stream_ptr(stream))
+    _check(st, "streamkl_sparse_attn_bwd")
+    return dq, dk, dv
+
+
+class SparseAttentionFunction(torch.autograd.Function):
+    """Attention over selected blocks; gradients flow to q, k and v."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, block_idx, seqlens_k, scale: float, causal: bool):
+        from .autograd import _after_launch
+        out, lse = streamkl_sparse_attn_fwd(q, k, v, block_idx, scale, causal, seqlens_k)
+        _after_launch("sparse_attention forward", q.device)
+        ctx.save_for_backward(q, k, v, out, lse, block_idx, seqlens_k)
+        ctx.params = (scale, causal)
+        ctx.mark_non_differentiable(lse)
+        return out, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_out, _g_lse=None):
+        from .autograd import _after_launch
+        q, k, v, out, lse, block_idx, seqlens_k = ctx.saved_tensors
+        scale, causal = ctx.params
+        dout = g_out.to(torch.bfloat16).contiguous()
+        dq, dk, dv = streamkl_sparse_attn_bwd(q, k, v, out, lse, dout, block_idx, scale, causal,
+                                              seqlens_k)
+        _after_launch("sparse_attention backward", q.device)
+        return dq, dk, dv, None, None, None, None
+
+
+def _lens_arg(seqlens_k):
+    return None if seqlens_k is None else seqlens_k.to(torch.int32).contiguous()
+
+
+def block_mass(q_s, k_s, scale: Optional[float] = None, causal: bool = False, lse=None,
+               seqlens_k=None):
+    """Mass of the student map on every block of 64 keys, averaged over the query heads that
+    share a K head: fp32 [B, H_kv, N_Q, NB]; a row sums to 1.
+
+    ``lse`` are the map's row log-sum-exps [B, H, N_Q] (``streamkl_fwd``'s lse_s) when they are
+    at hand; without them the rows are normalised by their own sums. The default scale is
+    1/sqrt(d). Not differentiable: the map is trained by its divergence."""
+    scale = 1.0 / math.sqrt(q_s.shape[-1]) if scale is None else float(scale)
+    return streamkl_block_mass(q_s.detach().contiguous(), k_s.detach().contiguous(), scale, causal,
+                               None if lse is None else lse.detach().contiguous(),
+                               _lens_arg(seqlens_k))
+
+
+def select_blocks(mass, n_k: int, topk: int, causal: bool = False, n_first: int = 1,
+                  n_last: int = 1, seqlens_k=None):
+    """Of the blocks a query sees: the first ``n_first``, the last ``n_last`` and the heaviest of
+    the rest, ``topk`` in all: int32 [B, H_sel, N_Q, topk], ascending, -1 behind the last.
+    Equal masses go to the lower index, NaN ranks below every number."""
+    return streamkl_block_select(mass.detach().contiguous(), n_k, causal, topk, n_first, n_last,
+                                 _lens_arg(seqlens_k))
+
+
+def sparse_attention(q, k, v, block_idx, scale: Optional[float] = None, causal: bool = False,
+                     seqlens_k=None, return_lse: bool = False):
+    """Softmax attention of every query over the keys of its listed blocks, differentiable in q,
+    k and v: bf16 [B, H, N_Q, d] (and the log-sum-exps fp32 [B, H, N_Q] with ``return_lse``,
+    without gradient).
+
+    block_idx int32 [B, H_sel, N_Q, topk]: a set per query (order and repeats do not matter,
+    entries outside 0 .. NB-1 select nothing); query head h reads list h // (H // H_sel). A query
+    with nothing to read gets 0 (log-sum-exp -inf) and passes no gradient."""
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
+    q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    block_idx, lens = block_idx.contiguous(), _lens_arg(seqlens_k)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        out, lse = SparseAttentionFunction.apply(q, k, v, block_idx, lens, scale, bool(causal))
+    else:
+        from .autograd import _after_launch
+        out, lse = streamkl_sparse_attn_fwd(q, k, v, block_idx, scale, causal, lens)
+        _after_launch("sparse_attention forward", q.device)
+    return (out, lse) if return_lse else out
+
+
+def student_sparse_attention(q, k, v, q_s, k_s, topk: int, scale: Optional[float] = None,
+                             scale_s: Optional[float] = None, causal: bool = False, lse_s=None,
+                             n_first: int = 1, n_last: int = 1, seqlens_k=None):
+    """Attention over the blocks that the student map of (q_s, k_s) puts most mass on:
+    ``block_mass``, ``select_blocks`` and ``sparse_attention`` in a row.
+
+    The student's K heads are the selection heads: their number and k's have to divide one
+    another. Gradients flow to q, k and v only. Returns (out, block_idx)."""
+    lens = _lens_arg(seqlens_k)
+    mass = block_mass(q_s, k_s, scale_s, causal, lse_s, lens)
+    idx = select_blocks(mass, k_s.shape[2], topk, causal, n_first, n_last, lens)
+    return sparse_attention(q, k, v, idx, scale, causal, lens), idx

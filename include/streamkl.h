@@ -247,6 +247,89 @@ streamkl_status streamkl_bwd_teacher_shard(const void* q_t, const void* k_t, con
                                            cudaStream_t stream);
 
 /*
+ * Block-sparse attention steered by a distilled map. The student map that the divergence
+ * trains says how much of the teacher's attention each key gets; cut into blocks of 64 keys
+ * it selects, for every query, the blocks that full attention then reads:
+ *   streamkl_block_mass        mass of every block under the student map,
+ *   streamkl_block_select      the blocks each query reads,
+ *   streamkl_sparse_attn_fwd   softmax attention over those blocks,
+ *   streamkl_sparse_attn_bwd   its gradients.
+ * Conventions as above, with these additions:
+ * - Dense layout [B,heads,N,d], d in {64, 128}, NB = ceil(N_K / 64) blocks, the last one
+ *   possibly short. Causal alignment is bottom-right: query i sees keys j <= i + n_k - N_Q.
+ * - seqlens_k (DEVICE int32 [B], or null for N_K everywhere): sequence b has its first
+ *   n_k = seqlens_k[b] keys, 0 <= n_k <= N_K, in a padded cache; what the cache holds behind
+ *   them (NaN included) is never used. A length outside that range is read as 0 and recorded
+ *   as STREAMKL_ERR_INVALID_ARG in the device error word. Keys and values of the first n_k
+ *   rows, and queries and output gradients, have to be finite.
+ * - A query that sees no key (or lists no block with one) gets mass 0, no blocks, out = 0,
+ *   lse = -inf and zero gradients.
+ * - Workspaces are caller-allocated device memory of any content, 16-byte aligned, used
+ *   by the call's kernels on `stream` only; they may be reused by the next call on that stream.
+ *   Two calls that can run at the same time need one each.
+ *
+ * Block mass: k [B,H_kv,N_K,d], G = H / H_kv query heads share a K head,
+ *   mass[b,hk,i,c] = 1/G sum_{h in group hk} sum_{j in block c, allowed} exp(s[h,i,j] - lse[h,i])
+ * (fp32 [B,H_kv,N_Q,NB], fully overwritten). lse [B,H,N_Q] is streamkl_fwd's lse_s when the
+ * divergence has been computed; with lse = null the rows are normalised by their own sum, which
+ * takes a workspace of 4 * B * H * N_Q * NB bytes.
+ */
+streamkl_status streamkl_block_mass(const void* q, const void* k, const int* seqlens_k, int B,
+                                    int H, int H_kv, int N_Q, int N_K, int d, float scale,
+                                    int causal, const float* lse, void* workspace,
+                                    long long workspace_bytes, float* mass, cudaStream_t stream);
+
+/*
+ * Selection: of the blocks that hold a key query i sees, the first n_first, the last n_last and
+ * the heaviest of the rest, topk in all (n_first + n_last <= topk); equal masses go to the lower
+ * index, NaN ranks below every number. block_idx int32 [B,H_sel,N_Q,topk], ascending, -1
+ * behind the last entry. mass fp32 [B,H_sel,N_Q,NB]; masses of unseen blocks are not read.
+ * N_K <= 524288.
+ */
+streamkl_status streamkl_block_select(const float* mass, const int* seqlens_k, int B, int H_sel,
+                                      int N_Q, int N_K, int causal, int topk, int n_first,
+                                      int n_last, int* block_idx, cudaStream_t stream);
+
+/*
+ * Bytes of workspace that the forward (backward = 0) or the backward (1) needs for these
+ * sizes on the current device; -1 for sizes that the entry points reject.
+ */
+long long streamkl_sparse_attn_workspace(int B, int H, int H_kv, int H_sel, int N_Q, int N_K,
+                                         int d, int topk, int backward);
+
+/*
+ * Attention over selected blocks: q [B,H,N_Q,d], k, v [B,H_kv,N_K,d], block_idx
+ * [B,H_sel,N_Q,topk]; query head h reads K head h / (H / H_kv) and the list of selection head
+ * h / (H / H_sel). H_kv and H_sel divide H, one of them divides the other, and
+ * H / max(H_kv, H_sel) <= 128. A list is a set: any order, repeated entries count once, entries
+ * outside 0 .. NB-1 are ignored.
+ *   out (bf16 [B,H,N_Q,d]) = softmax over the listed, allowed keys of scale <q, k>, times v
+ *   lse (fp32 [B,H,N_Q])   = log-sum-exp of those scores
+ * The workspace holds one bit per query, block and selection head, and the partial outputs of
+ * lists that are split over several CTAs.
+ */
+streamkl_status streamkl_sparse_attn_fwd(const void* q, const void* k, const void* v,
+                                         const int* block_idx, const int* seqlens_k, int B, int H,
+                                         int H_kv, int H_sel, int N_Q, int N_K, int d, int topk,
+                                         float scale, int causal, void* workspace,
+                                         long long workspace_bytes, void* out, float* lse,
+                                         cudaStream_t stream);
+
+/*
+ * Gradients of the above from the forward's out and lse and dout (bf16 [B,H,N_Q,d]): dq, dk, dv
+ * in bf16 and the shapes of q, k, v, fully overwritten (0 for keys no query lists). Shared K
+ * heads and shared lists are summed in one place, without atomics: the same call gives the
+ * same bits. The selection itself has no gradient.
+ */
+streamkl_status streamkl_sparse_attn_bwd(const void* q, const void* k, const void* v,
+                                         const void* out, const float* lse, const void* dout,
+                                         const int* block_idx, const int* seqlens_k, int B, int H,
+                                         int H_kv, int H_sel, int N_Q, int N_K, int d, int topk,
+                                         float scale, int causal, void* workspace,
+                                         long long workspace_bytes, void* dq, void* dk, void* dv,
+                                         cudaStream_t stream);
+
+/*
  * Diagnostic: launches one thread that waits, with the library's bounded pipeline wait
  * (2 s), on a barrier nothing arrives on. After it gives up, streamkl_device_status(stream)
  * returns STREAMKL_ERR_TIMEOUT, exactly as for a kernel whose pipeline stalled, and the

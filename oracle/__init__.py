@@ -19,3 +19,9 @@ from .streamkl_oracle import (  # noqa: F401
     oracle_rows,
     row_pair_count,
 )
+from .sparse_oracle import (  # noqa: F401
+    oracle_block_mass,
+    oracle_block_select,
+    oracle_sparse_attn,
+    selected_keys,
+)

@@ -15,6 +15,9 @@
 // Bound by the exponential unit (one exponential per pair) for many queries, by reading K for
 // few. Two CTAs per SM.
 //
+// QUAD: tiles of at most 32 rows, four copies, each row warp 32 of a pair's 128 keys (sp_quad);
+// a block's two halves are joined when the staged values are written.
+//
 // Warps: 0-3 rows, 4 TMA producer, 5 MMA + TMEM.
 #pragma once
 
@@ -57,24 +60,27 @@ static_assert(sizeof(MassBars) <= 256, "barrier block");
 
 constexpr int kMassThreads = 192;
 
-// Row value of one block: sum 2^(s c - lse2) (NORM) or log2 sum 2^(s c).
-template <bool NORM>
-__device__ __forceinline__ float mass_block(const uint32_t (&v)[64], float c, float nl, int lim) {
+// Value of a row over N keys: sum 2^(s c - lse2) (NORM) or log2 sum 2^(s c); keys past lim are
+// left out.
+template <bool NORM, int N>
+__device__ __forceinline__ float mass_block(const uint32_t (&v)[N], float c, float nl, int lim) {
   float bias = nl;
   if (!NORM) {
     float mx = -INFINITY;
-    if (lim >= 63) {
-      mx = fmaxf(max_tree32<false>(v, 0, 31), max_tree32<false>(v, 32, 31));
+    if (lim >= N - 1) {
+#pragma unroll
+      for (int k = 0; k < N; k += 32) mx = fmaxf(mx, max_tree32<false>(v, k, 31));
     } else {
-      mx = fmaxf(max_tree32<true>(v, 0, lim), max_tree32<true>(v, 32, lim - 32));
+#pragma unroll
+      for (int k = 0; k < N; k += 32) mx = fmaxf(mx, max_tree32<true>(v, k, lim - k));
     }
     if (mx == -INFINITY) return -INFINITY;
     bias = -mx * c;
   }
   float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-  if (lim >= 63) {
+  if (lim >= N - 1) {
 #pragma unroll
-    for (int k = 0; k < 64; k += 4) {
+    for (int k = 0; k < N; k += 4) {
       s0 += ex2_approx(fmaf(__uint_as_float(v[k]), c, bias));
       s1 += ex2_approx(fmaf(__uint_as_float(v[k + 1]), c, bias));
       s2 += ex2_approx(fmaf(__uint_as_float(v[k + 2]), c, bias));
@@ -82,7 +88,7 @@ __device__ __forceinline__ float mass_block(const uint32_t (&v)[64], float c, fl
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 64; ++k) {
+    for (int k = 0; k < N; ++k) {
       const float e = ex2_approx(fmaf(__uint_as_float(v[k]), c, bias));
       s0 += k <= lim ? e : 0.f;
     }
@@ -91,7 +97,7 @@ __device__ __forceinline__ float mass_block(const uint32_t (&v)[64], float c, fl
   return NORM ? s : log2f(s) - bias;
 }
 
-template <int D, bool NORM>
+template <int D, bool NORM, bool QUAD>
 __global__ void __launch_bounds__(kMassThreads, 2)
 streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k, const MassArgs ma,
@@ -145,7 +151,7 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
   const uint32_t tmem = bars->tmem_base;
 
   if (warp < 4) {
-    const int r = warp * 32 + lane;
+    const int r = QUAD ? lane : warp * 32 + lane;
     const int g = r / a.Qn, qi = r - g * a.Qn, i = q0 + qi;
     const bool valid = g < a.G && i < a.N_Q;
     const int last = valid ? sp_last(i, nk, a.N_Q, a.causal) : -1;
@@ -163,20 +169,28 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
     const int nq = min(a.Qn, a.N_Q - q0);
     const float inv_g = 1.f / (float)a.G;
     // Writes the staged values of blocks cg .. cg + n - 1.
+    auto staged = [&](int row) -> float {
+      const float x = stage[row * 33 + lane];
+      if (!QUAD) return x;
+      const float y = stage[(32 + row) * 33 + lane];  // the block's other half
+      if (NORM) return x + y;
+      const float m = fmaxf(x, y);
+      return m == -INFINITY ? m : m + log2f(exp2f(x - m) + exp2f(y - m));
+    };
     auto flush = [&](int cg, int n) {
       named_bar_sync(1, 128);
       if (NORM) {
         float* dst = ma.mass + ((size_t)bp * a.N_Q + q0) * a.NB + cg;
         for (int q = warp; q < nq; q += 4) {
           float s = 0.f;
-          for (int h = 0; h < a.G; ++h) s += stage[(h * a.Qn + q) * 33 + lane];
+          for (int h = 0; h < a.G; ++h) s += staged(h * a.Qn + q);
           if (lane < n) dst[(size_t)q * a.NB + lane] = s * inv_g;
         }
       } else {
         float* dst = ma.blse + ((size_t)h0 * a.N_Q + q0) * a.NB + cg;
         for (int h = 0; h < a.G; ++h)
           for (int q = warp; q < nq; q += 4)
-            if (lane < n) dst[((size_t)h * a.N_Q + q) * a.NB + lane] = stage[(h * a.Qn + q) * 33 + lane];
+            if (lane < n) dst[((size_t)h * a.N_Q + q) * a.NB + lane] = staged(h * a.Qn + q);
       }
       named_bar_sync(1, 128);
     };
@@ -187,22 +201,39 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
       if (ok && !mbar_wait(smem_u32(&bars->s_full[s & 1]), (s >> 1) & 1)) ok = false;
       tc_fence_after();
       const int cb = 2 * s;  // first block of the pair, from c_begin
+      if constexpr (QUAD) {
+        // Keys 32 warp .. +31 of the pair: half warp & 1 of block warp / 2.
+        uint32_t v[32];
+        tmem_ld_32_wait(ts + (s & 1) * 128 + 32 * warp, v);
+        const int lim = row_on ? last - (c_begin + cb) * kSpBlock - 32 * warp : (valid ? -1 : 31);
+        float x = NORM ? 0.f : -INFINITY;
+        if (__all_sync(0xffffffffu, lim >= 31)) {
+          x = mass_block<NORM, 32>(v, c, nl, 31);
+        } else if (__any_sync(0xffffffffu, lim >= 0)) {
+          const float y = mass_block<NORM, 32>(v, c, nl, min(lim, 30));
+          const float z = mass_block<NORM, 32>(v, c, nl, 31);
+          x = lim >= 31 ? z : (lim >= 0 ? y : x);
+        }
+        stage[((warp & 1) * 32 + r) * 33 + ((cb + (warp >> 1)) & 31)] = x;
+      } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float x = NORM ? 0.f : -INFINITY;
         if (warp_live) {
           uint32_t v[64];
           tmem_ld_2x32_wait(ts + (s & 1) * 128 + 64 * h, ts + (s & 1) * 128 + 64 * h + 32, v);
-          const int lim = row_on ? last - (c_begin + cb + h) * kSpBlock : -1;
+          // Rows past the tile's end take the common path; their values are not written.
+          const int lim = row_on ? last - (c_begin + cb + h) * kSpBlock : (valid ? -1 : 63);
           if (__all_sync(0xffffffffu, lim >= 63)) {
-            x = mass_block<NORM>(v, c, nl, 63);
+            x = mass_block<NORM, 64>(v, c, nl, 63);
           } else if (__any_sync(0xffffffffu, lim >= 0)) {
-            const float y = mass_block<NORM>(v, c, nl, min(lim, 62));
-            const float z = mass_block<NORM>(v, c, nl, 63);
+            const float y = mass_block<NORM, 64>(v, c, nl, min(lim, 62));
+            const float z = mass_block<NORM, 64>(v, c, nl, 63);
             x = lim >= 63 ? z : (lim >= 0 ? y : x);
           }
         }
         stage[r * 33 + ((cb + h) & 31)] = x;
+      }
       }
       tc_fence_before();
       __syncwarp();
@@ -228,9 +259,11 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
       tma_prefetch_desc(&map_k);
       const uint64_t keep = l2_policy_evict_last();
       const uint32_t qb = smem_u32(&bars->q_full);
-      mbar_arrive_expect_tx(qb, a.Qn * a.G * D * 2);
+      mbar_arrive_expect_tx(qb, (QUAD ? 4 : 1) * a.Qn * a.G * D * 2);
       for (int blk = 0; blk < D / 64; ++blk)
-        tma_load_3d(sb + blk * (C::BM * 128), &map_q, qb, blk * 64, q0, h0, keep);
+        for (int copy = 0; copy < (QUAD ? 4 : 1); ++copy)
+          tma_load_3d(sb + blk * (C::BM * 128) + copy * (32 * 128), &map_q, qb, blk * 64, q0, h0,
+                      keep);
       int issued = 0;
       for (int s = 0; s < steps; ++s) {
         const int st = s % C::NST;
@@ -286,48 +319,50 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
 }
 
 // Second kernel of the form without LSEs: mass[c] = 1/G sum_g 2^(x_gc - L_g), with
-// L_g = log2 sum_c 2^(x_gc) over the row's visible blocks. One CTA per (K head, query).
+// L_g = log2 sum_c 2^(x_gc) over the row's visible blocks. One CTA per (K head, query): each warp
+// takes the sums of every eighth head, then all threads the blocks.
 __global__ void __launch_bounds__(256) streamkl_block_norm_kernel(const MassArgs ma) {
   const SparseArgs& a = ma.s;
-  __shared__ float red[8];
+  __shared__ float row_l[128];
   const int bp = blockIdx.x / a.N_Q, i = blockIdx.x - bp * a.N_Q, b = bp / a.P, p = bp - b * a.P;
   const int nk = sp_len(a.lens, b, a.N_K);
   const int last = sp_last(i, nk, a.N_Q, a.causal);
   const int n = last < 0 ? 0 : last / kSpBlock + 1;
   float* dst = ma.mass + ((size_t)bp * a.N_Q + i) * a.NB;
+  const float* x = ma.blse + ((size_t)(b * a.H + p * a.G) * a.N_Q + i) * a.NB;
+  const size_t hs = (size_t)a.N_Q * a.NB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float inv_g = 1.f / (float)a.G;
-  if (n == 0) {
-    for (int c = threadIdx.x; c < a.NB; c += blockDim.x) dst[c] = 0.f;
-    return;
-  }
-  for (int g = 0; g < a.G; ++g) {
-    const float* x = ma.blse + ((size_t)(b * a.H + p * a.G + g) * a.N_Q + i) * a.NB;
-    float mx = -INFINITY;
-    for (int c = threadIdx.x; c < n; c += blockDim.x) mx = fmaxf(mx, x[c]);
+  for (int g = warp; g < a.G; g += 8) {
+    float mx = -INFINITY, sum = 0.f;
+    for (int c = lane; c < n; c += 128) {  // four loads in flight
+      float y[4];
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-    if (lane == 0) red[warp] = mx;
-    __syncthreads();
-    mx = red[0];
+      for (int k = 0; k < 4; ++k) y[k] = c + 32 * k < n ? x[g * hs + c + 32 * k] : -INFINITY;
+      const float t = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+      if (t > mx) {
+        sum *= exp2f(mx - t);
+        mx = t;
+      }
+      if (mx > -INFINITY) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) mx = fmaxf(mx, red[k]);
-    __syncthreads();
-    float sum = 0.f;
-    for (int c = threadIdx.x; c < n; c += blockDim.x) sum += exp2f(x[c] - mx);
+        for (int k = 0; k < 4; ++k) sum += exp2f(y[k] - mx);
+      }
+    }
+    float all = mx;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, s));
+    sum = mx > -INFINITY ? sum * exp2f(mx - all) : 0.f;
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    if (lane == 0) red[warp] = sum;
-    __syncthreads();
-    sum = red[0];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) sum += red[k];
-    __syncthreads();
-    const float f = inv_g / sum;
-    for (int c = threadIdx.x; c < a.NB; c += blockDim.x) {
-      const float y = c < n ? exp2f(x[c] - mx) * f : 0.f;
-      dst[c] = g == 0 ? y : dst[c] + y;  // the same thread wrote it
-    }
+    if (lane == 0) row_l[g] = all + log2f(sum);
+  }
+  __syncthreads();
+  const float inv_g = 1.f / (float)a.G;
+  for (int c = threadIdx.x; c < a.NB; c += 256) {
+    float y = 0.f;
+    if (c < n)
+      for (int g = 0; g < a.G; ++g) y += exp2f(x[g * hs + c] - row_l[g]);
+    dst[c] = y * inv_g;
   }
 }
 

@@ -19,6 +19,18 @@ bool make_map_heads(CUtensorMap* m, const void* base, int d, long long rows, lon
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Raises a kernel's dynamic shared-memory limit on the current device once (`done`: one flag
+// per device and kernel; threads that race on it set the same value).
+template <typename Kern>
+bool set_smem_once(Kern k, int bytes, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return true;
+  if (!set_smem(k, bytes)) return false;
+  if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return true;
+}
+
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 constexpr int kMaxTopk = 1 << 20;
@@ -63,27 +75,24 @@ long long mask_bytes(const skl::SparseArgs& a) {
   return round256(4ll * a.B * a.Hsel * ((a.N_Q + 31) / 32) * a.NB);
 }
 
-// CTAs that share a tile's list: with fewer tiles than about two waves of CTAs (two per SM) the
-// lists are dealt out, down to one pair of blocks per CTA.
+// CTAs of a cluster that share a tile's list: as many as keep the grid within one wave (two CTAs
+// per SM), at most 8 (the portable cluster size), each with at least one pair of blocks. A
+// second wave costs more than longer lists: one token of 32 sequences of 8 K heads (256 tiles,
+// 8 pairs each) takes 53 us with 3 CTAs per tile and the figure in sparse_fwd.cuh with one.
 int sparse_splits(const skl::SparseArgs& a) {
-  const long long ctas = (long long)a.B * a.P * a.n_tiles, want = 4ll * sm_count();
-  long long blocks = (long long)a.Qn * a.topk;
-  if (blocks > a.NB) blocks = a.NB;
-  long long s = (want + ctas - 1) / ctas;
-  if (s > (blocks + 1) / 2) s = (blocks + 1) / 2;
-  return (int)(s < 1 ? 1 : (s > 32 ? 32 : s));
+  const long long ctas = (long long)a.B * a.P * a.n_tiles;
+  long long pairs = (long long)a.Qn * a.topk;
+  pairs = ((pairs < a.NB ? pairs : a.NB) + 1) / 2;
+  long long s = 2ll * sm_count() / ctas;
+  if (s > pairs) s = pairs;
+  return (int)(s < 1 ? 1 : (s > 8 ? 8 : s));
 }
 
 bool sparse_direct(const skl::SparseArgs& a) {
-  return a.N_Q == 1 && a.G <= 64 && a.NB <= 65536;
+  return a.N_Q == 1 && a.G <= 16 && a.NB <= 16384;
 }
 
-long long fwd_ws_bytes(const skl::SparseArgs& a, int d) {
-  const long long rows = (long long)a.B * a.H * a.N_Q;
-  const int s = sparse_splits(a);
-  return (sparse_direct(a) ? 0 : mask_bytes(a)) +
-         (s > 1 ? round256(4ll * s * rows * d) + round256(4ll * s * rows) : 0);
-}
+long long fwd_ws_bytes(const skl::SparseArgs& a) { return sparse_direct(a) ? 0 : mask_bytes(a); }
 
 long long bwd_ws_bytes(const skl::SparseArgs& a) {
   return mask_bytes(a) + round256(8ll * a.B * a.H * a.N_Q);
@@ -101,7 +110,7 @@ streamkl_status launch_mask(skl::SparseArgs& a, void* ws, cudaStream_t stream) {
   return ok_launch();
 }
 
-template <int D>
+template <int D, bool QUAD>
 streamkl_status launch_sparse_fwd(const skl::SparseArgs& a, const void* q, const void* k,
                                   const void* v, cudaStream_t stream) {
   using C = skl::SpFwdCfg<D>;
@@ -110,18 +119,26 @@ streamkl_status launch_sparse_fwd(const skl::SparseArgs& a, const void* q, const
       !make_map_heads(&mk, k, D, a.N_K, (long long)a.B * a.Hkv, 64, 1) ||
       !make_map_heads(&mv, v, D, a.N_K, (long long)a.B * a.Hkv, 64, 1))
     return STREAMKL_ERR_LAUNCH;
-  auto kern = skl::streamkl_sparse_fwd_kernel<D>;
-  if (!set_smem(kern, C::SMEM)) return STREAMKL_ERR_LAUNCH;
+  auto kern = skl::streamkl_sparse_fwd_kernel<D, QUAD>;
+  static std::atomic<bool> done[64] = {};
+  if (!set_smem_once(kern, C::SMEM, done)) return STREAMKL_ERR_LAUNCH;
   const bool neg = a.scale < 0.f;
-  const long long grid = (long long)a.B * a.P * a.n_tiles * a.splits;
-  kern<<<(unsigned)grid, skl::kSpThreads, C::SMEM, stream>>>(
-      mq, mk, mv, a, skl::idesc_bf16_f32(128, 128, false, false, neg),
-      skl::idesc_bf16_f32(128, 64, false, false, neg), skl::idesc_bf16_f32(128, D, false, true));
-  if (a.splits > 1) {
-    const long long rows = (long long)a.B * a.H * a.N_Q;
-    skl::streamkl_sparse_merge_kernel<D><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(a);
-  }
-  return ok_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((long long)a.B * a.P * a.n_tiles * a.splits));
+  cfg.blockDim = dim3(skl::kSpThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)a.splits, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a,
+                            skl::idesc_bf16_f32(128, 128, false, false, neg),
+                            skl::idesc_bf16_f32(128, 64, false, false, neg),
+                            skl::idesc_bf16_f32(128, D, false, true)) == cudaSuccess
+             ? STREAMKL_OK
+             : (cudaGetLastError(), STREAMKL_ERR_LAUNCH);
 }
 
 template <int D>
@@ -138,7 +155,9 @@ streamkl_status launch_sparse_bwd(const skl::SparseArgs& a, const void* q, const
     return STREAMKL_ERR_LAUNCH;
   auto kq = skl::streamkl_sparse_dq_kernel<D>;
   auto kk = skl::streamkl_sparse_dkv_kernel<D>;
-  if (!set_smem(kq, CQ::SMEM) || !set_smem(kk, CK::SMEM)) return STREAMKL_ERR_LAUNCH;
+  static std::atomic<bool> done_q[64] = {}, done_k[64] = {};
+  if (!set_smem_once(kq, CQ::SMEM, done_q) || !set_smem_once(kk, CK::SMEM, done_k))
+    return STREAMKL_ERR_LAUNCH;
   const bool neg = a.scale < 0.f;
   const uint32_t i_s = skl::idesc_bf16_f32(128, 64, false, false, neg);
   const uint32_t i_dp = skl::idesc_bf16_f32(128, 64, false, false);
@@ -153,7 +172,7 @@ streamkl_status launch_sparse_bwd(const skl::SparseArgs& a, const void* q, const
   return ok_launch();
 }
 
-template <int D, bool NORM>
+template <int D, bool NORM, bool QUAD>
 streamkl_status launch_mass(const skl::MassArgs& ma, const void* q, const void* k,
                             cudaStream_t stream) {
   using C = skl::MassCfg<D>;
@@ -162,8 +181,9 @@ streamkl_status launch_mass(const skl::MassArgs& ma, const void* q, const void* 
   if (!make_map_heads(&mq, q, D, a.N_Q, (long long)a.B * a.H, a.Qn, a.G) ||
       !make_map_heads(&mk, k, D, a.N_K, (long long)a.B * a.P, 128, 1))
     return STREAMKL_ERR_LAUNCH;
-  auto kern = skl::streamkl_block_mass_kernel<D, NORM>;
-  if (!set_smem(kern, C::SMEM)) return STREAMKL_ERR_LAUNCH;
+  auto kern = skl::streamkl_block_mass_kernel<D, NORM, QUAD>;
+  static std::atomic<bool> done[64] = {};
+  if (!set_smem_once(kern, C::SMEM, done)) return STREAMKL_ERR_LAUNCH;
   const long long grid = (long long)a.B * a.P * a.n_tiles * ma.n_chunks;
   if (grid >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
   kern<<<(unsigned)grid, skl::kMassThreads, C::SMEM, stream>>>(
@@ -185,7 +205,7 @@ long long streamkl_sparse_attn_workspace(int B, int H, int H_kv, int H_sel, int 
       sparse_problem(a, nullptr, B, H, H_kv, H_sel, N_Q, N_K, d, 1.f, 0) != STREAMKL_OK)
     return -1;
   a.topk = topk;
-  return backward ? bwd_ws_bytes(a) : fwd_ws_bytes(a, d);
+  return backward ? bwd_ws_bytes(a) : fwd_ws_bytes(a);
 }
 
 streamkl_status streamkl_sparse_attn_fwd(const void* q, const void* k, const void* v,
@@ -201,7 +221,7 @@ streamkl_status streamkl_sparse_attn_fwd(const void* q, const void* k, const voi
   if (topk < 1 || !q || !k || !v || !block_idx || !out || !lse) return STREAMKL_ERR_INVALID_ARG;
   if (topk > kMaxTopk) return STREAMKL_ERR_UNSUPPORTED;
   a.topk = topk;
-  const long long need = fwd_ws_bytes(a, d);
+  const long long need = fwd_ws_bytes(a);
   if (need > 0 && (!workspace || workspace_bytes < need)) return STREAMKL_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse) ||
       !aligned16(workspace) || misaligned4(block_idx))
@@ -211,19 +231,15 @@ streamkl_status streamkl_sparse_attn_fwd(const void* q, const void* k, const voi
   a.lse = lse;
   a.splits = sparse_splits(a);
   a.direct = sparse_direct(a) ? 1 : 0;
-  char* ws = static_cast<char*>(workspace);
   if (!a.direct) {
-    const streamkl_status sm = launch_mask(a, ws, stream);
+    const streamkl_status sm = launch_mask(a, workspace, stream);
     if (sm != STREAMKL_OK) return sm;
-    ws += mask_bytes(a);
   }
-  if (a.splits > 1) {
-    const long long rows = (long long)B * H * N_Q;
-    a.part_o = reinterpret_cast<float*>(ws);
-    a.part_l = reinterpret_cast<float*>(ws + round256(4ll * a.splits * rows * d));
-  }
-  return d == 128 ? launch_sparse_fwd<128>(a, q, k, v, stream)
-                  : launch_sparse_fwd<64>(a, q, k, v, stream);
+  if (skl::sp_quad(a.Qn, a.G))
+    return d == 128 ? launch_sparse_fwd<128, true>(a, q, k, v, stream)
+                    : launch_sparse_fwd<64, true>(a, q, k, v, stream);
+  return d == 128 ? launch_sparse_fwd<128, false>(a, q, k, v, stream)
+                  : launch_sparse_fwd<64, false>(a, q, k, v, stream);
 }
 
 streamkl_status streamkl_sparse_attn_bwd(const void* q, const void* k, const void* v,
@@ -276,17 +292,25 @@ streamkl_status streamkl_block_mass(const void* q, const void* k, const int* seq
   ma.row_lse = lse;
   ma.mass = mass;
   ma.blse = lse ? nullptr : static_cast<float*>(workspace);
-  // A tile's blocks are spread over CTAs while there are fewer than about two waves of them
-  // (two per SM); a CTA takes at least one pair.
-  const long long tiles = (long long)a.B * a.P * a.n_tiles, want = 4ll * sm_count();
-  long long chunks = (want + tiles - 1) / tiles;
-  long long bpc = (a.NB + chunks - 1) / chunks;
-  bpc = (bpc + 1) / 2 * 2;
+  // A tile's blocks are spread over CTAs while there are fewer than about four waves of them
+  // (two per SM; the tail of a wave and padded sequences' early ends even out); a CTA takes at
+  // least one pair.
+  const long long tiles = (long long)a.B * a.P * a.n_tiles, want = 8ll * sm_count();
+  const long long chunks = want / tiles > 1 ? want / tiles : 1;
+  const long long bpc = ((a.NB + chunks - 1) / chunks + 1) / 2 * 2;
   ma.bpc = (int)bpc;
   ma.n_chunks = (int)((a.NB + bpc - 1) / bpc);
-  if (d == 128)
-    return lse ? launch_mass<128, true>(ma, q, k, stream) : launch_mass<128, false>(ma, q, k, stream);
-  return lse ? launch_mass<64, true>(ma, q, k, stream) : launch_mass<64, false>(ma, q, k, stream);
+  const bool quad = skl::sp_quad(a.Qn, a.G);
+  auto go = [&](auto dim, auto norm) {
+    constexpr int D = decltype(dim)::value;
+    constexpr bool N = decltype(norm)::value;
+    return quad ? launch_mass<D, N, true>(ma, q, k, stream)
+                : launch_mass<D, N, false>(ma, q, k, stream);
+  };
+  using I64 = std::integral_constant<int, 64>;
+  using I128 = std::integral_constant<int, 128>;
+  if (d == 128) return lse ? go(I128{}, std::true_type{}) : go(I128{}, std::false_type{});
+  return lse ? go(I64{}, std::true_type{}) : go(I64{}, std::false_type{});
 }
 
 streamkl_status streamkl_block_select(const float* mass, const int* seqlens_k, int B, int H_sel,

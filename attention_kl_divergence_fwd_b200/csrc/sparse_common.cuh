@@ -28,7 +28,7 @@ struct SparseArgs {
   int Hkv, Hsel;           // K heads, selection heads (both divide P)
   int Qn, n_tiles;         // queries per 128-row tile, tiles per pack
   int causal, topk;
-  int splits;              // CTAs that share one tile's list (forward)
+  int splits;              // CTAs (one cluster) that share one tile's list (forward)
   int direct;              // forward of one query: blocks straight from the list
   float c, scale;          // |scale| * log2(e); signed scale
   const int* idx;          // [B, Hsel, N_Q, topk]
@@ -37,8 +37,6 @@ struct SparseArgs {
   float2* rows;            // backward: {LSE * log2(e), sum_d out * dout} per row
   __nv_bfloat16* out;      // forward
   float* lse;
-  float* part_o;           // splits > 1: [splits, rows, d] normalised partial outputs
-  float* part_l;           //             [splits, rows] base-2 log-sum-exps
   __nv_bfloat16* dq;       // backward
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
@@ -85,6 +83,12 @@ __device__ __forceinline__ SpTile sp_tile(const SparseArgs& a, int bp, int tile)
   t.nwords = a.Qn <= 32 ? 1 : min(a.Qn >> 5, iws - (t.q0 >> 5));
   return t;
 }
+
+// Tiles of at most 32 rows (single tokens of small groups): the tile's rows are loaded four
+// times, at lanes 0, 32, 64 and 96, and each of the four row warps takes a quarter of every key
+// tile's columns. TMEM lets a warp read only its own 32 lanes, so without the copies one warp
+// would do all of the tile's exponentials while three sit idle.
+__host__ __device__ inline bool sp_quad(int Qn, int G) { return Qn * G <= 32; }
 
 // Builds the bit matrix: one CTA per 32 queries of a selection head. Entries that are
 // negative, beyond the last block, or of a block the query may not see set no bit.

@@ -13,8 +13,11 @@
 // output's own rounding); the row sums, references and O stay in fp32.
 // A CTA keeps one score buffer: 256 TMEM columns and 97 KB of shared memory, so two CTAs share
 // an SM and one's MMAs run under the other's exponentials.
-// `splits` > 1: the tile's list is dealt to that many CTAs by rank, each writes a normalised
-// partial output and its log-sum-exp, and the merge kernel joins them.
+// `splits` > 1: the tile's list is dealt to the CTAs of a cluster by rank; their normalised
+// outputs and log-sum-exps are joined through distributed shared memory, so that a single
+// token is one launch and no partial result leaves the chip.
+// QUAD: tiles of at most 32 rows, four copies, each warp a quarter of the keys (sp_quad); the
+// four quarters are joined like splits.
 //
 // Warps: 0-3 softmax (row = TMEM lane), 4 producer (scans the bit matrix, TMA), 5 MMA + TMEM.
 #pragma once
@@ -57,6 +60,7 @@ struct SpFwdBars {
   uint32_t tmem_base;
   int abort_flag;
   SpInfo info[4];
+  float l2[128];  // base-2 log-sum-exps of the partial rows
 };
 static_assert(sizeof(SpFwdBars) <= 1024, "barrier block");
 
@@ -99,7 +103,54 @@ __device__ __forceinline__ bool sp_scan(const SparseArgs& a, const SpTile& t, in
   return true;
 }
 
-template <int D>
+// Joins the partial rows of this cluster's CTAs (and of the four quarters): every source holds
+// rows normalised by its own sum, with stage[slot * (D + 4)] and the base-2 log-sum-exps in l2;
+// out = sum_s 2^(l_s - L) o_s, L = log2 sum_s 2^(l_s). Row r is joined by CTA r % splits, one
+// warp per row.
+template <int D, bool QUAD>
+__device__ __forceinline__ void sp_join(const SparseArgs& a, const SpTile& t, uint32_t stage,
+                                        uint32_t l2, int split, int warp, int lane) {
+  constexpr int NS = QUAD ? 4 : 1;
+  const int rows = a.Qn * a.G;
+  for (int r = split + warp * a.splits; r < rows; r += 4 * a.splits) {
+    const int g = r / a.Qn, i = t.q0 + r - g * a.Qn;
+    if (i >= a.N_Q) continue;
+    const int srcs = a.splits * NS;
+    float mx = -INFINITY;
+    for (int s = lane; s < srcs; s += 32)
+      mx = fmaxf(mx, ld_cluster_f32(cluster_map(l2 + ((s % NS) * 32 + r) * 4, s / NS)));
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+    float acc[D / 32], tot = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
+    if (mx > -INFINITY) {
+#pragma unroll 4
+      for (int s = 0; s < srcs; ++s) {
+        const int slot = (s % NS) * 32 + r;
+        const float w = ex2_approx(ld_cluster_f32(cluster_map(l2 + slot * 4, s / NS)) - mx);
+        tot += w;
+        const uint32_t src = cluster_map(stage + slot * (D + 4) * 4, s / NS);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          const float2 o = ld_cluster_f32x2(src + (k * 64 + lane * 2) * 4);
+          acc[2 * k] = fmaf(w, o.x, acc[2 * k]);
+          acc[2 * k + 1] = fmaf(w, o.y, acc[2 * k + 1]);
+        }
+      }
+    }
+    const float inv = tot > 0.f ? 1.f / tot : 0.f;
+    const size_t row = (size_t)(t.h0 + g) * a.N_Q + i;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+      *reinterpret_cast<uint32_t*>(a.out + row * D + k * 64 + lane * 2) =
+          pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    if (lane == 0)
+      a.lse[row] = tot > 0.f ? (mx + log2f(tot)) * 0.69314718055994530942f : -INFINITY;
+  }
+}
+
+template <int D, bool QUAD>
 __global__ void __launch_bounds__(kSpThreads, 2)
 streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k,
@@ -150,7 +201,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
 
   if (warp < 4) {
     // ------------------------------------------------------------- softmax rows
-    const int r = warp * 32 + lane;
+    const int r = QUAD ? lane : warp * 32 + lane;
     const int g = r / a.Qn, qi = r - g * a.Qn, i = t.q0 + qi;
     const bool valid = g < a.G && i < a.N_Q;
     const int last = valid ? sp_last(i, t.nk, a.N_Q, a.causal) : -1;
@@ -160,6 +211,17 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     const uint32_t ts = tmem + lane_off + C::TM_S, to = tmem + lane_off + C::TM_O;
     const float c = a.c;
     float m = -INFINITY, l = 0.f;
+    // O *= f0 (this row). S(n) is complete, so O holds every earlier product.
+    auto rescale = [&](float f0) {
+#pragma unroll
+      for (int k = 0; k < D; k += 32) {
+        uint32_t o[32];
+        tmem_ld_32_wait(to + k, o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+        tmem_st_32(to + k, o);
+      }
+    };
     bool ok = true;
     int n = 0;
     for (;; ++n) {
@@ -191,7 +253,48 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           }
       }
       if (!ok) break;
-      if (warp_live) {
+      if constexpr (QUAD) {
+        // Columns 32 warp .. +31 of the key tile: half of block warp / 2.
+        const int h = warp >> 1;
+        const int lq = h < nb ? min(lim[h] - 32 * (warp & 1), 31) : -1;  // -1 or less: none
+        uint32_t v[32];
+        tmem_ld_32_wait(ts + 32 * warp, v);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          if (k > lq) v[k] = 0xff800000u;  // -inf
+          mx = fmaxf(mx, __uint_as_float(v[k]));
+        }
+        const float ms = mx == -INFINITY ? -INFINITY : mx * c;
+        const bool raise = ms > m + 8.f || (m == -INFINITY && ms > -INFINITY);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f0 = raise ? ex2_approx(m - ms) : 1.f;
+          if (raise) m = ms;
+          l *= f0;
+          if (n > 0) rescale(f0);
+        }
+        const float bias = m == -INFINITY ? 0.f : -m;
+        uint32_t p[16], zero[16];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float e0 = ex2_approx(fmaf(__uint_as_float(v[k]), c, bias));
+          const float e1 = ex2_approx(fmaf(__uint_as_float(v[k + 1]), c, bias));
+          s0 += e0;
+          s1 += e1;
+          p[k >> 1] = pack_bf16x2(e0, e1);
+          zero[k >> 1] = 0u;
+        }
+        l += s0 + s1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q == warp)
+            tmem_st_16(ts + 16 * q, p);
+          else
+            tmem_st_16(ts + 16 * q, zero);
+        }
+        tmem_st_wait();
+      } else if (warp_live) {
         uint32_t v[128];
         tmem_ld_4x32_wait(ts, ts + 32, ts + 64, ts + 96, v);
         // Blocks are read whole or not at all except at the causal diagonal and the
@@ -211,16 +314,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           const float f0 = raise ? ex2_approx(m - ms) : 1.f;  // m = -inf: 0
           if (raise) m = ms;
           l *= f0;
-          if (n > 0) {  // S(n) is complete, so O holds every earlier product
-#pragma unroll
-            for (int k = 0; k < D; k += 32) {
-              uint32_t o[32];
-              tmem_ld_32_wait(to + k, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
-              tmem_st_32(to + k, o);
-            }
-          }
+          if (n > 0) rescale(f0);
         }
         const float bias = m == -INFINITY ? 0.f : -m;
         const float b0 = lim[0] >= 0 ? bias : -INFINITY, b1 = lim[1] >= 0 ? bias : -INFINITY;
@@ -258,20 +352,38 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       *abort_flag = 1;
     }
     tc_fence_after();
-    if (warp_live && ok) {
-      const size_t row = (size_t)(t.h0 + g) * a.N_Q + i;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const bool some = n > 0;  // else O was never written
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float l2 = l > 0.f ? m + log2f(l) : -INFINITY;
+    const bool some = n > 0;  // else O was never written
+    if (QUAD || a.splits > 1) {
+      // The copies and products of this CTA are done; its buffers take the partial rows.
+      if (!mbar_wait(smem_u32(&bars->q_full), 0)) ok = false;
+      const int slot = warp * 32 + lane;
+      bars->l2[slot] = ok && valid ? l2 : -INFINITY;
+      float* dst = reinterpret_cast<float*>(smem) + slot * (D + 4);
 #pragma unroll
       for (int k = 0; k < D; k += 32) {
         uint32_t o[32];
         if (some) tmem_ld_32_wait(to + k, o);
+        if (valid) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          o[e] = some && l > 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-        if (!valid) {
-          // no row to write
-        } else if (a.splits == 1) {
+          for (int e = 0; e < 32; ++e)
+            o[e] = some && l > 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(dst + k + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+    } else if (warp_live && ok) {
+      const size_t row = (size_t)(t.h0 + g) * a.N_Q + i;
+#pragma unroll
+      for (int k = 0; k < D; k += 32) {
+        uint32_t o[32];
+        if (some) tmem_ld_32_wait(to + k, o);
+        if (valid) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = some && l > 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
           uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + k);
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
@@ -282,20 +394,9 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
             w.w = pack_bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
             dst[e >> 3] = w;
           }
-        } else {
-          const size_t rows = (size_t)a.B * a.H * a.N_Q;
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + (split * rows + row) * D + k);
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) dst[e >> 2] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
-      if (valid) {
-        const float l2 = l > 0.f ? m + log2f(l) : -INFINITY;
-        if (a.splits == 1)
-          a.lse[row] = l2 * 0.69314718055994530942f;
-        else
-          a.part_l[split * ((size_t)a.B * a.H * a.N_Q) + row] = l2;
-      }
+      if (valid) a.lse[row] = l2 * 0.69314718055994530942f;
     }
   } else if (warp == 4) {
     // ---------------------------------------------------- producer (whole warp scans)
@@ -304,10 +405,11 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       tma_prefetch_desc(&map_k);
       tma_prefetch_desc(&map_v);
       const uint32_t qb = smem_u32(&bars->q_full);
-      mbar_arrive_expect_tx(qb, a.Qn * a.G * D * 2);
+      mbar_arrive_expect_tx(qb, (QUAD ? 4 : 1) * a.Qn * a.G * D * 2);
       for (int blk = 0; blk < D / 64; ++blk)
-        tma_load_3d(sb + blk * (C::BM * 128), &map_q, qb, blk * 64, t.q0, t.h0,
-                    l2_policy_evict_first());
+        for (int copy = 0; copy < (QUAD ? 4 : 1); ++copy)
+          tma_load_3d(sb + blk * (C::BM * 128) + copy * (32 * 128), &map_q, qb, blk * 64, t.q0,
+                      t.h0, l2_policy_evict_first());
     }
     const uint64_t keep = l2_policy_evict_last();
     bool ok = true;
@@ -362,9 +464,9 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       return ++pend < 2 ? true : push(2);
     };
     if (a.direct) {
-      // One query: its list as a bitmap over the blocks, in the rows of the Q buffer that
-      // the pack's at most 64 rows leave unused.
-      uint32_t* bits = reinterpret_cast<uint32_t*>(smem + 64 * 128);
+      // One query: its list as a bitmap over the blocks, in the rows 16-31 of the Q buffer that
+      // the pack's at most 16 rows leave unused (2 KB: 16384 blocks).
+      uint32_t* bits = reinterpret_cast<uint32_t*>(smem + 16 * 128);
       const int sel = t.b * a.Hsel + t.p / (a.P / a.Hsel);
       const int* idx = a.idx + (size_t)sel * a.topk;
       const int lastkey = sp_last(0, t.nk, 1, a.causal);
@@ -454,37 +556,12 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
-}
-
-// Joins the partial outputs of `splits` CTAs: out = sum_s 2^(l_s - L) o_s with
-// L = log2 sum_s 2^(l_s). One warp per row; each lane holds D / 32 columns.
-template <int D>
-__global__ void __launch_bounds__(128) streamkl_sparse_merge_kernel(const SparseArgs a) {
-  const size_t rows = (size_t)a.B * a.H * a.N_Q;
-  const size_t row = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  float mx = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) mx = fmaxf(mx, __ldg(a.part_l + s * rows + row));
-  float acc[D / 32], tot = 0.f;
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
-  if (mx > -INFINITY) {
-    for (int s = 0; s < a.splits; ++s) {
-      const float w = exp2f(__ldg(a.part_l + s * rows + row) - mx);
-      tot += w;
-      const float* src = a.part_o + (s * rows + row) * D + lane * (D / 32);
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) acc[k] += w * __ldg(src + k);
-    }
-  }
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;
-#pragma unroll
-  for (int k = 0; k < D / 32; k += 2)
-    *reinterpret_cast<uint32_t*>(a.out + row * D + lane * (D / 32) + k) =
-        pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
-  if (lane == 0)
-    a.lse[row] = tot > 0.f ? (mx + log2f(tot)) * 0.69314718055994530942f : -INFINITY;
+  __syncwarp();
+  if (a.splits > 1) cluster_sync();
+  if ((QUAD || a.splits > 1) && warp < 4)
+    sp_join<D, QUAD>(a, t, sb, smem_u32(bars->l2), split, warp, lane);
+  __syncwarp();
+  if (a.splits > 1) cluster_sync();  // another CTA may still be reading this one's rows
 }
 
 }  // namespace skl

@@ -18,15 +18,40 @@ safe to capture into a CUDA graph. The selection has no gradient.
 """
 from __future__ import annotations
 
+import functools
 import math
 from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import StreamKLError, _check, _on_device, _stream_ptr, load_library
+from . import StreamKLError, _check, autograd, load_library
 
 BLOCK = 64  # keys per block
+
+
+def _on_device(fn):
+    """Runs an entry point on the device of its first tensor (made current when it is not) and
+    passes the raw stream: the given one, else the current one. Single-token calls take a few
+    microseconds on the GPU, so nothing here costs more than a lookup."""
+    @functools.wraps(fn)
+    def wrapper(first, *args, stream=None, **kwargs):
+        if not first.is_cuda:
+            raise ValueError(f"{fn.__name__}: tensors must be on a CUDA device")
+        dev = first.device.index
+        if stream is not None and stream.device_index != dev:
+            raise ValueError(f"{fn.__name__}: stream on {stream.device}, tensors on {first.device}")
+        if dev != torch._C._cuda_getDevice():
+            with torch.cuda.device(dev):
+                return fn(first, *args, stream=stream, **kwargs)
+        return fn(first, *args, stream=stream, **kwargs)
+    return wrapper
+
+
+def _stream_ptr(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def num_blocks(n_k: int) -> int:
@@ -34,21 +59,21 @@ def num_blocks(n_k: int) -> int:
     return (int(n_k) + BLOCK - 1) // BLOCK
 
 
-def _bf16(name, t, like=None):
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 4 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous 4-D bf16 CUDA tensor [B, heads, N, d]")
+def _bf16(name, t, dev, like=None):
+    if t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 4 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 4-D bf16 tensor [B, heads, N, d] on {dev}")
     if like is not None and t.shape != like:
         raise ValueError(f"{name} must have shape {tuple(like)}, got {tuple(t.shape)}")
 
 
-def _typed(name, t, dtype, shape):
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+def _typed(name, t, dev, dtype, shape):
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
     return t
 
 
-def _lens(seqlens_k, B):
-    return 0 if seqlens_k is None else _typed("seqlens_k", seqlens_k, torch.int32, (B,)).data_ptr()
+def _lens(seqlens_k, dev, B):
+    return 0 if seqlens_k is None else _typed("seqlens_k", seqlens_k, dev, torch.int32, (B,)).data_ptr()
 
 
 def _workspace(nbytes, device, stream):
@@ -65,8 +90,8 @@ def _workspace(nbytes, device, stream):
 
 
 def _qk_shape(q, k):
-    _bf16("q", q)
-    _bf16("k", k)
+    _bf16("q", q, q.device)
+    _bf16("k", k, q.device)
     B, H, n_q, d = q.shape
     if k.shape[0] != B or k.shape[3] != d:
         raise ValueError("inconsistent shapes of q and k")
@@ -75,11 +100,11 @@ def _qk_shape(q, k):
 
 def _qkv_shape(q, k, v, block_idx):
     B, H, h_kv, n_q, n_k, d = _qk_shape(q, k)
-    _bf16("v", v, k.shape)
+    _bf16("v", v, q.device, k.shape)
     if block_idx.dim() != 4:
         raise ValueError("block_idx must be [B, H_sel, N_Q, topk]")
     h_sel, topk = block_idx.shape[1], block_idx.shape[3]
-    _typed("block_idx", block_idx, torch.int32, (B, h_sel, n_q, topk))
+    _typed("block_idx", block_idx, q.device, torch.int32, (B, h_sel, n_q, topk))
     return B, H, h_kv, h_sel, n_q, n_k, d, topk
 
 
@@ -93,17 +118,17 @@ def streamkl_block_mass(q_s, k_s, scale_S: float, causal: bool, lse_s=None, seql
     if mass is None:
         mass = torch.empty(B, h_kv, n_q, nb, device=q_s.device, dtype=torch.float32)
     else:
-        _typed("mass", mass, torch.float32, (B, h_kv, n_q, nb))
+        _typed("mass", mass, q_s.device, torch.float32, (B, h_kv, n_q, nb))
     nbytes = ws = lse = 0
     keep = None
     if lse_s is None:
         nbytes = 4 * B * H * n_q * nb
         keep, ws = _workspace(nbytes, q_s.device, stream)
     else:
-        lse = _typed("lse_s", lse_s, torch.float32, (B, H, n_q)).data_ptr()
+        lse = _typed("lse_s", lse_s, q_s.device, torch.float32, (B, H, n_q)).data_ptr()
     st = load_library().streamkl_block_mass(
-        q_s.data_ptr(), k_s.data_ptr(), _lens(seqlens_k, B), B, H, h_kv, n_q, n_k, d,
-        float(scale_S), int(bool(causal)), lse, ws, nbytes, mass.data_ptr(), _stream_ptr(stream))
+        q_s.data_ptr(), k_s.data_ptr(), _lens(seqlens_k, q_s.device, B), B, H, h_kv, n_q, n_k, d,
+        float(scale_S), int(bool(causal)), lse, ws, nbytes, mass.data_ptr(), _stream_ptr(stream, q_s.device))
     _check(st, "streamkl_block_mass")
     return mass
 
@@ -115,17 +140,17 @@ def streamkl_block_select(mass, n_k: int, causal: bool, topk: int, n_first: int 
     if mass.dim() != 4:
         raise ValueError("mass must be [B, H_sel, N_Q, NB]")
     B, h_sel, n_q, nb = mass.shape
-    _typed("mass", mass, torch.float32, (B, h_sel, n_q, nb))
+    _typed("mass", mass, mass.device, torch.float32, (B, h_sel, n_q, nb))
     n_k, topk = int(n_k), int(topk)
     if num_blocks(n_k) != nb:
         raise ValueError(f"mass has {nb} blocks, n_k = {n_k} keys make {num_blocks(n_k)}")
     if block_idx is None:
         block_idx = torch.empty(B, h_sel, n_q, max(topk, 0), device=mass.device, dtype=torch.int32)
     else:
-        _typed("block_idx", block_idx, torch.int32, (B, h_sel, n_q, topk))
+        _typed("block_idx", block_idx, mass.device, torch.int32, (B, h_sel, n_q, topk))
     st = load_library().streamkl_block_select(
-        mass.data_ptr(), _lens(seqlens_k, B), B, h_sel, n_q, n_k, int(bool(causal)), topk,
-        int(n_first), int(n_last), block_idx.data_ptr(), _stream_ptr(stream))
+        mass.data_ptr(), _lens(seqlens_k, mass.device, B), B, h_sel, n_q, n_k, int(bool(causal)), topk,
+        int(n_first), int(n_last), block_idx.data_ptr(), _stream_ptr(stream, mass.device))
     _check(st, "streamkl_block_select")
     return block_idx
 
@@ -140,17 +165,17 @@ def streamkl_sparse_attn_fwd(q, k, v, block_idx, scale: float, causal: bool, seq
     if out is None:
         out = torch.empty_like(q)
     else:
-        _bf16("out", out, q.shape)
+        _bf16("out", out, q.device, q.shape)
     if lse is None:
         lse = torch.empty(B, H, n_q, device=q.device, dtype=torch.float32)
     else:
-        _typed("lse", lse, torch.float32, (B, H, n_q))
+        _typed("lse", lse, q.device, torch.float32, (B, H, n_q))
     nbytes = lib.streamkl_sparse_attn_workspace(B, H, h_kv, h_sel, n_q, n_k, d, topk, 0)
     keep, ws = _workspace(max(nbytes, 0), q.device, stream)
     st = lib.streamkl_sparse_attn_fwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), block_idx.data_ptr(), _lens(seqlens_k, B), B, H,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), block_idx.data_ptr(), _lens(seqlens_k, q.device, B), B, H,
         h_kv, h_sel, n_q, n_k, d, topk, float(scale), int(bool(causal)), ws, nbytes,
-        out.data_ptr(), lse.data_ptr(), _stream_ptr(stream))
+        out.data_ptr(), lse.data_ptr(), _stream_ptr(stream, q.device))
     _check(st, "streamkl_sparse_attn_fwd")
     return out, lse
 
@@ -160,15 +185,15 @@ def streamkl_sparse_attn_bwd(q, k, v, out, lse, dout, block_idx, scale: float, c
                              seqlens_k=None, dq=None, dk=None, dv=None, stream=None):
     """dQ, dK, dV (bf16, the shapes of q, k, v) from the forward's out and lse."""
     B, H, h_kv, h_sel, n_q, n_k, d, topk = _qkv_shape(q, k, v, block_idx)
-    _bf16("out", out, q.shape)
-    _bf16("dout", dout, q.shape)
-    _typed("lse", lse, torch.float32, (B, H, n_q))
+    _bf16("out", out, q.device, q.shape)
+    _bf16("dout", dout, q.device, q.shape)
+    _typed("lse", lse, q.device, torch.float32, (B, H, n_q))
     grads = []
     for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if g is None:
             g = torch.empty_like(like)
         else:
-            _bf16(name, g, like.shape)
+            _bf16(name, g, q.device, like.shape)
         grads.append(g)
     dq, dk, dv = grads
     lib = load_library()
@@ -176,11 +201,16 @@ def streamkl_sparse_attn_bwd(q, k, v, out, lse, dout, block_idx, scale: float, c
     keep, ws = _workspace(max(nbytes, 0), q.device, stream)
     st = lib.streamkl_sparse_attn_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
-        block_idx.data_ptr(), _lens(seqlens_k, B), B, H, h_kv, h_sel, n_q, n_k, d, topk,
+        block_idx.data_ptr(), _lens(seqlens_k, q.device, B), B, H, h_kv, h_sel, n_q, n_k, d, topk,
         float(scale), int(bool(causal)), ws, nbytes, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-        _stream_ptr(stream))
+        _stream_ptr(stream, q.device))
     _check(st, "streamkl_sparse_attn_bwd")
     return dq, dk, dv
+
+
+def _after_launch(where, device):
+    if autograd._check_status:
+        autograd._after_launch(where, device)
 
 
 class SparseAttentionFunction(torch.autograd.Function):
@@ -188,20 +218,21 @@ class SparseAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, block_idx, seqlens_k, scale: float, causal: bool):
-        from .autograd import _after_launch
         out, lse = streamkl_sparse_attn_fwd(q, k, v, block_idx, scale, causal, seqlens_k)
         _after_launch("sparse_attention forward", q.device)
         ctx.save_for_backward(q, k, v, out, lse, block_idx, seqlens_k)
         ctx.params = (scale, causal)
         ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)
         return out, lse
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g_out, _g_lse=None):
-        from .autograd import _after_launch
         q, k, v, out, lse, block_idx, seqlens_k = ctx.saved_tensors
         scale, causal = ctx.params
+        if g_out is None:
+            return (None,) * 7
         dout = g_out.to(torch.bfloat16).contiguous()
         dq, dk, dv = streamkl_sparse_attn_bwd(q, k, v, out, lse, dout, block_idx, scale, causal,
                                               seqlens_k)
@@ -210,7 +241,9 @@ class SparseAttentionFunction(torch.autograd.Function):
 
 
 def _lens_arg(seqlens_k):
-    return None if seqlens_k is None else seqlens_k.to(torch.int32).contiguous()
+    if seqlens_k is None or (seqlens_k.dtype == torch.int32 and seqlens_k.is_contiguous()):
+        return seqlens_k
+    return seqlens_k.to(torch.int32).contiguous()
 
 
 def block_mass(q_s, k_s, scale: Optional[float] = None, causal: bool = False, lse=None,
@@ -251,7 +284,6 @@ def sparse_attention(q, k, v, block_idx, scale: Optional[float] = None, causal: 
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         out, lse = SparseAttentionFunction.apply(q, k, v, block_idx, lens, scale, bool(causal))
     else:
-        from .autograd import _after_launch
         out, lse = streamkl_sparse_attn_fwd(q, k, v, block_idx, scale, causal, lens)
         _after_launch("sparse_attention forward", q.device)
     return (out, lse) if return_lse else out

@@ -305,8 +305,7 @@ long long streamkl_sparse_attn_workspace(int B, int H, int H_kv, int H_sel, int 
  * outside 0 .. NB-1 are ignored.
  *   out (bf16 [B,H,N_Q,d]) = softmax over the listed, allowed keys of scale <q, k>, times v
  *   lse (fp32 [B,H,N_Q])   = log-sum-exp of those scores
- * The workspace holds one bit per query, block and selection head, and the partial outputs of
- * lists that are split over several CTAs.
+ * The workspace holds one bit per query, block and selection head (none for single tokens).
  */
 streamkl_status streamkl_sparse_attn_fwd(const void* q, const void* k, const void* v,
                                          const int* block_idx, const int* seqlens_k, int B, int H,

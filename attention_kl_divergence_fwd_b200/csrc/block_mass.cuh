@@ -18,9 +18,11 @@
 // QUAD: tiles of at most 32 rows, four copies, each row warp 32 of a pair's 128 keys (sp_quad);
 // a block's two halves are joined when the staged values are written.
 //
-// Warps: 0-3 rows, 4 TMA producer, 5 MMA + TMEM.
+// Warps: 0-7 rows (warp w: lane quarter w & 3, block w >> 2 of every pair; QUAD: the pairs of
+// parity w >> 2), 8 TMA producer, 9 MMA + TMEM.
 #pragma once
 
+#include "fwd_kernel.cuh"
 #include "sparse_common.cuh"
 
 namespace skl {
@@ -58,7 +60,13 @@ struct MassBars {
 };
 static_assert(sizeof(MassBars) <= 256, "barrier block");
 
-constexpr int kMassThreads = 192;
+constexpr int kMassThreads = 320;
+
+// Exponentials of a block on the FMA pipe, of every 8 pairs of keys (the rest on the
+// exponential unit, which otherwise bounds the kernel).
+#ifndef SKL_MASS_POLY
+#define SKL_MASS_POLY 3
+#endif
 
 // Value of a row over N keys: sum 2^(s c - lse2) (NORM) or log2 sum 2^(s c); keys past lim are
 // left out.
@@ -77,24 +85,39 @@ __device__ __forceinline__ float mass_block(const uint32_t (&v)[N], float c, flo
     if (mx == -INFINITY) return -INFINITY;
     bias = -mx * c;
   }
-  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  float sum;
   if (lim >= N - 1) {
+    const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(bias, bias);
+    uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-    for (int k = 0; k < N; k += 4) {
-      s0 += ex2_approx(fmaf(__uint_as_float(v[k]), c, bias));
-      s1 += ex2_approx(fmaf(__uint_as_float(v[k + 1]), c, bias));
-      s2 += ex2_approx(fmaf(__uint_as_float(v[k + 2]), c, bias));
-      s3 += ex2_approx(fmaf(__uint_as_float(v[k + 3]), c, bias));
+    for (int k = 0; k < N; k += 2) {
+      const uint64_t x =
+          f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, b2);
+      uint64_t e;
+      if (poly_rank((k >> 1) & 7) < SKL_MASS_POLY) {
+        e = exp2_fma2(x);
+      } else {
+        float x0, x1;
+        f2_unpack(x, x0, x1);
+        e = f2_pack(ex2_approx(x0), ex2_approx(x1));
+      }
+      if (k & 2)
+        acc1 = f2_add(acc1, e);
+      else
+        acc0 = f2_add(acc0, e);
     }
+    float s0, s1;
+    f2_unpack(f2_add(acc0, acc1), s0, s1);
+    sum = s0 + s1;
   } else {
+    sum = 0.f;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const float e = ex2_approx(fmaf(__uint_as_float(v[k]), c, bias));
-      s0 += k <= lim ? e : 0.f;
+      sum += k <= lim ? e : 0.f;
     }
   }
-  const float s = (s0 + s1) + (s2 + s3);
-  return NORM ? s : log2f(s) - bias;
+  return NORM ? sum : log2f(sum) - bias;
 }
 
 template <int D, bool NORM, bool QUAD>
@@ -135,13 +158,13 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&bars->s_full[s]), 1);
-      mbar_init(smem_u32(&bars->s_free[s]), 4);
+      mbar_init(smem_u32(&bars->s_free[s]), QUAD ? 4 : 8);
     }
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
     tmem_relinquish();
   }
@@ -150,13 +173,14 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp < 4) {
-    const int r = QUAD ? lane : warp * 32 + lane;
+  if (warp < 8) {
+    const int quarter = warp & 3, wg = warp >> 2;
+    const int r = QUAD ? lane : quarter * 32 + lane;
     const int g = r / a.Qn, qi = r - g * a.Qn, i = q0 + qi;
     const bool valid = g < a.G && i < a.N_Q;
     const int last = valid ? sp_last(i, nk, a.N_Q, a.causal) : -1;
     const bool warp_live = __any_sync(0xffffffffu, valid);
-    const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16);
     const float c = a.c;
     float nl = 0.f;
     bool row_on = valid;
@@ -178,10 +202,10 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
       return m == -INFINITY ? m : m + log2f(exp2f(x - m) + exp2f(y - m));
     };
     auto flush = [&](int cg, int n) {
-      named_bar_sync(1, 128);
+      named_bar_sync(1, 256);
       if (NORM) {
         float* dst = ma.mass + ((size_t)bp * a.N_Q + q0) * a.NB + cg;
-        for (int q = warp; q < nq; q += 4) {
+        for (int q = warp; q < nq; q += 8) {
           float s = 0.f;
           for (int h = 0; h < a.G; ++h) s += staged(h * a.Qn + q);
           if (lane < n) dst[(size_t)q * a.NB + lane] = s * inv_g;
@@ -189,55 +213,54 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
       } else {
         float* dst = ma.blse + ((size_t)h0 * a.N_Q + q0) * a.NB + cg;
         for (int h = 0; h < a.G; ++h)
-          for (int q = warp; q < nq; q += 4)
+          for (int q = warp; q < nq; q += 8)
             if (lane < n) dst[((size_t)h * a.N_Q + q) * a.NB + lane] = staged(h * a.Qn + q);
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(1, 256);
     };
     bool ok = true;
     const int n_blocks = c_end - c_begin;
     for (int s = 0; s < steps; ++s) {
-      // After a wait that ran out the warp still takes part in every named barrier.
-      if (ok && !mbar_wait(smem_u32(&bars->s_full[s & 1]), (s >> 1) & 1)) ok = false;
-      tc_fence_after();
       const int cb = 2 * s;  // first block of the pair, from c_begin
-      if constexpr (QUAD) {
-        // Keys 32 warp .. +31 of the pair: half warp & 1 of block warp / 2.
-        uint32_t v[32];
-        tmem_ld_32_wait(ts + (s & 1) * 128 + 32 * warp, v);
-        const int lim = row_on ? last - (c_begin + cb) * kSpBlock - 32 * warp : (valid ? -1 : 31);
+      if (!QUAD || (s & 1) == wg) {
+        // After a wait that ran out the warp still takes part in every named barrier.
+        if (ok && !mbar_wait(smem_u32(&bars->s_full[s & 1]), (s >> 1) & 1)) ok = false;
+        tc_fence_after();
         float x = NORM ? 0.f : -INFINITY;
-        if (__all_sync(0xffffffffu, lim >= 31)) {
-          x = mass_block<NORM, 32>(v, c, nl, 31);
-        } else if (__any_sync(0xffffffffu, lim >= 0)) {
-          const float y = mass_block<NORM, 32>(v, c, nl, min(lim, 30));
-          const float z = mass_block<NORM, 32>(v, c, nl, 31);
-          x = lim >= 31 ? z : (lim >= 0 ? y : x);
-        }
-        stage[((warp & 1) * 32 + r) * 33 + ((cb + (warp >> 1)) & 31)] = x;
-      } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float x = NORM ? 0.f : -INFINITY;
-        if (warp_live) {
-          uint32_t v[64];
-          tmem_ld_2x32_wait(ts + (s & 1) * 128 + 64 * h, ts + (s & 1) * 128 + 64 * h + 32, v);
-          // Rows past the tile's end take the common path; their values are not written.
-          const int lim = row_on ? last - (c_begin + cb + h) * kSpBlock : (valid ? -1 : 63);
-          if (__all_sync(0xffffffffu, lim >= 63)) {
-            x = mass_block<NORM, 64>(v, c, nl, 63);
+        if constexpr (QUAD) {
+          // Keys 32 quarter .. +31 of the pair: half quarter & 1 of block quarter / 2.
+          uint32_t v[32];
+          tmem_ld_32_wait(ts + (s & 1) * 128 + 32 * quarter, v);
+          const int lim =
+              row_on ? last - (c_begin + cb) * kSpBlock - 32 * quarter : (valid ? -1 : 31);
+          if (__all_sync(0xffffffffu, lim >= 31)) {
+            x = mass_block<NORM, 32>(v, c, nl, 31);
           } else if (__any_sync(0xffffffffu, lim >= 0)) {
-            const float y = mass_block<NORM, 64>(v, c, nl, min(lim, 62));
-            const float z = mass_block<NORM, 64>(v, c, nl, 63);
-            x = lim >= 63 ? z : (lim >= 0 ? y : x);
+            const float y = mass_block<NORM, 32>(v, c, nl, min(lim, 30));
+            const float z = mass_block<NORM, 32>(v, c, nl, 31);
+            x = lim >= 31 ? z : (lim >= 0 ? y : x);
           }
+          stage[((quarter & 1) * 32 + r) * 33 + ((cb + (quarter >> 1)) & 31)] = x;
+        } else {
+          if (warp_live) {
+            uint32_t v[64];
+            tmem_ld_2x32_wait(ts + (s & 1) * 128 + 64 * wg, ts + (s & 1) * 128 + 64 * wg + 32, v);
+            // Rows past the tile's end take the common path; their values are not written.
+            const int lim = row_on ? last - (c_begin + cb + wg) * kSpBlock : (valid ? -1 : 63);
+            if (__all_sync(0xffffffffu, lim >= 63)) {
+              x = mass_block<NORM, 64>(v, c, nl, 63);
+            } else if (__any_sync(0xffffffffu, lim >= 0)) {
+              const float y = mass_block<NORM, 64>(v, c, nl, min(lim, 62));
+              const float z = mass_block<NORM, 64>(v, c, nl, 63);
+              x = lim >= 63 ? z : (lim >= 0 ? y : x);
+            }
+          }
+          stage[r * 33 + ((cb + wg) & 31)] = x;
         }
-        stage[r * 33 + ((cb + h) & 31)] = x;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[s & 1]));
       }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[s & 1]));
       if (((cb + 2) & 31) == 0 || s == steps - 1) {
         const int cg = cb & ~31;
         flush(c_begin + cg, min(cb + 2, n_blocks) - cg);
@@ -250,10 +273,10 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
     if (NORM) {  // blocks that no query of the tile sees
       const int z0 = c_begin + min(2 * steps, n_blocks);
       float* dst = ma.mass + ((size_t)bp * a.N_Q + q0) * a.NB;
-      for (int q = warp; q < nq; q += 4)
+      for (int q = warp; q < nq; q += 8)
         for (int cc = z0 + lane; cc < c_end; cc += 32) dst[(size_t)q * a.NB + cc] = 0.f;
     }
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     if (lane == 0 && steps > 0) {
       tma_prefetch_desc(&map_q);
       tma_prefetch_desc(&map_k);
@@ -312,7 +335,7 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }

@@ -167,7 +167,7 @@ streamkl_status launch_sparse_bwd(const skl::SparseArgs& a, const void* q, const
       a.rows);
   kk<<<(unsigned)((long long)a.B * a.Hkv * a.NB), skl::kSpDkvThreads, CK::SMEM, stream>>>(
       mq, mdo, mk, mv, a, i_s, i_dp, skl::idesc_bf16_f32(128, 64, true, true));
-  kq<<<(unsigned)((long long)a.B * a.P * a.n_tiles), skl::kSpThreads, CQ::SMEM, stream>>>(
+  kq<<<(unsigned)((long long)a.B * a.P * a.n_tiles), skl::kSpDqThreads, CQ::SMEM, stream>>>(
       mq, mdo, mk, mv, a, i_s, i_dp, skl::idesc_bf16_f32(128, D, false, true));
   return ok_launch();
 }

@@ -41,8 +41,10 @@ streamkl_sparse_rows_kernel(const __nv_bfloat16* out, const __nv_bfloat16* dout,
 // ------------------------------------------------------------------ dQ, query-major
 //
 // CTA = one 128-row tile, as in the forward; key tiles are single blocks. Per block:
-// S = Q K^T and dP = dO V^T into TMEM, one thread per row forms dS and writes it over S as
+// S = Q K^T and dP = dO V^T into TMEM, two threads per row form dS and write it over S as
 // bf16, dQ += dS K. 256 TMEM columns and 113 KB: two CTAs per SM.
+// Warps: 0-7 rows (warp w: lane quarter w & 3, keys 32 (w >> 2) .. +31), 8 producer, 9 MMA.
+constexpr int kSpDqThreads = 320;
 template <int D>
 struct SpDqCfg {
   static constexpr int BM = 128;
@@ -75,8 +77,36 @@ struct SpDqBars {
 };
 static_assert(sizeof(SpDqBars) <= 1024, "barrier block");
 
+// dS = p (dP - D), and p itself (BOTH), of 32 keys as bf16 pairs, from scores v[0..31] and
+// dP v[32..63]; keys past lim give 0.
+template <bool BOTH>
+__device__ __forceinline__ void sp_ds(const uint32_t (&v)[64], float c, float nl, float nd,
+                                      int lim, uint32_t (&ds)[16], uint32_t (&pp)[16]) {
+  const uint64_t c2 = f2_pack(c, c), nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+  const bool whole = __all_sync(0xffffffffu, lim >= 31);
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    float x0, x1, d0, d1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, nl2), x0, x1);
+    const uint64_t e = f2_pack(ex2_approx(x0), ex2_approx(x1));
+    const uint64_t t =
+        f2_add(f2_pack(__uint_as_float(v[32 + k]), __uint_as_float(v[33 + k])), nd2);
+    f2_unpack(f2_mul(e, t), d0, d1);
+    float e0, e1;
+    f2_unpack(e, e0, e1);
+    if (!whole) {
+      d0 = k <= lim ? d0 : 0.f;
+      d1 = k + 1 <= lim ? d1 : 0.f;
+      e0 = k <= lim ? e0 : 0.f;
+      e1 = k + 1 <= lim ? e1 : 0.f;
+    }
+    ds[k >> 1] = pack_bf16x2(d0, d1);
+    if (BOTH) pp[k >> 1] = pack_bf16x2(e0, e1);
+  }
+}
+
 template <int D>
-__global__ void __launch_bounds__(kSpThreads, 2)
+__global__ void __launch_bounds__(kSpDqThreads, 2)
 streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
                           const __grid_constant__ CUtensorMap map_do,
                           const __grid_constant__ CUtensorMap map_k,
@@ -106,12 +136,12 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
     mbar_init(smem_u32(&bars->s_full), 1);
-    mbar_init(smem_u32(&bars->ds_full), 4);
+    mbar_init(smem_u32(&bars->ds_full), 8);
     mbar_init(smem_u32(&bars->dq_full), 1);
     bars->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
     tmem_relinquish();
   }
@@ -120,14 +150,15 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp < 4) {
-    const int r = warp * 32 + lane;
+  if (warp < 8) {
+    const int quarter = warp & 3, half = warp >> 2;
+    const int r = quarter * 32 + lane;
     const int g = r / a.Qn, qi = r - g * a.Qn, i = t.q0 + qi;
     const bool valid = g < a.G && i < a.N_Q;
     const int last = valid ? sp_last(i, t.nk, a.N_Q, a.causal) : -1;
     const int wi = qi >> 5, bi = a.Qn >= 32 ? (qi & 31) : t.bit0 + qi;
     const size_t row = (size_t)(t.h0 + g) * a.N_Q + i;
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t ts = tmem + lane_off + C::TM_S, tp = tmem + lane_off + C::TM_DP;
     const uint32_t tq = tmem + lane_off + C::TM_DQ;
     const float2 rv = valid ? __ldg(a.rows + row) : make_float2(0.f, 0.f);
@@ -147,27 +178,15 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
       if (at_end) {  // S is complete: K may lose its rows past nk before dQ += dS K
         uint8_t* kb = smem + C::OFF_K + (n % C::NK) * C::SLOT;
         const int per = (kSpBlock - tail) * 8;
-        for (int e = threadIdx.x; e < per * (D / 64); e += 128)
+        for (int e = threadIdx.x; e < per * (D / 64); e += 256)
           *reinterpret_cast<uint4*>(kb + (e / per) * (64 * 128) + tail * 128 + (e % per) * 16) =
               make_uint4(0u, 0u, 0u, 0u);
         fence_async_smem();
       }
-      uint32_t p[32];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[64];  // 32 scores, 32 dP
-        tmem_ld_2x32_wait(ts + 32 * h, tp + 32 * h, v);
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float d0 = ex2_approx(fmaf(__uint_as_float(v[k]), c, nl)) * (__uint_as_float(v[32 + k]) + nd);
-          float d1 = ex2_approx(fmaf(__uint_as_float(v[k + 1]), c, nl)) *
-                     (__uint_as_float(v[33 + k]) + nd);
-          d0 = 32 * h + k <= lim ? d0 : 0.f;
-          d1 = 32 * h + k + 1 <= lim ? d1 : 0.f;
-          p[16 * h + (k >> 1)] = pack_bf16x2(d0, d1);
-        }
-      }
-      tmem_st_32(ts, p);
+      uint32_t v[64], p[16];  // 32 scores, 32 dP
+      tmem_ld_2x32_wait(ts + 32 * half, tp + 32 * half, v);
+      sp_ds<false>(v, c, nl, nd, lim - 32 * half, p, p);
+      tmem_st_16(ts + 32 * half, p);  // over the scores this thread has read
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -181,7 +200,8 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
     tc_fence_after();
     if (ok) {
 #pragma unroll
-      for (int k = 0; k < D; k += 32) {
+      for (int k0 = 0; k0 < D / 2; k0 += 32) {
+        const int k = half * (D / 2) + k0;
         uint32_t o[32];
         if (n > 0) tmem_ld_32_wait(tq + k, o);
         if (valid) {
@@ -197,7 +217,7 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
         }
       }
     }
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     if (lane == 0) {
       tma_prefetch_desc(&map_q);
       tma_prefetch_desc(&map_do);
@@ -289,7 +309,7 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        umma_bf16_ts(tmem + C::TM_DQ, tmem + C::TM_S + kk * 8,
+        umma_bf16_ts(tmem + C::TM_DQ, tmem + C::TM_S + (kk >> 1) * 32 + (kk & 1) * 8,
                      sdesc_sw128(sk + kk * 2048, 64 * 128, 1024), idesc_dq,
                      (n > 0 || kk > 0) ? 1u : 0u);
       umma_commit(smem_u32(&bars->k_empty[ks]));
@@ -303,7 +323,7 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
@@ -317,8 +337,9 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
 //   dV^T += dO^T P  and  dK^T += Q^T dS   (d on the lanes, keys on the columns).
 // For d = 64 both products take the stacked operand [dO | Q] (128 lanes) and keep the half
 // they need: an M of 64 would run at the same speed.
-// Warps: 0-3 tiles of even steps, 4-7 of odd steps, 8 producer, 9 MMA + TMEM.
-constexpr int kSpDkvThreads = 320;
+// Warps: 0-15 rows (warp w: lane quarter w & 3, steps of parity (w >> 2) & 1, keys 32 (w >> 3)
+// .. +31), 16 producer, 17 MMA + TMEM.
+constexpr int kSpDkvThreads = 576;
 
 template <int D>
 struct SpDkvCfg {
@@ -386,8 +407,8 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(smem_u32(&bars->q_full[s]), 1);
       mbar_init(smem_u32(&bars->q_empty[s]), 1);
       mbar_init(smem_u32(&bars->s_full[s]), 1);
-      mbar_init(smem_u32(&bars->s_free[s]), 4);
-      mbar_init(smem_u32(&bars->ds_full[s]), 4);
+      mbar_init(smem_u32(&bars->s_free[s]), 8);
+      mbar_init(smem_u32(&bars->ds_full[s]), 8);
       mbar_init(smem_u32(&bars->ds_empty[s]), 1);
     }
     for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
@@ -395,7 +416,7 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
     bars->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
     tmem_relinquish();
   }
@@ -413,8 +434,8 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp < 8) {
-    const int wg = warp >> 2, quarter = warp & 3;
+  if (warp < 16) {
+    const int wg = (warp >> 2) & 1, half = warp >> 3, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const int g = r / a.Qn, qi = r - g * a.Qn;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
@@ -439,29 +460,16 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
       const uint32_t ph = (n >> 1) & 1;
       if (!mbar_wait(smem_u32(&bars->s_full[wg]), ph)) { ok = false; break; }
       tc_fence_after();
-      uint32_t p[32], d[32];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[64];
-        tmem_ld_2x32_wait(ts + 32 * h, ts + 64 + 32 * h, v);
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float e0 = ex2_approx(fmaf(__uint_as_float(v[k]), c, nl));
-          float e1 = ex2_approx(fmaf(__uint_as_float(v[k + 1]), c, nl));
-          float d0 = e0 * (__uint_as_float(v[32 + k]) + nd);
-          float d1 = e1 * (__uint_as_float(v[33 + k]) + nd);
-          const bool k0 = 32 * h + k <= lim, k1 = 32 * h + k + 1 <= lim;
-          p[16 * h + (k >> 1)] = pack_bf16x2(k0 ? e0 : 0.f, k1 ? e1 : 0.f);
-          d[16 * h + (k >> 1)] = pack_bf16x2(k0 ? d0 : 0.f, k1 ? d1 : 0.f);
-        }
-      }
+      uint32_t v[64], p[16], d[16];
+      tmem_ld_2x32_wait(ts + 32 * half, ts + 64 + 32 * half, v);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[wg]));
+      sp_ds<true>(v, c, nl, nd, lim - 32 * half, d, p);
       if (!mbar_wait(smem_u32(&bars->ds_empty[wg]), ph ^ 1)) { ok = false; break; }
 #pragma unroll
-      for (int ch = 0; ch < 8; ++ch) {
-        const uint32_t at = prow + ((ch ^ (r & 7)) << 4);
+      for (int ch = 0; ch < 4; ++ch) {
+        const uint32_t at = prow + (((4 * half + ch) ^ (r & 7)) << 4);
         st_shared_v4(at, p[4 * ch], p[4 * ch + 1], p[4 * ch + 2], p[4 * ch + 3]);
         st_shared_v4(at + C::PT, d[4 * ch], d[4 * ch + 1], d[4 * ch + 2], d[4 * ch + 3]);
       }
@@ -475,27 +483,24 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
       *abort_flag = 1;
     }
     tc_fence_after();
-    // Warps 0-3 write dV, warps 4-7 dK: lane = d, columns = keys. For d = 64 dV is on lanes
-    // 0-63 and dK on lanes 64-127 of the stacked products.
+    // Parity 0 writes dV, parity 1 dK, each warp 32 keys: lane = d, columns = keys. For d = 64
+    // dV is on lanes 0-63 and dK on lanes 64-127 of the stacked products.
     const int col = D == 128 ? r : (wg == 0 ? r : r - 64);
     const bool mine = D == 128 || (wg == 0 ? quarter < 2 : quarter >= 2);
     if (ok && mine) {
       const float f = wg == 0 ? 1.f : a.scale;
       __nv_bfloat16* dst = wg == 0 ? a.dv : a.dk;
+      uint32_t v[32];
+      if (n > 0) tmem_ld_32_wait(tmem + lane_off + (wg == 0 ? C::TM_DV : C::TM_DK) + 32 * half, v);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[32];
-        if (n > 0) tmem_ld_32_wait(tmem + lane_off + (wg == 0 ? C::TM_DV : C::TM_DK) + 32 * h, v);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int key = blk0 * kSpBlock + 32 * h + k;
-          if (key < a.N_K)
-            dst[((size_t)kv * a.N_K + key) * D + col] =
-                __float2bfloat16_rn(n > 0 ? __uint_as_float(v[k]) * f : 0.f);
-        }
+      for (int k = 0; k < 32; ++k) {
+        const int key = blk0 * kSpBlock + 32 * half + k;
+        if (key < a.N_K)
+          dst[((size_t)kv * a.N_K + key) * D + col] =
+              __float2bfloat16_rn(n > 0 ? __uint_as_float(v[k]) * f : 0.f);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     const uint64_t keep = l2_policy_evict_last();
     if (lane == 0) {
       tma_prefetch_desc(&map_q);
@@ -638,7 +643,7 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }

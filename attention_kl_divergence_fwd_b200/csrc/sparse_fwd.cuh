@@ -5,10 +5,12 @@
 //
 // CTA = one 128-row tile of packed query heads (sparse_common.cuh). Key tiles are pairs of
 // listed blocks (128 keys, gathered into one buffer by two TMA boxes). Per key tile:
-//   S = Q K^T into TMEM; one thread per row turns its 128 scores into probabilities against
-//   a running reference m (raised, with a rescale of O in TMEM, only when a score exceeds it
-//   by 2^8, so that most tiles leave O alone) and writes them back over the scores as bf16;
-//   O += P V with P read from TMEM.
+//   S = Q K^T into TMEM; two threads per row (one per block of the pair) turn 64 scores each
+//   into probabilities against the row's reference m and write them back over the scores as
+//   bf16; O += P V with P read from TMEM.
+// The two threads share m. They raise it, with a rescale of O in TMEM, only when a score of
+// theirs exceeds it by 2^8, so most tiles leave m and O alone; they exchange their maxima
+// through shared memory every tile and so decide alike. Each thread keeps its own sum.
 // P is rounded to bf16 for the tensor core (relative error at most 2^-8 each, the same as the
 // output's own rounding); the row sums, references and O stay in fp32.
 // A CTA keeps one score buffer: 256 TMEM columns and 97 KB of shared memory, so two CTAs share
@@ -19,14 +21,15 @@
 // QUAD: tiles of at most 32 rows, four copies, each warp a quarter of the keys (sp_quad); the
 // four quarters are joined like splits.
 //
-// Warps: 0-3 softmax (row = TMEM lane), 4 producer (scans the bit matrix, TMA), 5 MMA + TMEM.
+// Warps: 0-7 softmax (warp w: lane quarter w & 3, block w >> 2 of the pair), 8 producer (scans
+// the bit matrix, TMA), 9 MMA + TMEM. QUAD: warps 0-3 only, 32 keys each.
 #pragma once
 
 #include "sparse_common.cuh"
 
 namespace skl {
 
-constexpr int kSpThreads = 192;
+constexpr int kSpThreads = 320;
 
 // One key tile as the producer announces it: how many blocks (0 = end), which, and which of
 // the tile's queries list them.
@@ -45,7 +48,8 @@ struct SpFwdCfg {
   static constexpr int OFF_K = QBYTES;
   static constexpr int OFF_V = OFF_K + NST * KVBYTES;
   static constexpr int OFF_BAR = OFF_V + NST * KVBYTES;
-  static constexpr int SMEM = OFF_BAR + 1024;
+  static constexpr int BAR_BYTES = 3584;
+  static constexpr int SMEM = OFF_BAR + BAR_BYTES;
   static constexpr int TM_S = 0;    // 128 columns of scores, P over the first 64
   static constexpr int TM_O = 128;  // D columns
   static constexpr int TM_COLS = 256;
@@ -57,12 +61,14 @@ struct SpFwdBars {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t info_full[4];
   uint64_t s_full, p_full, o_full;
+  uint64_t pair[4];  // the two warps of a lane quarter
   uint32_t tmem_base;
   int abort_flag;
   SpInfo info[4];
-  float l2[128];  // base-2 log-sum-exps of the partial rows
+  float l2[128];  // row sums, then base-2 log-sum-exps of the partial rows
+  float xch[2][2][128];  // what the two threads of a row exchange: tile parity, thread, row
 };
-static_assert(sizeof(SpFwdBars) <= 1024, "barrier block");
+static_assert(sizeof(SpFwdBars) <= SpFwdCfg<128>::BAR_BYTES, "barrier block");
 
 // Sets the rows past nk of a [D/64][128][64] pair buffer's half to zero: with a padded cache
 // they hold whatever the cache held, and 0 * NaN would reach the products.
@@ -185,12 +191,13 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
     mbar_init(smem_u32(&bars->s_full), 1);
-    mbar_init(smem_u32(&bars->p_full), 4);
+    mbar_init(smem_u32(&bars->p_full), QUAD ? 4 : 8);
     mbar_init(smem_u32(&bars->o_full), 1);
+    for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->pair[s]), 2);
     bars->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
     tmem_relinquish();
   }
@@ -199,27 +206,31 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp < 4) {
+  if (warp < (QUAD ? 4 : 8)) {
     // ------------------------------------------------------------- softmax rows
-    const int r = QUAD ? lane : warp * 32 + lane;
+    const int quarter = warp & 3, half = warp >> 2;
+    const int r = QUAD ? lane : quarter * 32 + lane;
     const int g = r / a.Qn, qi = r - g * a.Qn, i = t.q0 + qi;
     const bool valid = g < a.G && i < a.N_Q;
     const int last = valid ? sp_last(i, t.nk, a.N_Q, a.causal) : -1;
     const int wi = qi >> 5, bi = a.Qn >= 32 ? (qi & 31) : t.bit0 + qi;
     const bool warp_live = __any_sync(0xffffffffu, valid);
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t ts = tmem + lane_off + C::TM_S, to = tmem + lane_off + C::TM_O;
     const float c = a.c;
     float m = -INFINITY, l = 0.f;
-    // O *= f0 (this row). S(n) is complete, so O holds every earlier product.
+    // O *= f0 (this row; the two threads of a row take half of the columns each). S(n) is
+    // complete, so O holds every earlier product.
     auto rescale = [&](float f0) {
+      constexpr int DC = QUAD ? D : D / 2;
 #pragma unroll
-      for (int k = 0; k < D; k += 32) {
-        uint32_t o[32];
-        tmem_ld_32_wait(to + k, o);
+      for (int k = 0; k < DC; k += 8) {  // few registers: the scores are live
+        const uint32_t at = to + (QUAD ? 0 : half * DC) + k;
+        uint32_t o[8];
+        tmem_ld_8_wait(at, o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
-        tmem_st_32(to + k, o);
+        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+        tmem_st_8(at, o);
       }
     };
     bool ok = true;
@@ -229,12 +240,11 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       const SpInfo& f = bars->info[n & 3];
       const int nb = f.nb;
       if (nb == 0) break;
-      int lim[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool on = h < nb && ((f.w[h][wi & 3] >> bi) & 1u);
-        lim[h] = on ? last - f.c[h] * kSpBlock : -1;
-      }
+      // This thread's block of the pair (QUAD: its half of one), and the last key of it that
+      // the row reads.
+      const int hb = QUAD ? quarter >> 1 : half;
+      const bool on = hb < nb && ((f.w[hb][wi & 3] >> bi) & 1u);
+      const int lim = on ? last - f.c[hb] * kSpBlock : -1;
       if (!mbar_wait(smem_u32(&bars->s_full), n & 1)) { ok = false; break; }
       tc_fence_after();
       // A padded cache's last block: rows past nk of V must not reach the product. S(n) is
@@ -247,7 +257,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           if (h < nb && f.c[h] == t.nk / kSpBlock) {
             const int st = n % C::NST;
             if (!mbar_wait(smem_u32(&bars->v_full[st]), (n / C::NST) & 1)) ok = false;
-            sp_zero_tail<D>(smem + C::OFF_V + st * C::KVBYTES, h, tail, threadIdx.x, 128);
+            sp_zero_tail<D>(smem + C::OFF_V + st * C::KVBYTES, h, tail, threadIdx.x, QUAD ? 128 : 256);
             fence_async_smem();
             at_end = true;
           }
@@ -255,8 +265,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       if (!ok) break;
       if constexpr (QUAD) {
         // Columns 32 warp .. +31 of the key tile: half of block warp / 2.
-        const int h = warp >> 1;
-        const int lq = h < nb ? min(lim[h] - 32 * (warp & 1), 31) : -1;  // -1 or less: none
+        const int lq = lim - 32 * (warp & 1);
         uint32_t v[32];
         tmem_ld_32_wait(ts + 32 * warp, v);
         float mx = -INFINITY;
@@ -288,58 +297,72 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         l += s0 + s1;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          const uint32_t at = ts + (q >> 1) * 64 + (q & 1) * 16;
           if (q == warp)
-            tmem_st_16(ts + 16 * q, p);
+            tmem_st_16(at, p);
           else
-            tmem_st_16(ts + 16 * q, zero);
+            tmem_st_16(at, zero);
         }
         tmem_st_wait();
-      } else if (warp_live) {
-        uint32_t v[128];
-        tmem_ld_4x32_wait(ts, ts + 32, ts + 64, ts + 96, v);
-        // Blocks are read whole or not at all except at the causal diagonal and the
-        // sequence's end; only those mask single scores (the end's scores may be NaN).
-        const bool partial = (lim[0] >= 0 && lim[0] < 63) || (lim[1] >= 0 && lim[1] < 63);
-        if (at_end || __any_sync(0xffffffffu, partial)) {
+      } else {
+        uint32_t v[64];
+        float mx = -INFINITY;
+        // A warp without rows, or whose block of the pair is missing, only votes.
+        const bool work = warp_live && hb < nb;
+        if (work) {
+          tmem_ld_2x32_wait(ts + 64 * half, ts + 64 * half + 32, v);
+          // Blocks are read whole or not at all except at the causal diagonal and the
+          // sequence's end; only those mask single scores (the end's scores may be NaN).
+          if (at_end || __any_sync(0xffffffffu, lim >= 0 && lim < 63)) {
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if ((k & 63) > lim[k >> 6]) v[k] = 0xff800000u;  // -inf
+            for (int k = 0; k < 64; ++k)
+              if (k > lim) v[k] = 0xff800000u;  // -inf
+          }
+          mx = fmaxf(max_tree32<false>(v, 0, 31), max_tree32<false>(v, 32, 31));
+          if (lim < 0) mx = -INFINITY;
         }
-        const float mx0 = fmaxf(max_tree32<false>(v, 0, 31), max_tree32<false>(v, 32, 31));
-        const float mx1 = fmaxf(max_tree32<false>(v, 64, 31), max_tree32<false>(v, 96, 31));
-        const float mx = fmaxf(lim[0] >= 0 ? mx0 : -INFINITY, lim[1] >= 0 ? mx1 : -INFINITY);
         const float ms = mx == -INFINITY ? -INFINITY : mx * c;
-        const bool raise = ms > m + 8.f || (m == -INFINITY && ms > -INFINITY);
+        // Exchange with the row's other thread (slots alternate by tile: the other thread has
+        // read tile n - 2's before it arrives for n - 1).
+        bars->xch[n & 1][half][quarter * 32 + lane] = ms;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->pair[quarter]));
+        if (!mbar_wait(smem_u32(&bars->pair[quarter]), n & 1)) { ok = false; break; }
+        const float both = fmaxf(ms, bars->xch[n & 1][half ^ 1][quarter * 32 + lane]);
+        const bool raise = both > m + 8.f || (m == -INFINITY && both > -INFINITY);
         if (__any_sync(0xffffffffu, raise)) {
-          const float f0 = raise ? ex2_approx(m - ms) : 1.f;  // m = -inf: 0
-          if (raise) m = ms;
+          const float f0 = raise ? ex2_approx(m - both) : 1.f;  // m = -inf: 0
+          if (raise) m = both;
           l *= f0;
           if (n > 0) rescale(f0);
         }
-        const float bias = m == -INFINITY ? 0.f : -m;
-        const float b0 = lim[0] >= 0 ? bias : -INFINITY, b1 = lim[1] >= 0 ? bias : -INFINITY;
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        if (work) {
+          const float bias = lim < 0 ? -INFINITY : (m == -INFINITY ? 0.f : -m);
+          const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(bias, bias);
+          uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+          // Over the scores this thread has read, 32 keys at a time.
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (q >= nb) break;  // a single block: the other half holds no scores
-          uint32_t p[32];
-          const float bq = q ? b1 : b0;
+          for (int q = 0; q < 64; q += 32) {
+            uint32_t p[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float e0 = ex2_approx(fmaf(__uint_as_float(v[64 * q + 2 * k]), c, bq));
-            const float e1 = ex2_approx(fmaf(__uint_as_float(v[64 * q + 2 * k + 1]), c, bq));
-            const float e2 = ex2_approx(fmaf(__uint_as_float(v[64 * q + 2 * k + 2]), c, bq));
-            const float e3 = ex2_approx(fmaf(__uint_as_float(v[64 * q + 2 * k + 3]), c, bq));
-            s0 += e0;
-            s1 += e1;
-            s2 += e2;
-            s3 += e3;
-            p[k] = pack_bf16x2(e0, e1);
-            p[k + 1] = pack_bf16x2(e2, e3);
+            for (int k = 0; k < 32; k += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[q + k]), __uint_as_float(v[q + k + 1])), c2,
+                               b2), x0, x1);
+              x0 = ex2_approx(x0);
+              x1 = ex2_approx(x1);
+              if (k & 2)
+                acc1 = f2_add(acc1, f2_pack(x0, x1));
+              else
+                acc0 = f2_add(acc0, f2_pack(x0, x1));
+              p[k >> 1] = pack_bf16x2(x0, x1);
+            }
+            tmem_st_16(ts + 64 * half + q / 2, p);
           }
-          tmem_st_32(ts + 32 * q, p);
+          float s0, s1;
+          f2_unpack(f2_add(acc0, acc1), s0, s1);
+          l += s0 + s1;
         }
-        l += (s0 + s1) + (s2 + s3);
         tmem_st_wait();
       }
       tc_fence_before();
@@ -352,17 +375,30 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       *abort_flag = 1;
     }
     tc_fence_after();
+    if constexpr (!QUAD) {  // the row's sum over both blocks of every pair
+      const int at = quarter * 32 + lane;
+      bars->xch[n & 1][half][at] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->pair[quarter]));
+      if (ok && !mbar_wait(smem_u32(&bars->pair[quarter]), n & 1)) {
+        atomicOr(&g_skl_error, 1u);
+        ok = false;
+      }
+      l = bars->xch[n & 1][0][at] + bars->xch[n & 1][1][at];
+    }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const float l2 = l > 0.f ? m + log2f(l) : -INFINITY;
     const bool some = n > 0;  // else O was never written
+    constexpr int DC = QUAD ? D : D / 2;  // columns this thread writes
     if (QUAD || a.splits > 1) {
       // The copies and products of this CTA are done; its buffers take the partial rows.
       if (!mbar_wait(smem_u32(&bars->q_full), 0)) ok = false;
-      const int slot = warp * 32 + lane;
-      bars->l2[slot] = ok && valid ? l2 : -INFINITY;
+      const int slot = quarter * 32 + lane;
+      if (half == 0) bars->l2[slot] = ok && valid ? l2 : -INFINITY;
       float* dst = reinterpret_cast<float*>(smem) + slot * (D + 4);
 #pragma unroll
-      for (int k = 0; k < D; k += 32) {
+      for (int k0 = 0; k0 < DC; k0 += 32) {
+        const int k = half * DC + k0;
         uint32_t o[32];
         if (some) tmem_ld_32_wait(to + k, o);
         if (valid) {
@@ -377,7 +413,8 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     } else if (warp_live && ok) {
       const size_t row = (size_t)(t.h0 + g) * a.N_Q + i;
 #pragma unroll
-      for (int k = 0; k < D; k += 32) {
+      for (int k0 = 0; k0 < DC; k0 += 32) {
+        const int k = half * DC + k0;
         uint32_t o[32];
         if (some) tmem_ld_32_wait(to + k, o);
         if (valid) {
@@ -396,9 +433,9 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           }
         }
       }
-      if (valid) a.lse[row] = l2 * 0.69314718055994530942f;
+      if (valid && half == 0) a.lse[row] = l2 * 0.69314718055994530942f;
     }
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ---------------------------------------------------- producer (whole warp scans)
     if (lane == 0) {
       tma_prefetch_desc(&map_q);
@@ -436,16 +473,18 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           fine = mbar_wait(smem_u32(&bars->k_empty[st]), ph);
           if (fine) {
             mbar_arrive_expect_tx(kf, nb * 64 * D * 2);
-            for (int h = 0; h < nb; ++h)
-              for (int blk = 0; blk < D / 64; ++blk)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              for (int blk = 0; blk < D / 64 && h < nb; ++blk)
                 tma_load_3d(sb + C::OFF_K + st * C::KVBYTES + blk * (128 * 128) + h * (64 * 128),
                             &map_k, kf, blk * 64, pc[h] * kSpBlock, t.kv, keep);
             fine = mbar_wait(smem_u32(&bars->v_empty[st]), ph);
           }
           if (fine) {
             mbar_arrive_expect_tx(vf, nb * 64 * D * 2);
-            for (int h = 0; h < nb; ++h)
-              for (int blk = 0; blk < D / 64; ++blk)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              for (int blk = 0; blk < D / 64 && h < nb; ++blk)
                 tma_load_3d(sb + C::OFF_V + st * C::KVBYTES + blk * (128 * 128) + h * (64 * 128),
                             &map_v, vf, blk * 64, pc[h] * kSpBlock, t.kv, keep);
           }
@@ -458,10 +497,17 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     };
     auto emit = [&](int c, const uint32_t (&u)[4]) -> bool {
       if (rank++ % a.splits != split) return true;
-      pc[pend] = c;
+      if (pend == 0) {
+        pc[0] = c;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) pw[pend][k] = u[k];
-      return ++pend < 2 ? true : push(2);
+        for (int k = 0; k < 4; ++k) pw[0][k] = u[k];
+        pend = 1;
+        return true;
+      }
+      pc[1] = c;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pw[1][k] = u[k];
+      return push(2);
     };
     if (a.direct) {
       // One query: its list as a bitmap over the blocks, in the rows 16-31 of the Q buffer that
@@ -509,7 +555,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     // With no key tile nothing else waits for the Q copy.
     if (lane == 0 && tiles == 0) mbar_wait(smem_u32(&bars->q_full), 0);
-  } else if (elect_one()) {
+  } else if (warp == 9 && elect_one()) {
     // ------------------------------------------------------------------ MMA issuer
     bool ok = mbar_wait(smem_u32(&bars->q_full), 0);
     for (int n = 0; ok; ++n) {
@@ -536,7 +582,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       tc_fence_after();
       // O += P V: A = P from TMEM, B = V [keys][d] MN-major, 16 keys per step.
       for (int kk = 0; kk < 4 * nb; ++kk)
-        umma_bf16_ts(tmem + C::TM_O, tmem + C::TM_S + kk * 8,
+        umma_bf16_ts(tmem + C::TM_O, tmem + C::TM_S + (kk >> 2) * 64 + (kk & 3) * 8,
                      sdesc_sw128(sv + kk * 2048, 128 * 128, 1024), idesc_o,
                      (n > 0 || kk > 0) ? 1u : 0u);
       umma_commit(smem_u32(&bars->v_empty[st]));
@@ -552,7 +598,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }

@@ -65,7 +65,7 @@ constexpr int kMassThreads = 320;
 // Exponentials of a block on the FMA pipe, of every 8 pairs of keys (the rest on the
 // exponential unit, which otherwise bounds the kernel).
 #ifndef SKL_MASS_POLY
-#define SKL_MASS_POLY 3
+#define SKL_MASS_POLY 2
 #endif
 
 // Value of a row over N keys: sum 2^(s c - lse2) (NORM) or log2 sum 2^(s c); keys past lim are

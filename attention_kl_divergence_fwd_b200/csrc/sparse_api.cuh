@@ -76,15 +76,15 @@ long long mask_bytes(const skl::SparseArgs& a) {
 }
 
 // CTAs of a cluster that share a tile's list: as many as keep the grid within one wave (two CTAs
-// per SM), at most 8 (the portable cluster size), each with at least one pair of blocks. A
+// per SM), at most 8 (the portable cluster size), each with at least one block. A
 // second wave costs more than longer lists: one token of 32 sequences of 8 K heads (256 tiles,
 // 8 pairs each) takes 53 us with 3 CTAs per tile and the figure in sparse_fwd.cuh with one.
 int sparse_splits(const skl::SparseArgs& a) {
   const long long ctas = (long long)a.B * a.P * a.n_tiles;
-  long long pairs = (long long)a.Qn * a.topk;
-  pairs = ((pairs < a.NB ? pairs : a.NB) + 1) / 2;
+  long long blocks = (long long)a.Qn * a.topk;
+  blocks = blocks < a.NB ? blocks : a.NB;
   long long s = 2ll * sm_count() / ctas;
-  if (s > pairs) s = pairs;
+  if (s > blocks) s = blocks;
   return (int)(s < 1 ? 1 : (s > 8 ? 8 : s));
 }
 
@@ -134,7 +134,6 @@ streamkl_status launch_sparse_fwd(const skl::SparseArgs& a, const void* q, const
   cfg.attrs = attr;
   cfg.numAttrs = a.splits > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a,
-                            skl::idesc_bf16_f32(128, 128, false, false, neg),
                             skl::idesc_bf16_f32(128, 64, false, false, neg),
                             skl::idesc_bf16_f32(128, D, false, true)) == cudaSuccess
              ? STREAMKL_OK

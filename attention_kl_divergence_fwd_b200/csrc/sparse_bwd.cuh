@@ -61,11 +61,6 @@ struct SpDqCfg {
   static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
 };
 
-struct SpBlockInfo {
-  int c;  // block, -1 = end
-  uint32_t w[4];
-};
-
 struct SpDqBars {
   uint64_t q_full;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
@@ -279,39 +274,37 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     if (lane == 0 && n == 0) mbar_wait(smem_u32(&bars->q_full), 0);
   } else if (elect_one()) {
+    const uint32_t hi = sdesc_hi(1024);
+    const uint32_t lq = sdesc_lo(sb, 16), ldo = sdesc_lo(sb + C::OFF_DO, 16);
+    const uint32_t lk0 = sdesc_lo(sb + C::OFF_K, 16), lv0 = sdesc_lo(sb + C::OFF_V, 16);
+    const uint32_t lkn0 = sdesc_lo(sb + C::OFF_K, 64 * 128);  // K as [keys][d], MN-major
     bool ok = mbar_wait(smem_u32(&bars->q_full), 0);
     for (int n = 0; ok; ++n) {
       if (!(ok = mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1))) break;
       if (bars->info[n & 3].c < 0) break;
       const int ks = n % C::NK, vs = n % C::NV;
-      const uint32_t sk = sb + C::OFF_K + ks * C::SLOT, sv = sb + C::OFF_V + vs * C::SLOT;
+      const uint32_t lk = lk0 + ks * (C::SLOT >> 4), lv = lv0 + vs * (C::SLOT >> 4);
       if (!(ok = mbar_wait(smem_u32(&bars->k_full[ks]), (n / C::NK) & 1))) break;
       tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t qa = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-        const uint32_t ka = (kk >> 2) * (64 * 128) + (kk & 3) * 32;
-        umma_bf16_ss(tmem + C::TM_S, sdesc_sw128(sb + qa, 16, 1024), sdesc_sw128(sk + ka, 16, 1024),
-                     idesc_s, kk > 0);
-      }
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_bf16_ss_lh(tmem + C::TM_S, lq + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
+                        lk + (((kk >> 2) * (64 * 128) + (kk & 3) * 32) >> 4), hi, idesc_s, kk > 0);
       if (!(ok = mbar_wait(smem_u32(&bars->v_full[vs]), (n / C::NV) & 1))) break;
       tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t qa = C::OFF_DO + (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-        const uint32_t ka = (kk >> 2) * (64 * 128) + (kk & 3) * 32;
-        umma_bf16_ss(tmem + C::TM_DP, sdesc_sw128(sb + qa, 16, 1024),
-                     sdesc_sw128(sv + ka, 16, 1024), idesc_dp, kk > 0);
-      }
-      umma_commit(smem_u32(&bars->v_empty[vs]));
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_bf16_ss_lh(tmem + C::TM_DP, ldo + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
+                        lv + (((kk >> 2) * (64 * 128) + (kk & 3) * 32) >> 4), hi, idesc_dp, kk > 0);
       umma_commit(smem_u32(&bars->s_full));
+      umma_commit(smem_u32(&bars->v_empty[vs]));
       if (!(ok = mbar_wait(smem_u32(&bars->ds_full), n & 1))) break;
       tc_fence_after();
+      const uint32_t lkn = lkn0 + ks * (C::SLOT >> 4);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        umma_bf16_ts(tmem + C::TM_DQ, tmem + C::TM_S + (kk >> 1) * 32 + (kk & 1) * 8,
-                     sdesc_sw128(sk + kk * 2048, 64 * 128, 1024), idesc_dq,
-                     (n > 0 || kk > 0) ? 1u : 0u);
+        umma_bf16_ts_lh(tmem + C::TM_DQ, tmem + C::TM_S + (kk >> 1) * 32 + (kk & 1) * 8,
+                        lkn + kk * (2048 >> 4), hi, idesc_dq, (n > 0 || kk > 0) ? 1u : 0u);
       umma_commit(smem_u32(&bars->k_empty[ks]));
     }
     umma_commit(smem_u32(&bars->dq_full));
@@ -345,13 +338,23 @@ template <int D>
 struct SpDkvCfg {
   static constexpr int SLOT = 64 * D * 2;
   static constexpr int QBYTES = 128 * D * 2;
-  static constexpr int STAGE = 2 * QBYTES;          // {dO, Q}
   static constexpr int PT = 128 * 128;              // bf16 [128 rows][64 keys]
+  // Buffers of Q, dO and {P, dS}. At d = 128 shared memory holds three Q, two dO and one P / dS;
+  // at d = 64 {dO, Q} are stacked operands, adjacent in four stages.
+  static constexpr int NQ = D == 128 ? 3 : 4;
+  static constexpr int ND = D == 128 ? 2 : 4;
+  static constexpr int NP = D == 128 ? 1 : 2;
   static constexpr int OFF_V = SLOT;                // K first
-  static constexpr int OFF_Q = 2 * SLOT;            // two stages
-  static constexpr int OFF_P = OFF_Q + 2 * STAGE;   // two buffers {P, dS}
-  static constexpr int OFF_BAR = OFF_P + 4 * PT;
+  static constexpr int OFF_Q = 2 * SLOT;
+  static constexpr int OFF_P = OFF_Q + (NQ + ND) * QBYTES;
+  static constexpr int OFF_BAR = OFF_P + NP * 2 * PT;
   static constexpr int SMEM = OFF_BAR + 1024;
+  static __device__ __forceinline__ uint32_t off_do(int n) {
+    return OFF_Q + (D == 128 ? (n % ND) * QBYTES : (n % ND) * 2 * QBYTES);
+  }
+  static __device__ __forceinline__ uint32_t off_q(int n) {
+    return OFF_Q + (D == 128 ? (ND + n % NQ) * QBYTES : (n % NQ) * 2 * QBYTES + QBYTES);
+  }
   static constexpr int TM_S = 0;                    // buffer b: S at 128 b, dP at 128 b + 64
   static constexpr int TM_DV = 256, TM_DK = 320, TM_COLS = 512;
   static_assert(SMEM <= 232448, "shared memory budget");
@@ -365,13 +368,13 @@ struct SpTileInfo {
 
 struct SpDkvBars {
   uint64_t k_full;
-  uint64_t q_full[2], q_empty[2];
-  uint64_t info_full[4];
-  uint64_t s_full[2], s_free[2], ds_full[2], ds_empty[2];
+  uint64_t q_full[4], q_empty[4], do_full[4], do_empty[4];
+  uint64_t info_full[8];
+  uint64_t s_full[2], ds_full[2], ds_empty[2];  // ds_empty by P / dS buffer
   uint64_t acc_full;
   uint32_t tmem_base;
   int abort_flag;
-  SpTileInfo info[4];
+  SpTileInfo info[8];
 };
 static_assert(sizeof(SpDkvBars) <= 1024, "barrier block");
 
@@ -403,15 +406,18 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->k_full), 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(smem_u32(&bars->q_full[s]), 1);
       mbar_init(smem_u32(&bars->q_empty[s]), 1);
+      mbar_init(smem_u32(&bars->do_full[s]), 1);
+      mbar_init(smem_u32(&bars->do_empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&bars->s_full[s]), 1);
-      mbar_init(smem_u32(&bars->s_free[s]), 8);
       mbar_init(smem_u32(&bars->ds_full[s]), 8);
       mbar_init(smem_u32(&bars->ds_empty[s]), 1);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
+    for (int s = 0; s < 8; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
     mbar_init(smem_u32(&bars->acc_full), 1);
     bars->abort_flag = 0;
     fence_mbar_init();
@@ -424,7 +430,7 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
   // factor of 0 and must be finite: zero them once.
   if (rows < 128) {
     const int per = (128 - rows) * 8;
-    for (int e = threadIdx.x; e < per * 4 * (D / 64); e += kSpDkvThreads)
+    for (int e = threadIdx.x; e < per * (C::NQ + C::ND) * (D / 64); e += kSpDkvThreads)
       *reinterpret_cast<uint4*>(smem + C::OFF_Q + (e / per) * (128 * 128) + rows * 128 +
                                 (e % per) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
@@ -440,13 +446,13 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
     const int g = r / a.Qn, qi = r - g * a.Qn;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t ts = tmem + lane_off + C::TM_S + 128 * wg;
-    const uint32_t prow = sb + C::OFF_P + wg * 2 * C::PT + r * 128;
+    const uint32_t prow = sb + C::OFF_P + (C::NP == 2 ? wg * 2 * C::PT : 0) + r * 128;
     const float c = a.c;
     bool ok = true;
     int n = 0;
     for (;; ++n) {
-      if (!mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1)) { ok = false; break; }
-      const SpTileInfo& f = bars->info[n & 3];
+      if (!mbar_wait(smem_u32(&bars->info_full[n & 7]), (n >> 3) & 1)) { ok = false; break; }
+      const SpTileInfo& f = bars->info[n & 7];
       if (f.tile < 0) break;
       if ((n & 1) != wg) continue;
       const int i = f.tile * a.Qn + qi;
@@ -462,11 +468,15 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
       tc_fence_after();
       uint32_t v[64], p[16], d[16];
       tmem_ld_2x32_wait(ts + 32 * half, ts + 64 + 32 * half, v);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[wg]));
       sp_ds<true>(v, c, nl, nd, lim - 32 * half, d, p);
-      if (!mbar_wait(smem_u32(&bars->ds_empty[wg]), ph ^ 1)) { ok = false; break; }
+      // The buffer's last products (step n - NP's) have to be complete. With one buffer the other
+      // parity's warps wait on the same barrier; step n - 1's products are at most one phase
+      // ahead, since step n + 1's need this step's P and dS.
+      if (n >= C::NP &&
+          !mbar_wait(smem_u32(&bars->ds_empty[C::NP == 2 ? wg : 0]), ((n / C::NP) - 1) & 1)) {
+        ok = false;
+        break;
+      }
 #pragma unroll
       for (int ch = 0; ch < 4; ++ch) {
         const uint32_t at = prow + (((4 * half + ch) ^ (r & 7)) << 4);
@@ -474,6 +484,7 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
         st_shared_v4(at + C::PT, d[4 * ch], d[4 * ch + 1], d[4 * ch + 2], d[4 * ch + 3]);
       }
       fence_async_smem();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[wg]));
     }
@@ -517,27 +528,31 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
     auto push = [&](int tile, int p, const uint32_t (&u)[4]) -> bool {
       bool fine = true;
       if (lane == 0) {
-        // Entry n & 3 was last read for step n - 4, whose P and dS were written before the
-        // products that freed step n - 2's stage (awaited below before step n - 1 was loaded).
-        SpTileInfo& f = bars->info[n & 3];
+        // Entry n & 7 was last read for step n - 8; loads run at most NQ steps ahead of the
+        // products, which wait for the warps of their step.
+        SpTileInfo& f = bars->info[n & 7];
         f.tile = tile;
         f.p = p;
 #pragma unroll
         for (int k = 0; k < 4; ++k) f.w[k] = u[k];
-        mbar_arrive(smem_u32(&bars->info_full[n & 3]));
+        mbar_arrive(smem_u32(&bars->info_full[n & 7]));
         if (tile >= 0) {
-          const int st = n & 1;
-          fine = mbar_wait(smem_u32(&bars->q_empty[st]), ((n >> 1) & 1) ^ 1);
+          const int sq = n % C::NQ, sd = n % C::ND, head = b * a.H + p * a.G;
+          fine = mbar_wait(smem_u32(&bars->q_empty[sq]), ((n / C::NQ) & 1) ^ 1);
           if (fine) {
-            const uint32_t qf = smem_u32(&bars->q_full[st]);
-            const uint32_t base = sb + C::OFF_Q + st * C::STAGE;
-            mbar_arrive_expect_tx(qf, 2 * rows * D * 2);
-            for (int blk = 0; blk < D / 64; ++blk) {
-              tma_load_3d(base + blk * (128 * 128), &map_do, qf, blk * 64, tile * a.Qn,
-                          b * a.H + p * a.G, keep);
-              tma_load_3d(base + C::QBYTES + blk * (128 * 128), &map_q, qf, blk * 64,
-                          tile * a.Qn, b * a.H + p * a.G, keep);
-            }
+            const uint32_t qf = smem_u32(&bars->q_full[sq]);
+            mbar_arrive_expect_tx(qf, rows * D * 2);
+            for (int blk = 0; blk < D / 64; ++blk)
+              tma_load_3d(sb + C::off_q(n) + blk * (128 * 128), &map_q, qf, blk * 64, tile * a.Qn,
+                          head, keep);
+            fine = mbar_wait(smem_u32(&bars->do_empty[sd]), ((n / C::ND) & 1) ^ 1);
+          }
+          if (fine) {
+            const uint32_t df = smem_u32(&bars->do_full[sd]);
+            mbar_arrive_expect_tx(df, rows * D * 2);
+            for (int blk = 0; blk < D / 64; ++blk)
+              tma_load_3d(sb + C::off_do(n) + blk * (128 * 128), &map_do, df, blk * 64,
+                          tile * a.Qn, head, keep);
           }
         }
       }
@@ -577,63 +592,72 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
     if (!ok && lane == 0) {
       atomicOr(&g_skl_error, 2u);
       *abort_flag = 1;
-      for (int j = max(0, n - 2); j < n; ++j)
-        mbar_wait(smem_u32(&bars->q_full[j & 1]), (j >> 1) & 1);
+      for (int j = max(0, n - C::NQ); j < n; ++j)
+        mbar_wait(smem_u32(&bars->q_full[j % C::NQ]), (j / C::NQ) & 1);
+      for (int j = max(0, n - C::ND); j < n; ++j)
+        mbar_wait(smem_u32(&bars->do_full[j % C::ND]), (j / C::ND) & 1);
     }
   } else if (elect_one()) {
+    const uint32_t hi = sdesc_hi(1024);
+    const uint32_t lk = sdesc_lo(sb, 16), lv = sdesc_lo(sb + C::OFF_V, 16);
+    const uint32_t lp0 = sdesc_lo(sb + C::OFF_P, 128 * 128);
     bool ok = mbar_wait(smem_u32(&bars->k_full), 0);
-    // Scores of step n, when there is one: 1, none left: 0, a wait ran out: -1.
+    // S and dP of step n: 1, no such step: 0, a wait ran out: -1. Score buffer n & 1 was last
+    // read for step n - 2, whose P and dS this thread has seen.
     auto scores = [&](int n) -> int {
-      if (!mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1)) return -1;
-      if (bars->info[n & 3].tile < 0) return 0;
-      const int st = n & 1;
-      const uint32_t ph = (n >> 1) & 1;
-      if (!mbar_wait(smem_u32(&bars->q_full[st]), ph)) return -1;
-      if (!mbar_wait(smem_u32(&bars->s_free[st]), ph ^ 1)) return -1;
+      if (!mbar_wait(smem_u32(&bars->info_full[n & 7]), (n >> 3) & 1)) return -1;
+      if (bars->info[n & 7].tile < 0) return 0;
+      if (!mbar_wait(smem_u32(&bars->q_full[n % C::NQ]), (n / C::NQ) & 1)) return -1;
       tc_fence_after();
-      const uint32_t sdo = sb + C::OFF_Q + st * C::STAGE, sq = sdo + C::QBYTES;
-      const uint32_t ds = tmem + C::TM_S + 128 * st;
+      const uint32_t ds = tmem + C::TM_S + 128 * (n & 1);
+      const uint32_t lq = sdesc_lo(sb + C::off_q(n), 16), ldo = sdesc_lo(sb + C::off_do(n), 16);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t qa = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-        const uint32_t ka = (kk >> 2) * (64 * 128) + (kk & 3) * 32;
-        umma_bf16_ss(ds, sdesc_sw128(sq + qa, 16, 1024), sdesc_sw128(sb + ka, 16, 1024), idesc_s,
-                     kk > 0);
-      }
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_bf16_ss_lh(ds, lq + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
+                        lk + (((kk >> 2) * (64 * 128) + (kk & 3) * 32) >> 4), hi, idesc_s, kk > 0);
+      if (!mbar_wait(smem_u32(&bars->do_full[n % C::ND]), (n / C::ND) & 1)) return -1;
+      tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t qa = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-        const uint32_t ka = C::OFF_V + (kk >> 2) * (64 * 128) + (kk & 3) * 32;
-        umma_bf16_ss(ds + 64, sdesc_sw128(sdo + qa, 16, 1024), sdesc_sw128(sb + ka, 16, 1024),
-                     idesc_dp, kk > 0);
-      }
-      umma_commit(smem_u32(&bars->s_full[st]));
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_bf16_ss_lh(ds + 64, ldo + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
+                        lv + (((kk >> 2) * (64 * 128) + (kk & 3) * 32) >> 4), hi, idesc_dp, kk > 0);
+      umma_commit(smem_u32(&bars->s_full[n & 1]));
       return 1;
     };
-    int more = ok ? scores(0) : 0;
-    for (int n = 0; more > 0; ++n) {
-      more = scores(n + 1);
-      if (more < 0) break;
-      const int st = n & 1;
-      if (!mbar_wait(smem_u32(&bars->ds_full[st]), (n >> 1) & 1)) { more = -1; break; }
+    int ahead = 0;  // steps whose scores have been issued
+    bool more = ok;
+    auto reach = [&](int n) {
+      while (ok && more && ahead <= n) {
+        const int got = scores(ahead);
+        if (got < 0) ok = false;
+        if (got == 0) more = false;
+        if (got > 0) ++ahead;
+      }
+    };
+    reach(1);
+    for (int n = 0; ok && n < ahead; ++n) {
+      if (!(ok = mbar_wait(smem_u32(&bars->ds_full[n & 1]), (n >> 1) & 1))) break;
       tc_fence_after();
-      const uint32_t sdo = sb + C::OFF_Q + st * C::STAGE;
-      const uint32_t sq = D == 128 ? sdo + C::QBYTES : sdo;  // d = 64: stacked [dO | Q]
-      const uint32_t sp = sb + C::OFF_P + st * 2 * C::PT;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)  // 16 rows a step; A and B are both row-contracted
-        umma_bf16_ss(tmem + C::TM_DV, sdesc_sw128(sdo + kk * 2048, 128 * 128, 1024),
-                     sdesc_sw128(sp + kk * 2048, 128 * 128, 1024), idesc_acc,
-                     (n > 0 || kk > 0) ? 1u : 0u);
+      // A = dO (d = 64: the stacked [dO | Q]) and Q, B = P and dS; 16 rows a step, both operands
+      // row-contracted (MN-major).
+      const uint32_t ldo = sdesc_lo(sb + C::off_do(n), 128 * 128);
+      const uint32_t lq = D == 128 ? sdesc_lo(sb + C::off_q(n), 128 * 128) : ldo;
+      const uint32_t lp = lp0 + (C::NP == 2 ? (n & 1) * (2 * C::PT >> 4) : 0);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
-        umma_bf16_ss(tmem + C::TM_DK, sdesc_sw128(sq + kk * 2048, 128 * 128, 1024),
-                     sdesc_sw128(sp + C::PT + kk * 2048, 128 * 128, 1024), idesc_acc,
-                     (n > 0 || kk > 0) ? 1u : 0u);
-      umma_commit(smem_u32(&bars->q_empty[st]));
-      umma_commit(smem_u32(&bars->ds_empty[st]));
+        umma_bf16_ss_lh(tmem + C::TM_DV, ldo + kk * (2048 >> 4), lp + kk * (2048 >> 4), hi,
+                        idesc_acc, (n > 0 || kk > 0) ? 1u : 0u);
+      if (D == 128) umma_commit(smem_u32(&bars->do_empty[n % C::ND]));
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        umma_bf16_ss_lh(tmem + C::TM_DK, lq + kk * (2048 >> 4),
+                        lp + (C::PT >> 4) + kk * (2048 >> 4), hi, idesc_acc,
+                        (n > 0 || kk > 0) ? 1u : 0u);
+      umma_commit(smem_u32(&bars->ds_empty[C::NP == 2 ? n & 1 : 0]));
+      umma_commit(smem_u32(&bars->q_empty[n % C::NQ]));
+      if (D != 128) umma_commit(smem_u32(&bars->do_empty[n % C::ND]));
+      reach(n + 2);
     }
-    if (more < 0) ok = false;
     umma_commit(smem_u32(&bars->acc_full));
     if (!ok) {
       atomicOr(&g_skl_error, 2u);

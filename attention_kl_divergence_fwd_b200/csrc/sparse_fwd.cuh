@@ -3,54 +3,59 @@
 //   out[i] = sum_j p_ij v_j,  p_ij = exp(s_ij - LSE_i),  s_ij = scale <q_i, k_j>,
 //   LSE_i = log sum_j exp(s_ij),  j over the allowed keys of the blocks that i lists.
 //
-// CTA = one 128-row tile of packed query heads (sparse_common.cuh). Key tiles are pairs of
-// listed blocks (128 keys, gathered into one buffer by two TMA boxes). Per key tile:
-//   S = Q K^T into TMEM; two threads per row (one per block of the pair) turn 64 scores each
-//   into probabilities against the row's reference m and write them back over the scores as
-//   bf16; O += P V with P read from TMEM.
-// The two threads share m. They raise it, with a rescale of O in TMEM, only when a score of
-// theirs exceeds it by 2^8, so most tiles leave m and O alone; they exchange their maxima
-// through shared memory every tile and so decide alike. Each thread keeps its own sum.
+// CTA = one 128-row tile of packed query heads (sparse_common.cuh); it walks the blocks of its
+// union. Per block:
+//   S = Q K^T into one of two TMEM score buffers; one thread per row turns its 64 scores into
+//   probabilities against the row's reference m and writes them back over the scores as bf16;
+//   O += P V with P read from TMEM; S of the next but one block follows at once.
+// Two groups of four warps take alternate blocks, so one block's exponentials run under the other
+// block's products and loads. They share m, handed from block to block through shared memory;
+// m rises, with a rescale of O in TMEM, only when a score exceeds it by 2^8, so most blocks leave
+// m and O alone. Each group keeps its own part of the row sum.
 // P is rounded to bf16 for the tensor core (relative error at most 2^-8 each, the same as the
 // output's own rounding); the row sums, references and O stay in fp32.
-// A CTA keeps one score buffer: 256 TMEM columns and 97 KB of shared memory, so two CTAs share
-// an SM and one's MMAs run under the other's exponentials.
+// A CTA takes 256 TMEM columns and about 100 KB of shared memory: two CTAs share an SM, which
+// hides the start and end of one behind the other.
 // `splits` > 1: the tile's list is dealt to the CTAs of a cluster by rank; their normalised
 // outputs and log-sum-exps are joined through distributed shared memory, so that a single
 // token is one launch and no partial result leaves the chip.
-// QUAD: tiles of at most 32 rows, four copies, each warp a quarter of the keys (sp_quad); the
-// four quarters are joined like splits.
+// QUAD: tiles of at most 32 rows, four copies, each warp a quarter of the block's keys (sp_quad);
+// the four quarters are joined like splits.
 //
-// Warps: 0-7 softmax (warp w: lane quarter w & 3, block w >> 2 of the pair), 8 producer (scans
-// the bit matrix, TMA), 9 MMA + TMEM. QUAD: warps 0-3 only, 32 keys each.
+// Warps: 0-7 softmax (warp w: lane quarter w & 3, blocks of parity w >> 2), 8 producer (scans the
+// bit matrix, TMA), 9 MMA + TMEM.
 #pragma once
 
+#include "fwd_kernel.cuh"
 #include "sparse_common.cuh"
 
 namespace skl {
 
 constexpr int kSpThreads = 320;
 
-// One key tile as the producer announces it: how many blocks (0 = end), which, and which of
-// the tile's queries list them.
-struct SpInfo {
-  int nb;
-  int c[2];
-  uint32_t w[2][4];
+// Pairs of every 8 whose exponentials go to the FMA pipe, in blocks that every row reads whole.
+#ifndef SKL_SP_POLY
+#define SKL_SP_POLY 2
+#endif
+
+// One block as the producer announces it: which (-1 = end), and which queries list it.
+struct SpBlockInfo {
+  int c;
+  uint32_t w[4];
 };
 
 template <int D>
 struct SpFwdCfg {
   static constexpr int BM = 128;
   static constexpr int QBYTES = BM * D * 2;
-  static constexpr int KVBYTES = 128 * D * 2;         // one pair of K (or V) blocks
-  static constexpr int NST = D == 128 ? 1 : 2;        // pair buffers each of K and V
+  static constexpr int SLOT = 64 * D * 2;             // one K (or V) block
+  static constexpr int NST = D == 128 ? 2 : 4;        // slots each of K and V
   static constexpr int OFF_K = QBYTES;
-  static constexpr int OFF_V = OFF_K + NST * KVBYTES;
-  static constexpr int OFF_BAR = OFF_V + NST * KVBYTES;
-  static constexpr int BAR_BYTES = 3584;
+  static constexpr int OFF_V = OFF_K + NST * SLOT;
+  static constexpr int OFF_BAR = OFF_V + NST * SLOT;
+  static constexpr int BAR_BYTES = 4352;
   static constexpr int SMEM = OFF_BAR + BAR_BYTES;
-  static constexpr int TM_S = 0;    // 128 columns of scores, P over the first 64
+  static constexpr int TM_S = 0;    // two buffers of 64 columns of scores, P over the first 32
   static constexpr int TM_O = 128;  // D columns
   static constexpr int TM_COLS = 256;
   static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
@@ -58,28 +63,52 @@ struct SpFwdCfg {
 
 struct SpFwdBars {
   uint64_t q_full;
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t info_full[4];
-  uint64_t s_full, p_full, o_full;
-  uint64_t pair[4];  // the two warps of a lane quarter
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t info_full[8];
+  uint64_t s_full[2], p_full[2], o_full;
+  uint64_t m_pass[4][2];  // per lane quarter: the reference after an even / odd block is there
+  uint64_t pair[4];       // the two warps of a lane quarter at the end
   uint32_t tmem_base;
   int abort_flag;
-  SpInfo info[4];
-  float l2[128];  // row sums, then base-2 log-sum-exps of the partial rows
-  float xch[2][2][128];  // what the two threads of a row exchange: tile parity, thread, row
+  SpBlockInfo info[8];
+  float l2[128];       // base-2 log-sum-exps of the partial rows
+  float m[2][128];     // the rows' references after an even / odd block
+  float ml[2][2][128];  // the groups' final references and sums
 };
 static_assert(sizeof(SpFwdBars) <= SpFwdCfg<128>::BAR_BYTES, "barrier block");
 
-// Sets the rows past nk of a [D/64][128][64] pair buffer's half to zero: with a padded cache
-// they hold whatever the cache held, and 0 * NaN would reach the products.
+// Sets the rows from `first` of a [D/64][64][64] block to zero: with a padded cache the rows
+// past nk hold whatever the cache held, and 0 * NaN would reach the products.
 template <int D>
-__device__ __forceinline__ void sp_zero_tail(uint8_t* buf, int half, int first, int tid,
-                                             int nthreads) {
-  const int n = (kSpBlock - first) * 8 * (D / 64);  // 16-byte pieces
-  for (int e = tid; e < n; e += nthreads) {
-    const int blk = e / ((kSpBlock - first) * 8), r = e % ((kSpBlock - first) * 8);
-    *reinterpret_cast<uint4*>(buf + blk * (128 * 128) + (half * 64 + first) * 128 + r * 16) =
+__device__ __forceinline__ void sp_zero_tail(uint8_t* buf, int first, int tid, int nthreads) {
+  const int per = (kSpBlock - first) * 8;  // 16-byte pieces
+  for (int e = tid; e < per * (D / 64); e += nthreads)
+    *reinterpret_cast<uint4*>(buf + (e / per) * (64 * 128) + first * 128 + (e % per) * 16) =
         make_uint4(0u, 0u, 0u, 0u);
+}
+
+// 2^(v c + bias) of 32 scores as bf16 pairs, and their sum (two packed partial sums). POLY: a share
+// on the FMA pipe, for arguments known to be finite.
+template <bool POLY, int N>
+__device__ __forceinline__ void sp_exp32(const uint32_t (&v)[N], int at, uint64_t c2, uint64_t b2,
+                                         uint64_t& acc0, uint64_t& acc1, uint32_t (&p)[16]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    const uint64_t x =
+        f2_fma(f2_pack(__uint_as_float(v[at + k]), __uint_as_float(v[at + k + 1])), c2, b2);
+    float x0, x1;
+    if (POLY && poly_rank((k >> 1) & 7) < SKL_SP_POLY) {
+      f2_unpack(exp2_fma2(x), x0, x1);
+    } else {
+      f2_unpack(x, x0, x1);
+      x0 = ex2_approx(x0);
+      x1 = ex2_approx(x1);
+    }
+    if (k & 2)
+      acc1 = f2_add(acc1, f2_pack(x0, x1));
+    else
+      acc0 = f2_add(acc0, f2_pack(x0, x1));
+    p[k >> 1] = pack_bf16x2(x0, x1);
   }
 }
 
@@ -118,7 +147,7 @@ __device__ __forceinline__ void sp_join(const SparseArgs& a, const SpTile& t, ui
                                         uint32_t l2, int split, int warp, int lane) {
   constexpr int NS = QUAD ? 4 : 1;
   const int rows = a.Qn * a.G;
-  for (int r = split + warp * a.splits; r < rows; r += 4 * a.splits) {
+  for (int r = split + warp * a.splits; r < rows; r += 8 * a.splits) {
     const int g = r / a.Qn, i = t.q0 + r - g * a.Qn;
     if (i >= a.N_Q) continue;
     const int srcs = a.splits * NS;
@@ -161,9 +190,9 @@ __global__ void __launch_bounds__(kSpThreads, 2)
 streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k,
                            const __grid_constant__ CUtensorMap map_v, const SparseArgs a,
-                           const uint32_t idesc_s2, const uint32_t idesc_s1,
-                           const uint32_t idesc_o) {
+                           const uint32_t idesc_s, const uint32_t idesc_o) {
   using C = SpFwdCfg<D>;
+  constexpr int NST = C::NST;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   if (sb & 1023u) {
@@ -183,17 +212,21 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->q_full), 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(smem_u32(&bars->k_full[s]), 1);
       mbar_init(smem_u32(&bars->k_empty[s]), 1);
       mbar_init(smem_u32(&bars->v_full[s]), 1);
       mbar_init(smem_u32(&bars->v_empty[s]), 1);
+      mbar_init(smem_u32(&bars->m_pass[s][0]), 1);
+      mbar_init(smem_u32(&bars->m_pass[s][1]), 1);
+      mbar_init(smem_u32(&bars->pair[s]), 2);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
-    mbar_init(smem_u32(&bars->s_full), 1);
-    mbar_init(smem_u32(&bars->p_full), QUAD ? 4 : 8);
+    for (int s = 0; s < 8; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&bars->s_full[s]), 1);
+      mbar_init(smem_u32(&bars->p_full[s]), 4);
+    }
     mbar_init(smem_u32(&bars->o_full), 1);
-    for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->pair[s]), 2);
     bars->abort_flag = 0;
     fence_mbar_init();
   }
@@ -206,221 +239,192 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp < (QUAD ? 4 : 8)) {
+  if (warp < 8) {
     // ------------------------------------------------------------- softmax rows
-    const int quarter = warp & 3, half = warp >> 2;
-    const int r = QUAD ? lane : quarter * 32 + lane;
+    const int quarter = warp & 3, grp = warp >> 2;
+    const int r = QUAD ? lane : quarter * 32 + lane, slot = quarter * 32 + lane;
     const int g = r / a.Qn, qi = r - g * a.Qn, i = t.q0 + qi;
     const bool valid = g < a.G && i < a.N_Q;
     const int last = valid ? sp_last(i, t.nk, a.N_Q, a.causal) : -1;
-    const int wi = qi >> 5, bi = a.Qn >= 32 ? (qi & 31) : t.bit0 + qi;
-    const bool warp_live = __any_sync(0xffffffffu, valid);
+    const int wi = (qi >> 5) & 3, bi = a.Qn >= 32 ? (qi & 31) : t.bit0 + qi;
+    const bool live = __any_sync(0xffffffffu, valid);
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t ts = tmem + lane_off + C::TM_S, to = tmem + lane_off + C::TM_O;
+    const uint32_t ts = tmem + lane_off + C::TM_S + 64 * grp, to = tmem + lane_off + C::TM_O;
     const float c = a.c;
+    // Block that holds the end of a padded sequence (rows of it past nk are not keys), or none.
+    const int c_end = (t.nk & (kSpBlock - 1)) != 0 && t.nk < a.N_K ? t.nk / kSpBlock : -1;
     float m = -INFINITY, l = 0.f;
-    // O *= f0 (this row; the two threads of a row take half of the columns each). S(n) is
-    // complete, so O holds every earlier product.
-    auto rescale = [&](float f0) {
-      constexpr int DC = QUAD ? D : D / 2;
-#pragma unroll
-      for (int k = 0; k < DC; k += 8) {  // few registers: the scores are live
-        const uint32_t at = to + (QUAD ? 0 : half * DC) + k;
-        uint32_t o[8];
-        tmem_ld_8_wait(at, o);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
-        tmem_st_8(at, o);
-      }
-    };
     bool ok = true;
     int n = 0;
     for (;; ++n) {
-      if (!mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1)) { ok = false; break; }
-      const SpInfo& f = bars->info[n & 3];
-      const int nb = f.nb;
-      if (nb == 0) break;
-      // This thread's block of the pair (QUAD: its half of one), and the last key of it that
-      // the row reads.
-      const int hb = QUAD ? quarter >> 1 : half;
-      const bool on = hb < nb && ((f.w[hb][wi & 3] >> bi) & 1u);
-      const int lim = on ? last - f.c[hb] * kSpBlock : -1;
-      if (!mbar_wait(smem_u32(&bars->s_full), n & 1)) { ok = false; break; }
+      if (!mbar_wait(smem_u32(&bars->info_full[n & 7]), (n >> 3) & 1)) { ok = false; break; }
+      const SpBlockInfo& f = bars->info[n & 7];
+      const int blk = f.c;
+      if (blk < 0) break;
+      if ((n & 1) != grp) continue;
+      // Last key of the block that this row reads, -1 or less for none.
+      const int lim = (f.w[wi] >> bi) & 1u ? last - blk * kSpBlock : -1;
+      if (!mbar_wait(smem_u32(&bars->s_full[grp]), (n >> 1) & 1)) { ok = false; break; }
       tc_fence_after();
-      // A padded cache's last block: rows past nk of V must not reach the product. S(n) is
-      // complete, so the products before it are too and v_full is in this tile's phase.
-      const int tail = t.nk & (kSpBlock - 1);
-      bool at_end = false;
-      if (tail != 0 && t.nk < a.N_K) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (h < nb && f.c[h] == t.nk / kSpBlock) {
-            const int st = n % C::NST;
-            if (!mbar_wait(smem_u32(&bars->v_full[st]), (n / C::NST) & 1)) ok = false;
-            sp_zero_tail<D>(smem + C::OFF_V + st * C::KVBYTES, h, tail, threadIdx.x, QUAD ? 128 : 256);
-            fence_async_smem();
-            at_end = true;
-          }
+      const bool at_end = blk == c_end;
+      if (at_end) {
+        // V's product with this block waits for p_full below, and its copy is the next phase of
+        // v_full: the product of block n - NST, which freed the slot, is complete (S(n) is,
+        // and products complete in order).
+        if (!mbar_wait(smem_u32(&bars->v_full[n % NST]), (n / NST) & 1)) { ok = false; break; }
+        sp_zero_tail<D>(smem + C::OFF_V + (n % NST) * C::SLOT, t.nk & (kSpBlock - 1),
+                        threadIdx.x & 127, 128);
+        fence_async_smem();
       }
-      if (!ok) break;
+      constexpr int NC = QUAD ? 16 : 64;  // score columns of this thread
+      uint32_t v[NC];
+      float mx = -INFINITY;
       if constexpr (QUAD) {
-        // Columns 32 warp .. +31 of the key tile: half of block warp / 2.
-        const int lq = lim - 32 * (warp & 1);
-        uint32_t v[32];
-        tmem_ld_32_wait(ts + 32 * warp, v);
-        float mx = -INFINITY;
+        tmem_ld_16_wait(ts + 16 * quarter, v);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          if (k > lq) v[k] = 0xff800000u;  // -inf
+        for (int k = 0; k < 16; ++k) {
+          if (16 * quarter + k > lim) v[k] = 0xff800000u;  // -inf
           mx = fmaxf(mx, __uint_as_float(v[k]));
         }
-        const float ms = mx == -INFINITY ? -INFINITY : mx * c;
-        const bool raise = ms > m + 8.f || (m == -INFINITY && ms > -INFINITY);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float f0 = raise ? ex2_approx(m - ms) : 1.f;
-          if (raise) m = ms;
-          l *= f0;
-          if (n > 0) rescale(f0);
-        }
-        const float bias = m == -INFINITY ? 0.f : -m;
-        uint32_t p[16], zero[16];
-        float s0 = 0.f, s1 = 0.f;
+      } else if (live) {
+        tmem_ld_2x32_wait(ts, ts + 32, v);
+        // Blocks are read whole or not at all except at the causal diagonal and the
+        // sequence's end; only those mask single scores (the end's scores may be NaN).
+        if (at_end || __any_sync(0xffffffffu, lim >= 0 && lim < 63)) {
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          const float e0 = ex2_approx(fmaf(__uint_as_float(v[k]), c, bias));
-          const float e1 = ex2_approx(fmaf(__uint_as_float(v[k + 1]), c, bias));
-          s0 += e0;
-          s1 += e1;
-          p[k >> 1] = pack_bf16x2(e0, e1);
+          for (int k = 0; k < 64; ++k)
+            if (k > lim) v[k] = 0xff800000u;  // -inf
+        }
+        mx = fmaxf(max_tree32<false>(v, 0, 31), max_tree32<false>(v, 32, 31));
+        if (lim < 0) mx = -INFINITY;
+      }
+      const float ms = mx == -INFINITY ? -INFINITY : mx * c;
+      // The reference after block n - 1, from the other group; slots alternate by block, and a
+      // slot's next value needs one from the other group in between.
+      float m0 = -INFINITY;
+      if (n > 0) {
+        if (!mbar_wait(smem_u32(&bars->m_pass[quarter][(n - 1) & 1]), ((n - 1) >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        m0 = bars->m[(n - 1) & 1][slot];
+      }
+      const bool raise = ms > m0 + 8.f || (m0 == -INFINITY && ms > -INFINITY);
+      const float m1 = raise ? ms : m0;
+      bars->m[n & 1][slot] = m1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->m_pass[quarter][n & 1]));
+      if (m1 != m) {
+        l *= ex2_approx(m - m1);  // m = -inf: l = 0
+        m = m1;
+      }
+      if (n > 0 && __any_sync(0xffffffffu, raise)) {
+        // O *= 2^(m0 - m1) once it holds every product before this block's.
+        if (!mbar_wait(smem_u32(&bars->v_empty[(n - 1) % NST]), ((n - 1) / NST) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float f0 = raise ? ex2_approx(m0 - m1) : 1.f;  // m0 = -inf: 0
+#pragma unroll
+        for (int k = 0; k < D; k += 8) {  // few registers: the scores are live
+          uint32_t o[8];
+          tmem_ld_8_wait(to + k, o);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+          tmem_st_8(to + k, o);
+        }
+      }
+      uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+      const float bias = lim < 0 ? -INFINITY : (m == -INFINITY ? 0.f : -m);
+      const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(bias, bias);
+      if constexpr (QUAD) {
+        uint32_t p[8], zero[8];
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          float x0, x1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, b2), x0,
+                    x1);
+          x0 = ex2_approx(x0);
+          x1 = ex2_approx(x1);
+          acc0 = f2_add(acc0, f2_pack(x0, x1));
+          p[k >> 1] = pack_bf16x2(x0, x1);
           zero[k >> 1] = 0u;
         }
-        l += s0 + s1;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const uint32_t at = ts + (q >> 1) * 64 + (q & 1) * 16;
-          if (q == warp)
-            tmem_st_16(at, p);
+          if (q == quarter)
+            tmem_st_8(ts + 8 * q, p);
           else
-            tmem_st_16(at, zero);
+            tmem_st_8(ts + 8 * q, zero);
         }
-        tmem_st_wait();
-      } else {
-        uint32_t v[64];
-        float mx = -INFINITY;
-        // A warp without rows, or whose block of the pair is missing, only votes.
-        const bool work = warp_live && hb < nb;
-        if (work) {
-          tmem_ld_2x32_wait(ts + 64 * half, ts + 64 * half + 32, v);
-          // Blocks are read whole or not at all except at the causal diagonal and the
-          // sequence's end; only those mask single scores (the end's scores may be NaN).
-          if (at_end || __any_sync(0xffffffffu, lim >= 0 && lim < 63)) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-              if (k > lim) v[k] = 0xff800000u;  // -inf
-          }
-          mx = fmaxf(max_tree32<false>(v, 0, 31), max_tree32<false>(v, 32, 31));
-          if (lim < 0) mx = -INFINITY;
+      } else if (live) {
+        // P goes over the scores this thread has read.
+        uint32_t p[16];
+        if (__all_sync(0xffffffffu, lim >= 63)) {
+          sp_exp32<true>(v, 0, c2, b2, acc0, acc1, p);
+          tmem_st_16(ts, p);
+          sp_exp32<true>(v, 32, c2, b2, acc0, acc1, p);
+          tmem_st_16(ts + 16, p);
+        } else {
+          sp_exp32<false>(v, 0, c2, b2, acc0, acc1, p);
+          tmem_st_16(ts, p);
+          sp_exp32<false>(v, 32, c2, b2, acc0, acc1, p);
+          tmem_st_16(ts + 16, p);
         }
-        const float ms = mx == -INFINITY ? -INFINITY : mx * c;
-        // Exchange with the row's other thread (slots alternate by tile: the other thread has
-        // read tile n - 2's before it arrives for n - 1).
-        bars->xch[n & 1][half][quarter * 32 + lane] = ms;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->pair[quarter]));
-        if (!mbar_wait(smem_u32(&bars->pair[quarter]), n & 1)) { ok = false; break; }
-        const float both = fmaxf(ms, bars->xch[n & 1][half ^ 1][quarter * 32 + lane]);
-        const bool raise = both > m + 8.f || (m == -INFINITY && both > -INFINITY);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float f0 = raise ? ex2_approx(m - both) : 1.f;  // m = -inf: 0
-          if (raise) m = both;
-          l *= f0;
-          if (n > 0) rescale(f0);
-        }
-        if (work) {
-          const float bias = lim < 0 ? -INFINITY : (m == -INFINITY ? 0.f : -m);
-          const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(bias, bias);
-          uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
-          // Over the scores this thread has read, 32 keys at a time.
-#pragma unroll
-          for (int q = 0; q < 64; q += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[q + k]), __uint_as_float(v[q + k + 1])), c2,
-                               b2), x0, x1);
-              x0 = ex2_approx(x0);
-              x1 = ex2_approx(x1);
-              if (k & 2)
-                acc1 = f2_add(acc1, f2_pack(x0, x1));
-              else
-                acc0 = f2_add(acc0, f2_pack(x0, x1));
-              p[k >> 1] = pack_bf16x2(x0, x1);
-            }
-            tmem_st_16(ts + 64 * half + q / 2, p);
-          }
-          float s0, s1;
-          f2_unpack(f2_add(acc0, acc1), s0, s1);
-          l += s0 + s1;
-        }
-        tmem_st_wait();
       }
+      float s0, s1;
+      f2_unpack(f2_add(acc0, acc1), s0, s1);
+      l += s0 + s1;
+      tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
+      if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[grp]));
     }
     if (ok && !mbar_wait(smem_u32(&bars->o_full), 0)) ok = false;
+    tc_fence_after();
+    // The two groups' sums, at the later of their references.
+    bars->ml[grp][0][slot] = m;
+    bars->ml[grp][1][slot] = l;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->pair[quarter]));
+    if (ok && !mbar_wait(smem_u32(&bars->pair[quarter]), 0)) ok = false;
     if (!ok) {
       atomicOr(&g_skl_error, 1u);
       *abort_flag = 1;
     }
-    tc_fence_after();
-    if constexpr (!QUAD) {  // the row's sum over both blocks of every pair
-      const int at = quarter * 32 + lane;
-      bars->xch[n & 1][half][at] = l;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->pair[quarter]));
-      if (ok && !mbar_wait(smem_u32(&bars->pair[quarter]), n & 1)) {
-        atomicOr(&g_skl_error, 1u);
-        ok = false;
-      }
-      l = bars->xch[n & 1][0][at] + bars->xch[n & 1][1][at];
+    {
+      const float ma = bars->ml[0][0][slot], mb = bars->ml[1][0][slot];
+      m = fmaxf(ma, mb);
+      l = 0.f;
+      if (ma > -INFINITY) l = bars->ml[0][1][slot] * ex2_approx(ma - m);
+      if (mb > -INFINITY) l += bars->ml[1][1][slot] * ex2_approx(mb - m);
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const float l2 = l > 0.f ? m + log2f(l) : -INFINITY;
     const bool some = n > 0;  // else O was never written
-    constexpr int DC = QUAD ? D : D / 2;  // columns this thread writes
-    if (QUAD || a.splits > 1) {
-      // The copies and products of this CTA are done; its buffers take the partial rows.
-      if (!mbar_wait(smem_u32(&bars->q_full), 0)) ok = false;
-      const int slot = quarter * 32 + lane;
-      if (half == 0) bars->l2[slot] = ok && valid ? l2 : -INFINITY;
-      float* dst = reinterpret_cast<float*>(smem) + slot * (D + 4);
+    const bool parts = QUAD || a.splits > 1;
+    // The copies and products of this CTA are done; its buffers take the partial rows.
+    if (parts && !mbar_wait(smem_u32(&bars->q_full), 0)) ok = false;
+    if (parts && grp == 0) bars->l2[slot] = ok && valid ? l2 : -INFINITY;
+    const size_t row = (size_t)(t.h0 + g) * a.N_Q + i;
+    if (live && ok) {
 #pragma unroll
-      for (int k0 = 0; k0 < DC; k0 += 32) {
-        const int k = half * DC + k0;
+      for (int k0 = 0; k0 < D / 2; k0 += 32) {  // half of the columns per group
+        const int k = grp * (D / 2) + k0;
         uint32_t o[32];
         if (some) tmem_ld_32_wait(to + k, o);
-        if (valid) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = some && l > 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+        for (int e = 0; e < 32; ++e)
+          o[e] = some && l > 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+        if (!valid) {
+          // no row to write
+        } else if (parts) {
+          float* dst = reinterpret_cast<float*>(smem) + slot * (D + 4) + k;
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(dst + k + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
-      }
-    } else if (warp_live && ok) {
-      const size_t row = (size_t)(t.h0 + g) * a.N_Q + i;
-#pragma unroll
-      for (int k0 = 0; k0 < DC; k0 += 32) {
-        const int k = half * DC + k0;
-        uint32_t o[32];
-        if (some) tmem_ld_32_wait(to + k, o);
-        if (valid) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = some && l > 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+            *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else {
           uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + k);
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
@@ -433,7 +437,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           }
         }
       }
-      if (valid && half == 0) a.lse[row] = l2 * 0.69314718055994530942f;
+      if (!parts && valid && grp == 0) a.lse[row] = l2 * 0.69314718055994530942f;
     }
   } else if (warp == 8) {
     // ---------------------------------------------------- producer (whole warp scans)
@@ -450,64 +454,42 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     const uint64_t keep = l2_policy_evict_last();
     bool ok = true;
-    int n = 0, rank = 0, pend = 0;
-    int pc[2] = {0, 0};
-    uint32_t pw[2][4] = {};
-    // Announces the pending blocks as key tile n and loads them (nb = 0: the end).
-    auto push = [&](int nb) -> bool {
+    int n = 0, rank = 0;
+    // Announces block c as step n and loads it (-1: the end).
+    auto push = [&](int c, const uint32_t (&u)[4]) -> bool {
+      if (c >= 0 && a.splits > 1 && rank++ % a.splits != split) return true;
       bool fine = true;
       if (lane == 0) {
-        SpInfo& f = bars->info[n & 3];
-        f.nb = nb;
+        // Entry n & 7 was last read for step n - 8: loads run at most NST + 2 steps ahead of
+        // the products, which wait for every softmax warp.
+        SpBlockInfo& f = bars->info[n & 7];
+        f.c = c;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          f.c[h] = pc[h];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) f.w[h][k] = pw[h][k];
-        }
-        mbar_arrive(smem_u32(&bars->info_full[n & 3]));
-        if (nb > 0) {
-          const int st = n % C::NST;
-          const uint32_t ph = ((n / C::NST) & 1) ^ 1;
+        for (int k = 0; k < 4; ++k) f.w[k] = u[k];
+        mbar_arrive(smem_u32(&bars->info_full[n & 7]));
+        if (c >= 0) {
+          const int st = n % NST;
+          const uint32_t ph = ((n / NST) & 1) ^ 1;
           const uint32_t kf = smem_u32(&bars->k_full[st]), vf = smem_u32(&bars->v_full[st]);
           fine = mbar_wait(smem_u32(&bars->k_empty[st]), ph);
           if (fine) {
-            mbar_arrive_expect_tx(kf, nb * 64 * D * 2);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              for (int blk = 0; blk < D / 64 && h < nb; ++blk)
-                tma_load_3d(sb + C::OFF_K + st * C::KVBYTES + blk * (128 * 128) + h * (64 * 128),
-                            &map_k, kf, blk * 64, pc[h] * kSpBlock, t.kv, keep);
+            mbar_arrive_expect_tx(kf, C::SLOT);
+            for (int blk = 0; blk < D / 64; ++blk)
+              tma_load_3d(sb + C::OFF_K + st * C::SLOT + blk * (64 * 128), &map_k, kf, blk * 64,
+                          c * kSpBlock, t.kv, keep);
             fine = mbar_wait(smem_u32(&bars->v_empty[st]), ph);
           }
           if (fine) {
-            mbar_arrive_expect_tx(vf, nb * 64 * D * 2);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              for (int blk = 0; blk < D / 64 && h < nb; ++blk)
-                tma_load_3d(sb + C::OFF_V + st * C::KVBYTES + blk * (128 * 128) + h * (64 * 128),
-                            &map_v, vf, blk * 64, pc[h] * kSpBlock, t.kv, keep);
+            mbar_arrive_expect_tx(vf, C::SLOT);
+            for (int blk = 0; blk < D / 64; ++blk)
+              tma_load_3d(sb + C::OFF_V + st * C::SLOT + blk * (64 * 128), &map_v, vf, blk * 64,
+                          c * kSpBlock, t.kv, keep);
           }
         }
       }
       fine = __shfl_sync(0xffffffffu, fine ? 1 : 0, 0) != 0;
-      ++n;
-      pend = 0;
+      if (c >= 0) ++n;
       return fine;
-    };
-    auto emit = [&](int c, const uint32_t (&u)[4]) -> bool {
-      if (rank++ % a.splits != split) return true;
-      if (pend == 0) {
-        pc[0] = c;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) pw[0][k] = u[k];
-        pend = 1;
-        return true;
-      }
-      pc[1] = c;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) pw[1][k] = u[k];
-      return push(2);
     };
     if (a.direct) {
       // One query: its list as a bitmap over the blocks, in the rows 16-31 of the Q buffer that
@@ -532,60 +514,77 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           lanes &= lanes - 1;
           uint32_t w = __shfl_sync(0xffffffffu, mine, src);
           while (ok && w) {
-            ok = emit((w0 + src) * 32 + __ffs(w) - 1, one);
+            ok = push((w0 + src) * 32 + __ffs(w) - 1, one);
             w &= w - 1;
           }
         }
       }
     } else {
-      ok = sp_scan(a, t, lane, emit);
+      ok = sp_scan(a, t, lane, push);
     }
-    if (ok && pend) ok = push(1);
-    const int tiles = n;
-    if (ok) ok = push(0);
+    const uint32_t none[4] = {0u, 0u, 0u, 0u};
+    if (ok) ok = push(-1, none);
     if (!ok && lane == 0) {
       atomicOr(&g_skl_error, 1u);
       *abort_flag = 1;
       // Let the copies in flight land before the CTA can exit (each wait is bounded).
       mbar_wait(smem_u32(&bars->q_full), 0);
-      for (int j = max(0, tiles - C::NST); j < tiles; ++j) {
-        mbar_wait(smem_u32(&bars->k_full[j % C::NST]), (j / C::NST) & 1);
-        mbar_wait(smem_u32(&bars->v_full[j % C::NST]), (j / C::NST) & 1);
+      for (int j = max(0, n - NST); j < n; ++j) {
+        mbar_wait(smem_u32(&bars->k_full[j % NST]), (j / NST) & 1);
+        mbar_wait(smem_u32(&bars->v_full[j % NST]), (j / NST) & 1);
       }
     }
-    // With no key tile nothing else waits for the Q copy.
-    if (lane == 0 && tiles == 0) mbar_wait(smem_u32(&bars->q_full), 0);
-  } else if (warp == 9 && elect_one()) {
+    // With no block nothing else waits for the Q copy.
+    if (lane == 0 && n == 0) mbar_wait(smem_u32(&bars->q_full), 0);
+  } else if (elect_one()) {
     // ------------------------------------------------------------------ MMA issuer
+    // Descriptors are a base per operand plus constants: this thread's instruction stream is on
+    // the critical path.
+    const uint32_t hi = sdesc_hi(1024);
+    const uint32_t lq = sdesc_lo(sb, 16), lk0 = sdesc_lo(sb + C::OFF_K, 16);
+    const uint32_t lv0 = sdesc_lo(sb + C::OFF_V, 64 * 128);
     bool ok = mbar_wait(smem_u32(&bars->q_full), 0);
-    for (int n = 0; ok; ++n) {
-      ok = mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1);
-      if (!ok) break;
-      const int nb = bars->info[n & 3].nb;
-      if (nb == 0) break;
-      const int st = n % C::NST;
-      const uint32_t ph = (n / C::NST) & 1;
-      const uint32_t sk = sb + C::OFF_K + st * C::KVBYTES, sv = sb + C::OFF_V + st * C::KVBYTES;
-      if (!(ok = mbar_wait(smem_u32(&bars->k_full[st]), ph))) break;
+    // S of step n: 1, no such step: 0, a wait ran out: -1. The buffer's last P has been handed
+    // to a product issued before.
+    auto scores = [&](int n) -> int {
+      if (!mbar_wait(smem_u32(&bars->info_full[n & 7]), (n >> 3) & 1)) return -1;
+      if (bars->info[n & 7].c < 0) return 0;
+      const int st = n % NST;
+      if (!mbar_wait(smem_u32(&bars->k_full[st]), (n / NST) & 1)) return -1;
       tc_fence_after();
-      const uint32_t id = nb == 2 ? idesc_s2 : idesc_s1;
+      const uint32_t lk = lk0 + st * (C::SLOT >> 4), ds = tmem + C::TM_S + 64 * (n & 1);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-        umma_bf16_ss(tmem + C::TM_S, sdesc_sw128(sb + off, 16, 1024),
-                     sdesc_sw128(sk + off, 16, 1024), id, kk > 0);
-      }
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_bf16_ss_lh(ds, lq + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
+                        lk + (((kk >> 2) * (64 * 128) + (kk & 3) * 32) >> 4), hi, idesc_s, kk > 0);
+      umma_commit(smem_u32(&bars->s_full[n & 1]));
       umma_commit(smem_u32(&bars->k_empty[st]));
-      umma_commit(smem_u32(&bars->s_full));
-      if (!(ok = mbar_wait(smem_u32(&bars->v_full[st]), ph))) break;
-      if (!(ok = mbar_wait(smem_u32(&bars->p_full), n & 1))) break;
+      return 1;
+    };
+    int ahead = 0;  // steps whose S has been issued
+    bool more = ok;
+    auto reach = [&](int n) {
+      while (ok && more && ahead <= n) {
+        const int got = scores(ahead);
+        if (got < 0) ok = false;
+        if (got == 0) more = false;
+        if (got > 0) ++ahead;
+      }
+    };
+    reach(1);
+    for (int n = 0; ok && n < ahead; ++n) {
+      const int st = n % NST;
+      if (!(ok = mbar_wait(smem_u32(&bars->v_full[st]), (n / NST) & 1))) break;
+      if (!(ok = mbar_wait(smem_u32(&bars->p_full[n & 1]), (n >> 1) & 1))) break;
       tc_fence_after();
       // O += P V: A = P from TMEM, B = V [keys][d] MN-major, 16 keys per step.
-      for (int kk = 0; kk < 4 * nb; ++kk)
-        umma_bf16_ts(tmem + C::TM_O, tmem + C::TM_S + (kk >> 2) * 64 + (kk & 3) * 8,
-                     sdesc_sw128(sv + kk * 2048, 128 * 128, 1024), idesc_o,
-                     (n > 0 || kk > 0) ? 1u : 0u);
+      const uint32_t lv = lv0 + st * (C::SLOT >> 4), tp = tmem + C::TM_S + 64 * (n & 1);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        umma_bf16_ts_lh(tmem + C::TM_O, tp + kk * 8, lv + kk * (2048 >> 4), hi, idesc_o,
+                        (n > 0 || kk > 0) ? 1u : 0u);
       umma_commit(smem_u32(&bars->v_empty[st]));
+      reach(n + 2);
     }
     umma_commit(smem_u32(&bars->o_full));
     if (!ok) {
@@ -604,7 +603,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   }
   __syncwarp();
   if (a.splits > 1) cluster_sync();
-  if ((QUAD || a.splits > 1) && warp < 4)
+  if ((QUAD || a.splits > 1) && warp < 8)
     sp_join<D, QUAD>(a, t, sb, smem_u32(bars->l2), split, warp, lane);
   __syncwarp();
   if (a.splits > 1) cluster_sync();  // another CTA may still be reading this one's rows

@@ -5,11 +5,13 @@
 // index, NaN ranks below every number. Written in ascending order, -1 behind the last.
 //
 // A row's masses become unsigned keys in their order (forced blocks get the largest key) and
-// stay in registers. The topk-th largest key is found bit by bit from the top: each step counts
-// the keys that reach the candidate and stops early once exactly topk do. The selection is then
-// written by ranks in index order, which gives the ascending list and the ties' order without
-// a sort. One warp per row up to 1024 blocks, one CTA per row beyond. Bound by reading the
-// masses for many rows, by latency for few.
+// stay in registers. A threshold that exactly topk keys reach is found by bisection between the
+// least and the largest free key: keys order like the logarithm of the mass, so the bracket
+// narrows to the gap behind the topk-th key in a few steps (about 7 for 256 blocks), and the
+// search ends with the first threshold in that gap, or, with ties, at the topk-th key itself. The
+// selection is then written by ranks in index order, which gives the ascending list and the
+// ties' order without a sort. One warp per row when there are many rows, four or eight when there
+// are few or long ones. Bound by issue slots for many rows, by latency for few.
 #pragma once
 
 #include "sparse_common.cuh"
@@ -33,90 +35,102 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
   return k;                                                       // inf: 0xff800000
 }
 
-template <int WARPS>
-__device__ __forceinline__ int select_sum(int x, int* red, int warp, int lane) {
-  x = __reduce_add_sync(0xffffffffu, x);
+// Reductions over a row's warps; `red` alternates between two sets so that one barrier per
+// reduction suffices.
+template <int WARPS, typename Op>
+__device__ __forceinline__ uint32_t select_join(uint32_t x, uint32_t (*red)[8], int& turn, int warp,
+                                                int lane, Op op) {
   if (WARPS == 1) return x;
-  if (lane == 0) red[warp] = x;
+  if (lane == 0) red[turn][warp] = x;
   __syncthreads();
-  int s = 0;
+  uint32_t r = red[turn][0];
 #pragma unroll
-  for (int k = 0; k < WARPS; ++k) s += red[k];
-  __syncthreads();
-  return s;
+  for (int k = 1; k < WARPS; ++k) r = op(r, red[turn][k]);
+  turn ^= 1;
+  return r;
 }
 
-// V keys per thread, WARPS warps per row (1: four rows per CTA). Thread t of a row holds the
-// blocks (w * V + k) * 32 + lane for warp w, k < V: reads are coalesced and ranks in index
-// order follow from ballots.
+// One row whose n visible blocks fit V keys per thread. Warp w, register k and lane hold block
+// (w * V + k) * 32 + lane: reads are coalesced and ranks in index order follow from ballots.
 template <int V, int WARPS>
-__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS)
-streamkl_block_select_kernel(const SelectArgs a) {
-  __shared__ int red[WARPS == 1 ? 1 : WARPS];
-  const int lane = threadIdx.x & 31;
-  const int warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
-  const long long row = WARPS == 1 ? (long long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-  if (row >= a.rows) return;
-  const long long bh = row / a.N_Q;
-  const int i = (int)(row - bh * a.N_Q), b = (int)(bh / a.Hsel);
-  const int nk = sp_len(a.lens, b, a.N_K);
-  const int last = sp_last(i, nk, a.N_Q, a.causal);
-  const int n = last < 0 ? 0 : last / kSpBlock + 1;
+__device__ __forceinline__ void select_row(const SelectArgs& a, long long row, int n,
+                                           uint32_t (*red)[8], int warp, int lane) {
+  int turn = 0;
   const float* src = a.mass + row * a.NB;
   int* dst = a.idx + row * a.topk;
-
-  uint32_t key[V];
+  const int base = warp * V * 32;
+  auto add = [](uint32_t x, uint32_t y) { return x + y; };
+  auto lesser = [](uint32_t x, uint32_t y) { return min(x, y); };
+  auto larger = [](uint32_t x, uint32_t y) { return max(x, y); };
+  uint32_t key[V], kmin = 0xffffffffu, kmax = 0u;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = (warp * V + k) * 32 + lane;
-    key[k] = 0u;
-    if (c < n) key[k] = c < a.n_first || c >= n - a.n_last ? 0xffffffffu : mass_key(__ldg(src + c));
+    const int c = base + k * 32 + lane;
+    key[k] = c < n ? mass_key(__ldg(src + c)) : 0u;
   }
-  // Largest threshold that at least topk keys reach (1 when fewer blocks are visible).
-  uint32_t thr = 1u;
-  int above = n;  // keys >= thr
-  if (n > a.topk) {
-    uint32_t t = 0u;
-    int reach = n;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t cand = t | (1u << bit);
-      int cnt = 0;
 #pragma unroll
-      for (int k = 0; k < V; ++k) cnt += key[k] >= cand ? 1 : 0;
-      cnt = select_sum<WARPS>(cnt, red, warp, lane);
-      if (cnt >= a.topk) {
-        t = cand;
-        reach = cnt;
-        if (cnt == a.topk) break;
+  for (int k = 0; k < V; ++k) {
+    const int c = base + k * 32 + lane;
+    if (c < n) {
+      if (c < a.n_first || c >= n - a.n_last) {
+        key[k] = 0xffffffffu;
+      } else {
+        kmin = min(kmin, key[k]);
+        kmax = max(kmax, key[k]);
       }
     }
-    thr = t;
-    above = reach;
   }
-  // Keys above thr are all taken; of those equal to it, the lowest indices fill up.
-  int ties = a.topk;  // how many keys equal to thr are taken
-  if (above > a.topk) {
-    int cnt = 0;
+  uint32_t thr = 1u;  // taken: keys above thr, and the first `ties` equal to it
+  int ties = a.topk;
+  if (n > a.topk) {
+    // count(key >= lo) >= topk > count(key >= hi); forced keys reach every threshold.
+    const int forced = min(a.n_first, n) + a.n_last;  // n > topk >= n_first + n_last
+    if (forced == a.topk) {
+      thr = 0xfffffffeu;  // no free key is taken (masses' keys end below)
+    } else {
+      kmin = select_join<WARPS>(__reduce_min_sync(0xffffffffu, kmin), red, turn, warp, lane, lesser);
+      kmax = select_join<WARPS>(__reduce_max_sync(0xffffffffu, kmax), red, turn, warp, lane, larger);
+      uint32_t lo = kmin, hi = kmax + 1u;
+      int reach = n;  // keys >= lo
+      while (hi - lo > 1u) {
+        const uint32_t mid = lo + ((hi - lo) >> 1);
+        uint32_t cnt = 0;
 #pragma unroll
-    for (int k = 0; k < V; ++k) cnt += key[k] > thr ? 1 : 0;
-    ties = a.topk - select_sum<WARPS>(cnt, red, warp, lane);
+        for (int k = 0; k < V; ++k) cnt += key[k] >= mid ? 1u : 0u;
+        cnt = select_join<WARPS>(__reduce_add_sync(0xffffffffu, cnt), red, turn, warp, lane, add);
+        if ((int)cnt >= a.topk) {
+          lo = mid;
+          reach = (int)cnt;
+          if (reach == a.topk) break;
+        } else {
+          hi = mid;
+        }
+      }
+      thr = lo;
+      if (reach > a.topk) {
+        uint32_t cnt = 0;
+#pragma unroll
+        for (int k = 0; k < V; ++k) cnt += key[k] > thr ? 1u : 0u;
+        ties = a.topk - (int)select_join<WARPS>(__reduce_add_sync(0xffffffffu, cnt), red, turn, warp,
+                                                lane, add);
+      }
+    }
   }
   // Ranks in index order: this warp's blocks are consecutive, earlier warps come first.
   int eq0 = 0, gt0 = 0;  // equal / greater keys of earlier warps
   if (WARPS > 1) {
-    int e = 0, g = 0;
+    uint32_t e = 0, g = 0;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       e += __popc(__ballot_sync(0xffffffffu, key[k] == thr));
       g += __popc(__ballot_sync(0xffffffffu, key[k] > thr));
     }
-    if (lane == 0) red[warp] = e;
+    if (lane == 0) red[turn][warp] = e | (g << 16);  // at most 8192 blocks
     __syncthreads();
-    for (int w = 0; w < warp; ++w) eq0 += red[w];
-    __syncthreads();
-    if (lane == 0) red[warp] = g;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) gt0 += red[w];
+    for (int w = 0; w < warp; ++w) {
+      eq0 += red[turn][w] & 0xffffu;
+      gt0 += red[turn][w] >> 16;
+    }
   }
   int at = gt0 + min(eq0, ties);
   const uint32_t below = (1u << lane) - 1u;
@@ -125,7 +139,7 @@ streamkl_block_select_kernel(const SelectArgs a) {
     const uint32_t eq = __ballot_sync(0xffffffffu, key[k] == thr);
     const bool take = key[k] > thr || (key[k] == thr && eq0 + __popc(eq & below) < ties);
     const uint32_t taken = __ballot_sync(0xffffffffu, take);
-    if (take) dst[at + __popc(taken & below)] = (warp * V + k) * 32 + lane;
+    if (take) dst[at + __popc(taken & below)] = base + k * 32 + lane;
     at += __popc(taken);
     eq0 += __popc(eq);
   }
@@ -133,6 +147,31 @@ streamkl_block_select_kernel(const SelectArgs a) {
   for (int e = have + (WARPS == 1 ? lane : (int)threadIdx.x); e < a.topk;
        e += WARPS == 1 ? 32 : 32 * WARPS)
     dst[e] = -1;
+}
+
+// WARPS = 1: four rows per CTA, one warp each, with the fewest registers that hold the row's
+// visible blocks (causal rows see half of them on average). WARPS > 1: one row per CTA.
+template <int V, int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS)
+streamkl_block_select_kernel(const SelectArgs a) {
+  __shared__ uint32_t red[2][8];
+  const int lane = threadIdx.x & 31;
+  const int warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
+  const unsigned row = WARPS == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  if (row >= (unsigned long long)a.rows) return;  // rows < 2^31
+  const unsigned bh = row / (unsigned)a.N_Q;
+  const int i = (int)(row - bh * (unsigned)a.N_Q), b = (int)(bh / (unsigned)a.Hsel);
+  const int nk = sp_len(a.lens, b, a.N_K);
+  const int last = sp_last(i, nk, a.N_Q, a.causal);
+  const int n = last < 0 ? 0 : last / kSpBlock + 1;
+  if (WARPS == 1 && V > 2 && n <= 64)
+    select_row<2, WARPS>(a, row, n, red, warp, lane);
+  else if (WARPS == 1 && V > 4 && n <= 128)
+    select_row<4, WARPS>(a, row, n, red, warp, lane);
+  else if (WARPS == 1 && V == 8 && n <= 192)
+    select_row<6, WARPS>(a, row, n, red, warp, lane);
+  else
+    select_row<V, WARPS>(a, row, n, red, warp, lane);
 }
 
 }  // namespace skl

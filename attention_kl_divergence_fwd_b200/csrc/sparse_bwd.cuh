@@ -279,34 +279,52 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
     const uint32_t lk0 = sdesc_lo(sb + C::OFF_K, 16), lv0 = sdesc_lo(sb + C::OFF_V, 16);
     const uint32_t lkn0 = sdesc_lo(sb + C::OFF_K, 64 * 128);  // K as [keys][d], MN-major
     bool ok = mbar_wait(smem_u32(&bars->q_full), 0);
-    for (int n = 0; ok; ++n) {
-      if (!(ok = mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1))) break;
-      if (bars->info[n & 3].c < 0) break;
+    // Waits for K and V of step n: 1, no such step: 0, a wait ran out: -1.
+    auto loaded = [&](int n) -> int {
+      if (!mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1)) return -1;
+      if (bars->info[n & 3].c < 0) return 0;
+      return mbar_wait(smem_u32(&bars->k_full[n % C::NK]), (n / C::NK) & 1) &&
+                     mbar_wait(smem_u32(&bars->v_full[n % C::NV]), (n / C::NV) & 1)
+                 ? 1
+                 : -1;
+    };
+    auto scores = [&](int n) {
       const int ks = n % C::NK, vs = n % C::NV;
       const uint32_t lk = lk0 + ks * (C::SLOT >> 4), lv = lv0 + vs * (C::SLOT >> 4);
-      if (!(ok = mbar_wait(smem_u32(&bars->k_full[ks]), (n / C::NK) & 1))) break;
-      tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         umma_bf16_ss_lh(tmem + C::TM_S, lq + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
                         lk + (((kk >> 2) * (64 * 128) + (kk & 3) * 32) >> 4), hi, idesc_s, kk > 0);
-      if (!(ok = mbar_wait(smem_u32(&bars->v_full[vs]), (n / C::NV) & 1))) break;
-      tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         umma_bf16_ss_lh(tmem + C::TM_DP, ldo + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
                         lv + (((kk >> 2) * (64 * 128) + (kk & 3) * 32) >> 4), hi, idesc_dp, kk > 0);
       umma_commit(smem_u32(&bars->s_full));
       umma_commit(smem_u32(&bars->v_empty[vs]));
-      if (!(ok = mbar_wait(smem_u32(&bars->ds_full), n & 1))) break;
+    };
+    int next = ok ? loaded(0) : -1;
+    if (next > 0) {
       tc_fence_after();
-      const uint32_t lkn = lkn0 + ks * (C::SLOT >> 4);
+      scores(0);
+    }
+    for (int n = 0; next > 0; ++n) {
+      // The next step's K and V are awaited before this step's dS, so that once dS is there its
+      // product and the next scores go out back to back.
+      if ((next = loaded(n + 1)) < 0) break;
+      if (!mbar_wait(smem_u32(&bars->ds_full), n & 1)) {
+        next = -1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t lkn = lkn0 + (n % C::NK) * (C::SLOT >> 4);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
         umma_bf16_ts_lh(tmem + C::TM_DQ, tmem + C::TM_S + (kk >> 1) * 32 + (kk & 1) * 8,
                         lkn + kk * (2048 >> 4), hi, idesc_dq, (n > 0 || kk > 0) ? 1u : 0u);
-      umma_commit(smem_u32(&bars->k_empty[ks]));
+      umma_commit(smem_u32(&bars->k_empty[n % C::NK]));
+      if (next > 0) scores(n + 1);
     }
+    ok = next >= 0;
     umma_commit(smem_u32(&bars->dq_full));
     if (!ok) {
       atomicOr(&g_skl_error, 2u);

@@ -9,9 +9,11 @@
 //   probabilities against the row's reference m and writes them back over the scores as bf16;
 //   O += P V with P read from TMEM; S of the next but one block follows at once.
 // Two groups of four warps take alternate blocks, so one block's exponentials run under the other
-// block's products and loads. They share m, handed from block to block through shared memory;
-// m rises, with a rescale of O in TMEM, only when a score exceeds it by 2^8, so most blocks leave
-// m and O alone. Each group keeps its own part of the row sum.
+// block's products and loads. They share m, handed from block to block through shared memory.
+// The sums are exact for any reference, so a block is folded against m as it stands; only a
+// row's first block, partial blocks and a block whose sum reaches 2^64 take its maximum first,
+// and raise m, with a rescale of O in TMEM, when it exceeds m by 2^8. Each group keeps its own
+// part of the row sum.
 // P is rounded to bf16 for the tensor core (relative error at most 2^-8 each, the same as the
 // output's own rounding); the row sums, references and O stay in fp32.
 // A CTA takes 256 TMEM columns and about 100 KB of shared memory: two CTAs share an SM, which
@@ -89,13 +91,13 @@ __device__ __forceinline__ void sp_zero_tail(uint8_t* buf, int first, int tid, i
 
 // 2^(v c + bias) of 32 scores as bf16 pairs, and their sum (two packed partial sums). POLY: a share
 // on the FMA pipe, for arguments known to be finite.
-template <bool POLY, int N>
-__device__ __forceinline__ void sp_exp32(const uint32_t (&v)[N], int at, uint64_t c2, uint64_t b2,
+template <bool POLY>
+__device__ __forceinline__ void sp_exp32(const uint32_t (&v)[32], uint64_t c2, uint64_t b2,
                                          uint64_t& acc0, uint64_t& acc1, uint32_t (&p)[16]) {
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
     const uint64_t x =
-        f2_fma(f2_pack(__uint_as_float(v[at + k]), __uint_as_float(v[at + k + 1])), c2, b2);
+        f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, b2);
     float x0, x1;
     if (POLY && poly_rank((k >> 1) & 7) < SKL_SP_POLY) {
       f2_unpack(exp2_fma2(x), x0, x1);
@@ -276,106 +278,150 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
                         threadIdx.x & 127, 128);
         fence_async_smem();
       }
-      constexpr int NC = QUAD ? 16 : 64;  // score columns of this thread
-      uint32_t v[NC];
-      float mx = -INFINITY;
-      if constexpr (QUAD) {
-        tmem_ld_16_wait(ts + 16 * quarter, v);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          if (16 * quarter + k > lim) v[k] = 0xff800000u;  // -inf
-          mx = fmaxf(mx, __uint_as_float(v[k]));
-        }
-      } else if (live) {
-        tmem_ld_2x32_wait(ts, ts + 32, v);
-        // Blocks are read whole or not at all except at the causal diagonal and the
-        // sequence's end; only those mask single scores (the end's scores may be NaN).
-        if (at_end || __any_sync(0xffffffffu, lim >= 0 && lim < 63)) {
-#pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (k > lim) v[k] = 0xff800000u;  // -inf
-        }
-        mx = fmaxf(max_tree32<false>(v, 0, 31), max_tree32<false>(v, 32, 31));
-        if (lim < 0) mx = -INFINITY;
-      }
-      const float ms = mx == -INFINITY ? -INFINITY : mx * c;
-      // The reference after block n - 1, from the other group; slots alternate by block, and a
-      // slot's next value needs one from the other group in between.
-      float m0 = -INFINITY;
-      if (n > 0) {
-        if (!mbar_wait(smem_u32(&bars->m_pass[quarter][(n - 1) & 1]), ((n - 1) >> 1) & 1)) {
-          ok = false;
-          break;
-        }
-        m0 = bars->m[(n - 1) & 1][slot];
-      }
-      const bool raise = ms > m0 + 8.f || (m0 == -INFINITY && ms > -INFINITY);
-      const float m1 = raise ? ms : m0;
-      bars->m[n & 1][slot] = m1;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->m_pass[quarter][n & 1]));
-      if (m1 != m) {
-        l *= ex2_approx(m - m1);  // m = -inf: l = 0
-        m = m1;
-      }
-      if (n > 0 && __any_sync(0xffffffffu, raise)) {
-        // O *= 2^(m0 - m1) once it holds every product before this block's.
-        if (!mbar_wait(smem_u32(&bars->v_empty[(n - 1) % NST]), ((n - 1) / NST) & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float f0 = raise ? ex2_approx(m0 - m1) : 1.f;  // m0 = -inf: 0
-#pragma unroll
-        for (int k = 0; k < D; k += 8) {  // few registers: the scores are live
-          uint32_t o[8];
-          tmem_ld_8_wait(to + k, o);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
-          tmem_st_8(to + k, o);
-        }
-      }
+      // Fast way: probabilities against the reference at hand, without the block's maximum first.
+      // It holds when no row's partial block or first block is among them, the row's sum stays
+      // below 2^64 (no score is far above the reference) and the other group has not raised it.
       uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
-      const float bias = lim < 0 ? -INFINITY : (m == -INFINITY ? 0.f : -m);
-      const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(bias, bias);
-      if constexpr (QUAD) {
-        uint32_t p[8], zero[8];
-#pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          float x0, x1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, b2), x0,
-                    x1);
-          x0 = ex2_approx(x0);
-          x1 = ex2_approx(x1);
-          acc0 = f2_add(acc0, f2_pack(x0, x1));
-          p[k >> 1] = pack_bf16x2(x0, x1);
-          zero[k >> 1] = 0u;
+      const uint64_t c2 = f2_pack(c, c);
+      float m0 = -INFINITY;  // the reference after block n - 1
+      bool have_m0 = n == 0;
+      // Slots alternate by block; a slot's next value needs one from the other group in between.
+      auto reference = [&]() -> bool {
+        if (have_m0) return true;
+        have_m0 = true;
+        if (!mbar_wait(smem_u32(&bars->m_pass[quarter][(n - 1) & 1]), ((n - 1) >> 1) & 1))
+          return false;
+        m0 = bars->m[(n - 1) & 1][slot];
+        return true;
+      };
+      auto publish = [&](float m1) {
+        bars->m[n & 1][slot] = m1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->m_pass[quarter][n & 1]));
+      };
+      bool done = false;
+      if constexpr (!QUAD) {
+        if (n == 1) {
+          if (!reference()) { ok = false; break; }
+          m = m0;
         }
+        if (live && n > 0 && !at_end &&
+            __all_sync(0xffffffffu, lim < 0 || (lim >= 63 && m > -INFINITY))) {
+          uint32_t v[32], p0[16], p1[16];  // 32 scores at a time: registers are short
+          const uint64_t b2 = f2_pack(-m, -m);
+          tmem_ld_32_wait(ts, v);
+          sp_exp32<true>(v, c2, b2, acc0, acc1, p0);
+          tmem_ld_32_wait(ts + 32, v);
+          sp_exp32<true>(v, c2, b2, acc0, acc1, p1);
+          float s0, s1;
+          f2_unpack(f2_add(acc0, acc1), s0, s1);
+          float sum = s0 + s1;
+          if (lim < 0) {  // this row does not list the block
+            sum = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (q == quarter)
-            tmem_st_8(ts + 8 * q, p);
-          else
-            tmem_st_8(ts + 8 * q, zero);
-        }
-      } else if (live) {
-        // P goes over the scores this thread has read.
-        uint32_t p[16];
-        if (__all_sync(0xffffffffu, lim >= 63)) {
-          sp_exp32<true>(v, 0, c2, b2, acc0, acc1, p);
-          tmem_st_16(ts, p);
-          sp_exp32<true>(v, 32, c2, b2, acc0, acc1, p);
-          tmem_st_16(ts + 16, p);
-        } else {
-          sp_exp32<false>(v, 0, c2, b2, acc0, acc1, p);
-          tmem_st_16(ts, p);
-          sp_exp32<false>(v, 32, c2, b2, acc0, acc1, p);
-          tmem_st_16(ts + 16, p);
+            for (int k = 0; k < 16; ++k) p0[k] = p1[k] = 0u;
+          }
+          if (!reference()) { ok = false; break; }
+          if (__all_sync(0xffffffffu, m0 == m && sum < 0x1p64f)) {
+            publish(m);
+            // P goes over the scores this thread has read.
+            tmem_st_16(ts, p0);
+            tmem_st_16(ts + 16, p1);
+            l += sum;
+            done = true;
+          }
         }
       }
-      float s0, s1;
-      f2_unpack(f2_add(acc0, acc1), s0, s1);
-      l += s0 + s1;
+      if (!done) {
+        constexpr int NC = QUAD ? 16 : 32;  // scores at a time
+        uint32_t v[NC];
+        float mx = -INFINITY;
+        // Blocks are read whole or not at all except at the causal diagonal and the sequence's
+        // end; only those mask single scores (the end's scores may be NaN).
+        const bool single = at_end || __any_sync(0xffffffffu, lim >= 0 && lim < 63);
+        auto mask = [&](int first) {
+#pragma unroll
+          for (int k = 0; k < NC; ++k)
+            if (first + k > lim) v[k] = 0xff800000u;  // -inf
+        };
+        if constexpr (QUAD) {
+          tmem_ld_16_wait(ts + 16 * quarter, v);
+          mask(16 * quarter);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
+        } else if (live) {
+#pragma unroll
+          for (int h = 0; h < 64; h += 32) {
+            tmem_ld_32_wait(ts + h, v);
+            if (single) mask(h);
+            mx = fmaxf(mx, max_tree32<false>(v, 0, 31));
+          }
+          if (lim < 0) mx = -INFINITY;
+        }
+        const float ms = mx == -INFINITY ? -INFINITY : mx * c;
+        if (!reference()) { ok = false; break; }
+        const bool raise = ms > m0 + 8.f || (m0 == -INFINITY && ms > -INFINITY);
+        const float m1 = raise ? ms : m0;
+        publish(m1);
+        if (m1 != m) {
+          l *= ex2_approx(m - m1);  // m = -inf: l = 0
+          m = m1;
+        }
+        if (n > 0 && __any_sync(0xffffffffu, raise)) {
+          // O *= 2^(m0 - m1) once it holds every product before this block's.
+          if (!mbar_wait(smem_u32(&bars->v_empty[(n - 1) % NST]), ((n - 1) / NST) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float f0 = raise ? ex2_approx(m0 - m1) : 1.f;  // m0 = -inf: 0
+#pragma unroll
+          for (int k = 0; k < D; k += 8) {  // few registers: the scores are live
+            uint32_t o[8];
+            tmem_ld_8_wait(to + k, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+            tmem_st_8(to + k, o);
+          }
+        }
+        acc0 = acc1 = f2_pack(0.f, 0.f);
+        const float bias = lim < 0 ? -INFINITY : (m == -INFINITY ? 0.f : -m);
+        const uint64_t b2 = f2_pack(bias, bias);
+        if constexpr (QUAD) {
+          uint32_t p[8], zero[8];
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, b2), x0,
+                      x1);
+            x0 = ex2_approx(x0);
+            x1 = ex2_approx(x1);
+            acc0 = f2_add(acc0, f2_pack(x0, x1));
+            p[k >> 1] = pack_bf16x2(x0, x1);
+            zero[k >> 1] = 0u;
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (q == quarter)
+              tmem_st_8(ts + 8 * q, p);
+            else
+              tmem_st_8(ts + 8 * q, zero);
+          }
+        } else if (live) {
+          // P goes over scores that have been read: keys 0-31 over the columns 0-15.
+          uint32_t p[16];
+#pragma unroll
+          for (int h = 0; h < 64; h += 32) {
+            tmem_ld_32_wait(ts + h, v);
+            if (single) mask(h);
+            sp_exp32<false>(v, c2, b2, acc0, acc1, p);
+            tmem_st_16(ts + h / 2, p);
+          }
+        }
+        float s0, s1;
+        f2_unpack(f2_add(acc0, acc1), s0, s1);
+        l += s0 + s1;
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -455,12 +501,15 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     const uint64_t keep = l2_policy_evict_last();
     bool ok = true;
     int n = 0, rank = 0;
-    // Announces block c as step n and loads it (-1: the end).
+    // Announces block c as step n and loads its K, then V of the step before: K's slot is free as
+    // soon as S(n - NST) is done, V's only after the product of step n - 1 - NST, and waiting for
+    // that first would hold K back (-1: the end, only V of the last step).
+    int c_prev = -1;
     auto push = [&](int c, const uint32_t (&u)[4]) -> bool {
       if (c >= 0 && a.splits > 1 && rank++ % a.splits != split) return true;
       bool fine = true;
       if (lane == 0) {
-        // Entry n & 7 was last read for step n - 8: loads run at most NST + 2 steps ahead of
+        // Entry n & 7 was last read for step n - 8: loads run at most NST + 3 steps ahead of
         // the products, which wait for every softmax warp.
         SpBlockInfo& f = bars->info[n & 7];
         f.c = c;
@@ -469,26 +518,32 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         mbar_arrive(smem_u32(&bars->info_full[n & 7]));
         if (c >= 0) {
           const int st = n % NST;
-          const uint32_t ph = ((n / NST) & 1) ^ 1;
-          const uint32_t kf = smem_u32(&bars->k_full[st]), vf = smem_u32(&bars->v_full[st]);
-          fine = mbar_wait(smem_u32(&bars->k_empty[st]), ph);
+          const uint32_t kf = smem_u32(&bars->k_full[st]);
+          fine = mbar_wait(smem_u32(&bars->k_empty[st]), ((n / NST) & 1) ^ 1);
           if (fine) {
             mbar_arrive_expect_tx(kf, C::SLOT);
             for (int blk = 0; blk < D / 64; ++blk)
               tma_load_3d(sb + C::OFF_K + st * C::SLOT + blk * (64 * 128), &map_k, kf, blk * 64,
                           c * kSpBlock, t.kv, keep);
-            fine = mbar_wait(smem_u32(&bars->v_empty[st]), ph);
           }
+        }
+        if (fine && n > 0) {
+          const int st = (n - 1) % NST;
+          const uint32_t vf = smem_u32(&bars->v_full[st]);
+          fine = mbar_wait(smem_u32(&bars->v_empty[st]), (((n - 1) / NST) & 1) ^ 1);
           if (fine) {
             mbar_arrive_expect_tx(vf, C::SLOT);
             for (int blk = 0; blk < D / 64; ++blk)
               tma_load_3d(sb + C::OFF_V + st * C::SLOT + blk * (64 * 128), &map_v, vf, blk * 64,
-                          c * kSpBlock, t.kv, keep);
+                          c_prev * kSpBlock, t.kv, keep);
           }
         }
       }
       fine = __shfl_sync(0xffffffffu, fine ? 1 : 0, 0) != 0;
-      if (c >= 0) ++n;
+      if (c >= 0) {
+        c_prev = c;
+        ++n;
+      }
       return fine;
     };
     if (a.direct) {
@@ -531,7 +586,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_wait(smem_u32(&bars->q_full), 0);
       for (int j = max(0, n - NST); j < n; ++j) {
         mbar_wait(smem_u32(&bars->k_full[j % NST]), (j / NST) & 1);
-        mbar_wait(smem_u32(&bars->v_full[j % NST]), (j / NST) & 1);
+        if (j < n - 1) mbar_wait(smem_u32(&bars->v_full[j % NST]), (j / NST) & 1);
       }
     }
     // With no block nothing else waits for the Q copy.
@@ -544,14 +599,15 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     const uint32_t lq = sdesc_lo(sb, 16), lk0 = sdesc_lo(sb + C::OFF_K, 16);
     const uint32_t lv0 = sdesc_lo(sb + C::OFF_V, 64 * 128);
     bool ok = mbar_wait(smem_u32(&bars->q_full), 0);
-    // S of step n: 1, no such step: 0, a wait ran out: -1. The buffer's last P has been handed
-    // to a product issued before.
-    auto scores = [&](int n) -> int {
+    // Waits for K of step n: 1, no such step: 0, a wait ran out: -1.
+    auto keys = [&](int n) -> int {
       if (!mbar_wait(smem_u32(&bars->info_full[n & 7]), (n >> 3) & 1)) return -1;
       if (bars->info[n & 7].c < 0) return 0;
+      return mbar_wait(smem_u32(&bars->k_full[n % NST]), (n / NST) & 1) ? 1 : -1;
+    };
+    // S of step n. The buffer's last P has been handed to a product issued before.
+    auto scores = [&](int n) {
       const int st = n % NST;
-      if (!mbar_wait(smem_u32(&bars->k_full[st]), (n / NST) & 1)) return -1;
-      tc_fence_after();
       const uint32_t lk = lk0 + st * (C::SLOT >> 4), ds = tmem + C::TM_S + 64 * (n & 1);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
@@ -559,23 +615,23 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
                         lk + (((kk >> 2) * (64 * 128) + (kk & 3) * 32) >> 4), hi, idesc_s, kk > 0);
       umma_commit(smem_u32(&bars->s_full[n & 1]));
       umma_commit(smem_u32(&bars->k_empty[st]));
-      return 1;
     };
-    int ahead = 0;  // steps whose S has been issued
-    bool more = ok;
-    auto reach = [&](int n) {
-      while (ok && more && ahead <= n) {
-        const int got = scores(ahead);
-        if (got < 0) ok = false;
-        if (got == 0) more = false;
-        if (got > 0) ++ahead;
-      }
-    };
-    reach(1);
-    for (int n = 0; ok && n < ahead; ++n) {
+    int ahead = 0;   // steps whose S has been issued
+    int next = ok ? 1 : -1;  // whether there is a step `ahead` with its K landed
+    for (; ahead < 2 && (next = next < 0 ? next : keys(ahead)) > 0; ++ahead) {
+      tc_fence_after();
+      scores(ahead);
+    }
+    for (int n = 0; next >= 0 && n < ahead; ++n) {
       const int st = n % NST;
-      if (!(ok = mbar_wait(smem_u32(&bars->v_full[st]), (n / NST) & 1))) break;
-      if (!(ok = mbar_wait(smem_u32(&bars->p_full[n & 1]), (n >> 1) & 1))) break;
+      // Everything but P is awaited first, so that once P is there the products of this step
+      // and S of the next but one go out back to back.
+      if (next > 0 && (next = keys(n + 2)) < 0) break;
+      if (!mbar_wait(smem_u32(&bars->v_full[st]), (n / NST) & 1) ||
+          !mbar_wait(smem_u32(&bars->p_full[n & 1]), (n >> 1) & 1)) {
+        next = -1;
+        break;
+      }
       tc_fence_after();
       // O += P V: A = P from TMEM, B = V [keys][d] MN-major, 16 keys per step.
       const uint32_t lv = lv0 + st * (C::SLOT >> 4), tp = tmem + C::TM_S + 64 * (n & 1);
@@ -584,8 +640,12 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         umma_bf16_ts_lh(tmem + C::TM_O, tp + kk * 8, lv + kk * (2048 >> 4), hi, idesc_o,
                         (n > 0 || kk > 0) ? 1u : 0u);
       umma_commit(smem_u32(&bars->v_empty[st]));
-      reach(n + 2);
+      if (next > 0) {
+        scores(n + 2);
+        ++ahead;
+      }
     }
+    ok = next >= 0;
     umma_commit(smem_u32(&bars->o_full));
     if (!ok) {
       atomicOr(&g_skl_error, 1u);

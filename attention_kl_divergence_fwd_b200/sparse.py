@@ -25,33 +25,37 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import StreamKLError, _check, autograd, load_library
+from . import _check, autograd, load_library
 
 BLOCK = 64  # keys per block
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _on_device(fn):
-    """Runs an entry point on the device of its first tensor (made current when it is not) and
-    passes the raw stream: the given one, else the current one. Single-token calls take a few
-    microseconds on the GPU, so nothing here costs more than a lookup."""
+    """Runs an entry point on the device of its first tensor, made current when it is not.
+    Single-token calls take a few microseconds on the GPU, so the common path costs one lookup."""
     @functools.wraps(fn)
-    def wrapper(first, *args, stream=None, **kwargs):
-        if not first.is_cuda:
+    def wrapper(first, *args, **kwargs):
+        dev = first.get_device()
+        if dev < 0:
             raise ValueError(f"{fn.__name__}: tensors must be on a CUDA device")
-        dev = first.device.index
-        if stream is not None and stream.device_index != dev:
-            raise ValueError(f"{fn.__name__}: stream on {stream.device}, tensors on {first.device}")
-        if dev != torch._C._cuda_getDevice():
-            with torch.cuda.device(dev):
-                return fn(first, *args, stream=stream, **kwargs)
-        return fn(first, *args, stream=stream, **kwargs)
+        if dev == _current_device():
+            return fn(first, *args, **kwargs)
+        with torch.cuda.device(dev):
+            return fn(first, *args, **kwargs)
     return wrapper
 
 
-def _stream_ptr(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _stream_ptr(stream, dev):
+    if stream is None:
+        return _current_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def num_blocks(n_k: int) -> int:
@@ -60,51 +64,53 @@ def num_blocks(n_k: int) -> int:
 
 
 def _bf16(name, t, dev, like=None):
-    if t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 4 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous 4-D bf16 tensor [B, heads, N, d] on {dev}")
+    if t.dtype is not _BF16 or t.get_device() != dev or t.dim() != 4 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 4-D bf16 tensor [B, heads, N, d] on cuda:{dev}")
     if like is not None and t.shape != like:
         raise ValueError(f"{name} must have shape {tuple(like)}, got {tuple(t.shape)}")
 
 
 def _typed(name, t, dev, dtype, shape):
-    if t.dtype != dtype or t.device != dev or not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"cuda:{dev}")
     return t
 
 
 def _lens(seqlens_k, dev, B):
-    return 0 if seqlens_k is None else _typed("seqlens_k", seqlens_k, dev, torch.int32, (B,)).data_ptr()
+    if seqlens_k is None:
+        return 0
+    return _typed("seqlens_k", seqlens_k, dev, _I32, (B,)).data_ptr()
 
 
-def _workspace(nbytes, device, stream):
+def _workspace(nbytes, like, stream):
     """Scratch of one call; on another stream than the current one it is kept until that
     stream is past the call."""
-    if nbytes < 0:
-        raise StreamKLError(2, "streamkl_sparse_attn_workspace")
-    if nbytes == 0:
+    if nbytes <= 0:
         return None, 0
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws = like.new_empty(nbytes, dtype=torch.uint8)
     if stream is not None:
         ws.record_stream(stream)
     return ws, ws.data_ptr()
 
 
-def _qk_shape(q, k):
-    _bf16("q", q, q.device)
-    _bf16("k", k, q.device)
+def _qk_shape(q, k, dev):
+    _bf16("q", q, dev)
+    _bf16("k", k, dev)
     B, H, n_q, d = q.shape
-    if k.shape[0] != B or k.shape[3] != d:
+    Bk, h_kv, n_k, dk = k.shape
+    if Bk != B or dk != d:
         raise ValueError("inconsistent shapes of q and k")
-    return B, H, k.shape[1], n_q, k.shape[2], d
+    return B, H, h_kv, n_q, n_k, d
 
 
-def _qkv_shape(q, k, v, block_idx):
-    B, H, h_kv, n_q, n_k, d = _qk_shape(q, k)
-    _bf16("v", v, q.device, k.shape)
+def _qkv_shape(q, k, v, block_idx, dev):
+    B, H, h_kv, n_q, n_k, d = _qk_shape(q, k, dev)
+    _bf16("v", v, dev, k.shape)
     if block_idx.dim() != 4:
         raise ValueError("block_idx must be [B, H_sel, N_Q, topk]")
-    h_sel, topk = block_idx.shape[1], block_idx.shape[3]
-    _typed("block_idx", block_idx, q.device, torch.int32, (B, h_sel, n_q, topk))
+    _, h_sel, _, topk = block_idx.shape
+    _typed("block_idx", block_idx, dev, _I32, (B, h_sel, n_q, topk))
     return B, H, h_kv, h_sel, n_q, n_k, d, topk
 
 
@@ -113,22 +119,23 @@ def streamkl_block_mass(q_s, k_s, scale_S: float, causal: bool, lse_s=None, seql
                         mass=None, stream=None):
     """Mass of the map softmax(scale <q_s, k_s>) on every block of 64 keys, averaged over the
     query heads of each K head: fp32 [B, H_kv, N_Q, ceil(N_K / 64)]."""
-    B, H, h_kv, n_q, n_k, d = _qk_shape(q_s, k_s)
+    dev = q_s.get_device()
+    B, H, h_kv, n_q, n_k, d = _qk_shape(q_s, k_s, dev)
     nb = num_blocks(n_k)
     if mass is None:
-        mass = torch.empty(B, h_kv, n_q, nb, device=q_s.device, dtype=torch.float32)
+        mass = q_s.new_empty((B, h_kv, n_q, nb), dtype=_F32)
     else:
-        _typed("mass", mass, q_s.device, torch.float32, (B, h_kv, n_q, nb))
+        _typed("mass", mass, dev, _F32, (B, h_kv, n_q, nb))
     nbytes = ws = lse = 0
     keep = None
     if lse_s is None:
         nbytes = 4 * B * H * n_q * nb
-        keep, ws = _workspace(nbytes, q_s.device, stream)
+        keep, ws = _workspace(nbytes, q_s, stream)
     else:
-        lse = _typed("lse_s", lse_s, q_s.device, torch.float32, (B, H, n_q)).data_ptr()
+        lse = _typed("lse_s", lse_s, dev, _F32, (B, H, n_q)).data_ptr()
     st = load_library().streamkl_block_mass(
-        q_s.data_ptr(), k_s.data_ptr(), _lens(seqlens_k, q_s.device, B), B, H, h_kv, n_q, n_k, d,
-        float(scale_S), int(bool(causal)), lse, ws, nbytes, mass.data_ptr(), _stream_ptr(stream, q_s.device))
+        q_s.data_ptr(), k_s.data_ptr(), _lens(seqlens_k, dev, B), B, H, h_kv, n_q, n_k, d,
+        scale_S, bool(causal), lse, ws, nbytes, mass.data_ptr(), _stream_ptr(stream, dev))
     _check(st, "streamkl_block_mass")
     return mass
 
@@ -139,18 +146,19 @@ def streamkl_block_select(mass, n_k: int, causal: bool, topk: int, n_first: int 
     """The blocks each query reads: int32 [B, H_sel, N_Q, topk], ascending, -1 behind the last."""
     if mass.dim() != 4:
         raise ValueError("mass must be [B, H_sel, N_Q, NB]")
+    dev = mass.get_device()
     B, h_sel, n_q, nb = mass.shape
-    _typed("mass", mass, mass.device, torch.float32, (B, h_sel, n_q, nb))
+    _typed("mass", mass, dev, _F32, (B, h_sel, n_q, nb))
     n_k, topk = int(n_k), int(topk)
     if num_blocks(n_k) != nb:
         raise ValueError(f"mass has {nb} blocks, n_k = {n_k} keys make {num_blocks(n_k)}")
     if block_idx is None:
-        block_idx = torch.empty(B, h_sel, n_q, max(topk, 0), device=mass.device, dtype=torch.int32)
+        block_idx = mass.new_empty((B, h_sel, n_q, max(topk, 0)), dtype=_I32)
     else:
-        _typed("block_idx", block_idx, mass.device, torch.int32, (B, h_sel, n_q, topk))
+        _typed("block_idx", block_idx, dev, _I32, (B, h_sel, n_q, topk))
     st = load_library().streamkl_block_select(
-        mass.data_ptr(), _lens(seqlens_k, mass.device, B), B, h_sel, n_q, n_k, int(bool(causal)), topk,
-        int(n_first), int(n_last), block_idx.data_ptr(), _stream_ptr(stream, mass.device))
+        mass.data_ptr(), _lens(seqlens_k, dev, B), B, h_sel, n_q, n_k, bool(causal), topk,
+        int(n_first), int(n_last), block_idx.data_ptr(), _stream_ptr(stream, dev))
     _check(st, "streamkl_block_select")
     return block_idx
 
@@ -160,22 +168,23 @@ def streamkl_sparse_attn_fwd(q, k, v, block_idx, scale: float, causal: bool, seq
                              out=None, lse=None, stream=None):
     """Attention of every query over its listed blocks: out bf16 [B, H, N_Q, d] and the
     log-sum-exps fp32 [B, H, N_Q]."""
-    B, H, h_kv, h_sel, n_q, n_k, d, topk = _qkv_shape(q, k, v, block_idx)
+    dev = q.get_device()
+    B, H, h_kv, h_sel, n_q, n_k, d, topk = _qkv_shape(q, k, v, block_idx, dev)
     lib = load_library()
     if out is None:
         out = torch.empty_like(q)
     else:
-        _bf16("out", out, q.device, q.shape)
+        _bf16("out", out, dev, q.shape)
     if lse is None:
-        lse = torch.empty(B, H, n_q, device=q.device, dtype=torch.float32)
+        lse = q.new_empty((B, H, n_q), dtype=_F32)
     else:
-        _typed("lse", lse, q.device, torch.float32, (B, H, n_q))
+        _typed("lse", lse, dev, _F32, (B, H, n_q))
     nbytes = lib.streamkl_sparse_attn_workspace(B, H, h_kv, h_sel, n_q, n_k, d, topk, 0)
-    keep, ws = _workspace(max(nbytes, 0), q.device, stream)
+    keep, ws = _workspace(nbytes, q, stream)
     st = lib.streamkl_sparse_attn_fwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), block_idx.data_ptr(), _lens(seqlens_k, q.device, B), B, H,
-        h_kv, h_sel, n_q, n_k, d, topk, float(scale), int(bool(causal)), ws, nbytes,
-        out.data_ptr(), lse.data_ptr(), _stream_ptr(stream, q.device))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), block_idx.data_ptr(), _lens(seqlens_k, dev, B), B, H,
+        h_kv, h_sel, n_q, n_k, d, topk, scale, bool(causal), ws, nbytes,
+        out.data_ptr(), lse.data_ptr(), _stream_ptr(stream, dev))
     _check(st, "streamkl_sparse_attn_fwd")
     return out, lse
 
@@ -184,26 +193,27 @@ def streamkl_sparse_attn_fwd(q, k, v, block_idx, scale: float, causal: bool, seq
 def streamkl_sparse_attn_bwd(q, k, v, out, lse, dout, block_idx, scale: float, causal: bool,
                              seqlens_k=None, dq=None, dk=None, dv=None, stream=None):
     """dQ, dK, dV (bf16, the shapes of q, k, v) from the forward's out and lse."""
-    B, H, h_kv, h_sel, n_q, n_k, d, topk = _qkv_shape(q, k, v, block_idx)
-    _bf16("out", out, q.device, q.shape)
-    _bf16("dout", dout, q.device, q.shape)
-    _typed("lse", lse, q.device, torch.float32, (B, H, n_q))
+    dev = q.get_device()
+    B, H, h_kv, h_sel, n_q, n_k, d, topk = _qkv_shape(q, k, v, block_idx, dev)
+    _bf16("out", out, dev, q.shape)
+    _bf16("dout", dout, dev, q.shape)
+    _typed("lse", lse, dev, _F32, (B, H, n_q))
     grads = []
     for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if g is None:
             g = torch.empty_like(like)
         else:
-            _bf16(name, g, q.device, like.shape)
+            _bf16(name, g, dev, like.shape)
         grads.append(g)
     dq, dk, dv = grads
     lib = load_library()
     nbytes = lib.streamkl_sparse_attn_workspace(B, H, h_kv, h_sel, n_q, n_k, d, topk, 1)
-    keep, ws = _workspace(max(nbytes, 0), q.device, stream)
+    keep, ws = _workspace(nbytes, q, stream)
     st = lib.streamkl_sparse_attn_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
-        block_idx.data_ptr(), _lens(seqlens_k, q.device, B), B, H, h_kv, h_sel, n_q, n_k, d, topk,
-        float(scale), int(bool(causal)), ws, nbytes, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-        _stream_ptr(stream, q.device))
+        block_idx.data_ptr(), _lens(seqlens_k, dev, B), B, H, h_kv, h_sel, n_q, n_k, d, topk,
+        scale, bool(causal), ws, nbytes, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+        _stream_ptr(stream, dev))
     _check(st, "streamkl_sparse_attn_bwd")
     return dq, dk, dv
 
@@ -255,9 +265,8 @@ def block_mass(q_s, k_s, scale: Optional[float] = None, causal: bool = False, ls
     at hand; without them the rows are normalised by their own sums. The default scale is
     1/sqrt(d). Not differentiable: the map is trained by its divergence."""
     scale = 1.0 / math.sqrt(q_s.shape[-1]) if scale is None else float(scale)
-    return streamkl_block_mass(q_s.detach().contiguous(), k_s.detach().contiguous(), scale, causal,
-                               None if lse is None else lse.detach().contiguous(),
-                               _lens_arg(seqlens_k))
+    return streamkl_block_mass(q_s.contiguous(), k_s.contiguous(), scale, causal,
+                               None if lse is None else lse.contiguous(), _lens_arg(seqlens_k))
 
 
 def select_blocks(mass, n_k: int, topk: int, causal: bool = False, n_first: int = 1,
@@ -265,7 +274,7 @@ def select_blocks(mass, n_k: int, topk: int, causal: bool = False, n_first: int 
     """Of the blocks a query sees: the first ``n_first``, the last ``n_last`` and the heaviest of
     the rest, ``topk`` in all: int32 [B, H_sel, N_Q, topk], ascending, -1 behind the last.
     Equal masses go to the lower index, NaN ranks below every number."""
-    return streamkl_block_select(mass.detach().contiguous(), n_k, causal, topk, n_first, n_last,
+    return streamkl_block_select(mass.contiguous(), n_k, causal, topk, n_first, n_last,
                                  _lens_arg(seqlens_k))
 
 
@@ -285,7 +294,8 @@ def sparse_attention(q, k, v, block_idx, scale: Optional[float] = None, causal: 
         out, lse = SparseAttentionFunction.apply(q, k, v, block_idx, lens, scale, bool(causal))
     else:
         out, lse = streamkl_sparse_attn_fwd(q, k, v, block_idx, scale, causal, lens)
-        _after_launch("sparse_attention forward", q.device)
+        if autograd._check_status:
+            autograd._after_launch("sparse_attention forward", q.device)
     return (out, lse) if return_lse else out
 
 

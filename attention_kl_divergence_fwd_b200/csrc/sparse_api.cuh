@@ -88,6 +88,28 @@ int sparse_splits(const skl::SparseArgs& a) {
   return (int)(s < 1 ? 1 : (s > 8 ? 8 : s));
 }
 
+// The same for the tiles of one block (dK, dV; one CTA per SM). A block that every query lists (the
+// first one) has n_tiles steps while the average one has its share of the lists, so with few
+// heads its CTA alone outlasts the rest of the grid. A CTA of a cluster costs about 17 steps
+// (measured: 1024 clusters of two instead of 1024 CTAs take 238 us more at 16384 tokens, 4 K
+// heads), so blocks are split only when the longest one dominates.
+int sparse_kv_splits(const skl::SparseArgs& a) {
+  const double longest = (double)a.n_tiles * (a.P / a.Hkv), heads = (double)a.B * a.Hkv;
+  const double per_tile = a.NB < 1.3 * a.topk ? a.NB : 1.3 * a.topk;
+  int best = 1;
+  double best_cost = 0;
+  for (int s = 1; s <= 8; s *= 2) {
+    const double start = s == 1 ? 2 : 17 * s;
+    const double work = heads * (longest * per_tile + a.NB * start) / sm_count();
+    const double cost = work > longest / s ? work : longest / s;
+    if (s == 1 || cost < 0.9 * best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 bool sparse_direct(const skl::SparseArgs& a) {
   return a.N_Q == 1 && a.G <= 16 && a.NB <= 16384;
 }
@@ -110,6 +132,26 @@ streamkl_status launch_mask(skl::SparseArgs& a, void* ws, cudaStream_t stream) {
   return ok_launch();
 }
 
+// Launches units * cluster CTAs in clusters (plain CTAs for a cluster of one).
+template <typename... Params, typename... Args>
+streamkl_status launch_cluster(void (*kern)(Params...), long long units, int cluster, int threads,
+                               int smem, cudaStream_t stream, const Args&... args) {
+  if (units * cluster >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(units * cluster));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return STREAMKL_OK;
+  cudaGetLastError();
+  return STREAMKL_ERR_LAUNCH;
+}
+
 template <int D, bool QUAD>
 streamkl_status launch_sparse_fwd(const skl::SparseArgs& a, const void* q, const void* k,
                                   const void* v, cudaStream_t stream) {
@@ -123,21 +165,9 @@ streamkl_status launch_sparse_fwd(const skl::SparseArgs& a, const void* q, const
   static std::atomic<bool> done[64] = {};
   if (!set_smem_once(kern, C::SMEM, done)) return STREAMKL_ERR_LAUNCH;
   const bool neg = a.scale < 0.f;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((long long)a.B * a.P * a.n_tiles * a.splits));
-  cfg.blockDim = dim3(skl::kSpThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)a.splits, 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = a.splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a,
-                            skl::idesc_bf16_f32(128, 64, false, false, neg),
-                            skl::idesc_bf16_f32(128, D, false, true)) == cudaSuccess
-             ? STREAMKL_OK
-             : (cudaGetLastError(), STREAMKL_ERR_LAUNCH);
+  return launch_cluster(kern, (long long)a.B * a.P * a.n_tiles, a.splits, skl::kSpThreads, C::SMEM,
+                        stream, mq, mk, mv, a, skl::idesc_bf16_f32(128, 64, false, false, neg),
+                        skl::idesc_bf16_f32(128, D, false, true));
 }
 
 template <int D>
@@ -164,11 +194,13 @@ streamkl_status launch_sparse_bwd(const skl::SparseArgs& a, const void* q, const
   skl::streamkl_sparse_rows_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout), lse, rows,
       a.rows);
-  kk<<<(unsigned)((long long)a.B * a.Hkv * a.NB), skl::kSpDkvThreads, CK::SMEM, stream>>>(
-      mq, mdo, mk, mv, a, i_s, i_dp, skl::idesc_bf16_f32(128, 64, true, true));
-  kq<<<(unsigned)((long long)a.B * a.P * a.n_tiles), skl::kSpDqThreads, CQ::SMEM, stream>>>(
-      mq, mdo, mk, mv, a, i_s, i_dp, skl::idesc_bf16_f32(128, D, false, true));
-  return ok_launch();
+  const streamkl_status st = launch_cluster(
+      kk, (long long)a.B * a.Hkv * a.NB, a.kv_splits, skl::kSpDkvThreads, CK::SMEM, stream, mq, mdo,
+      mk, mv, a, i_s, i_dp, skl::idesc_bf16_f32(128, 64, true, true));
+  if (st != STREAMKL_OK) return st;
+  return launch_cluster(kq, (long long)a.B * a.P * a.n_tiles, a.splits, skl::kSpDqThreads, CQ::SMEM,
+                        stream, mq, mdo, mk, mv, a, i_s, i_dp,
+                        skl::idesc_bf16_f32(128, D, false, true));
 }
 
 template <int D, bool NORM, bool QUAD>
@@ -267,6 +299,8 @@ streamkl_status streamkl_sparse_attn_bwd(const void* q, const void* k, const voi
   a.dv = static_cast<__nv_bfloat16*>(dv);
   char* ws = static_cast<char*>(workspace);
   a.rows = reinterpret_cast<float2*>(ws + mask_bytes(a));
+  a.splits = sparse_splits(a);
+  a.kv_splits = sparse_kv_splits(a);
   const streamkl_status sm = launch_mask(a, ws, stream);
   if (sm != STREAMKL_OK) return sm;
   return d == 128 ? launch_sparse_bwd<128>(a, q, k, v, out, lse, dout, stream)

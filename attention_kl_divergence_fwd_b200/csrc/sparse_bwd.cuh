@@ -118,8 +118,9 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
   SpDqBars* bars = reinterpret_cast<SpDqBars*>(smem + C::OFF_BAR);
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bp = blockIdx.x / a.n_tiles;
-  const SpTile t = sp_tile(a, bp, a.n_tiles - 1 - blockIdx.x % a.n_tiles);
+  const int split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
+  const int bp = unit / a.n_tiles;
+  const SpTile t = sp_tile(a, bp, a.n_tiles - 1 - unit % a.n_tiles);
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->q_full), 1);
@@ -188,6 +189,7 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
       if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
     }
     if (ok && !mbar_wait(smem_u32(&bars->dq_full), 0)) ok = false;
+    if (a.splits > 1 && ok && !mbar_wait(smem_u32(&bars->q_full), 0)) ok = false;
     if (!ok) {
       atomicOr(&g_skl_error, 2u);
       *abort_flag = 1;
@@ -199,7 +201,14 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
         const int k = half * (D / 2) + k0;
         uint32_t o[32];
         if (n > 0) tmem_ld_32_wait(tq + k, o);
-        if (valid) {
+        if (a.splits > 1) {
+          // The copies and products of this CTA are done; its buffers take the partial rows.
+          float* part = reinterpret_cast<float*>(smem) + r * (D + 4) + k;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(part + e) =
+                n > 0 ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0u, 0u, 0u, 0u);
+        } else if (valid) {
           uint4* dst = reinterpret_cast<uint4*>(a.dq + row * D + k);
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
@@ -228,8 +237,9 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
       }
     }
     const uint64_t keep = l2_policy_evict_last();
-    int n = 0;
+    int n = 0, rank = 0;
     auto push = [&](int c, const uint32_t (&u)[4]) -> bool {
+      if (c >= 0 && a.splits > 1 && rank++ % a.splits != split) return true;
       bool fine = true;
       if (lane == 0) {
         SpBlockInfo& f = bars->info[n & 3];
@@ -237,18 +247,20 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
         for (int k = 0; k < 4; ++k) f.w[k] = u[k];
         mbar_arrive(smem_u32(&bars->info_full[n & 3]));
-        if (c >= 0) {
+        {
           const int ks = n % C::NK, vs = n % C::NV;
           const uint32_t kf = smem_u32(&bars->k_full[ks]), vf = smem_u32(&bars->v_full[vs]);
           fine = mbar_wait(smem_u32(&bars->k_empty[ks]), ((n / C::NK) & 1) ^ 1);
-          if (fine) {
+          if (fine && c < 0) {
+            mbar_arrive(kf);  // the MMA thread learns of the end from k_full alone
+          } else if (fine) {
             mbar_arrive_expect_tx(kf, C::SLOT);
             for (int blk = 0; blk < D / 64; ++blk)
               tma_load_3d(sb + C::OFF_K + ks * C::SLOT + blk * (64 * 128), &map_k, kf, blk * 64,
                           c * kSpBlock, t.kv, keep);
             fine = mbar_wait(smem_u32(&bars->v_empty[vs]), ((n / C::NV) & 1) ^ 1);
           }
-          if (fine) {
+          if (fine && c >= 0) {
             mbar_arrive_expect_tx(vf, C::SLOT);
             for (int blk = 0; blk < D / 64; ++blk)
               tma_load_3d(sb + C::OFF_V + vs * C::SLOT + blk * (64 * 128), &map_v, vf, blk * 64,
@@ -280,13 +292,10 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
     const uint32_t lkn0 = sdesc_lo(sb + C::OFF_K, 64 * 128);  // K as [keys][d], MN-major
     bool ok = mbar_wait(smem_u32(&bars->q_full), 0);
     // Waits for K and V of step n: 1, no such step: 0, a wait ran out: -1.
-    auto loaded = [&](int n) -> int {
-      if (!mbar_wait(smem_u32(&bars->info_full[n & 3]), (n >> 2) & 1)) return -1;
+    auto loaded = [&](int n) -> int {  // the entry was written before the arrival on k_full
+      if (!mbar_wait(smem_u32(&bars->k_full[n % C::NK]), (n / C::NK) & 1)) return -1;
       if (bars->info[n & 3].c < 0) return 0;
-      return mbar_wait(smem_u32(&bars->k_full[n % C::NK]), (n / C::NK) & 1) &&
-                     mbar_wait(smem_u32(&bars->v_full[n % C::NV]), (n / C::NV) & 1)
-                 ? 1
-                 : -1;
+      return mbar_wait(smem_u32(&bars->v_full[n % C::NV]), (n / C::NV) & 1) ? 1 : -1;
     };
     auto scores = [&](int n) {
       const int ks = n % C::NK, vs = n % C::NV;
@@ -338,11 +347,34 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
+  if (a.splits > 1) {
+    // dQ = the sum of the cluster's parts, in rank order; row r is summed by CTA r % splits.
+    __syncwarp();
+    cluster_sync();
+    for (int r = split + warp * a.splits; r < a.Qn * a.G; r += 10 * a.splits) {
+      const int g = r / a.Qn, i = t.q0 + r - g * a.Qn;
+      if (i >= a.N_Q) continue;
+#pragma unroll
+      for (int k = lane * 2; k < D; k += 64) {
+        float x = 0.f, y = 0.f;
+        for (int p = 0; p < a.splits; ++p) {
+          const float2 v = ld_cluster_f32x2(cluster_map(sb + (r * (D + 4) + k) * 4, p));
+          x += v.x;
+          y += v.y;
+        }
+        *reinterpret_cast<uint32_t*>(a.dq + ((size_t)(t.h0 + g) * a.N_Q + i) * D + k) =
+            pack_bf16x2(x * a.scale, y * a.scale);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // another CTA may still be reading this one's rows
+  }
 }
 
 // ------------------------------------------------------------------ dK, dV, key-major
 //
-// CTA = one block of 64 keys of one K head; it walks the tiles (of every pack that reads this
+// CTA (or cluster of kv_splits CTAs, which deal the tiles by rank and sum their parts through
+// distributed shared memory) = one block of 64 keys of one K head; it walks the tiles (of every pack that reads this
 // K head) whose word column lists the block. Per tile: S = Q K^T and dP = dO V^T (rows on the
 // lanes, 64 key columns), one thread per row writes P and dS as bf16 into shared memory, then
 //   dV^T += dO^T P  and  dK^T += Q^T dS   (d on the lanes, keys on the columns).
@@ -415,7 +447,8 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Block 0 of every head first: causal maps list the early blocks most.
-  const int kv = blockIdx.x % (a.B * a.Hkv), blk0 = blockIdx.x / (a.B * a.Hkv);
+  const int split = blockIdx.x % a.kv_splits, unit = blockIdx.x / a.kv_splits;
+  const int kv = unit % (a.B * a.Hkv), blk0 = unit / (a.B * a.Hkv);
   const int b = kv / a.Hkv;
   const int nk = sp_len(a.lens, b, a.N_K);
   const int ppk = a.P / a.Hkv;               // packs that read this K head
@@ -519,14 +552,21 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
     if (ok && mine) {
       const float f = wg == 0 ? 1.f : a.scale;
       __nv_bfloat16* dst = wg == 0 ? a.dv : a.dk;
+      float* part = reinterpret_cast<float*>(smem + C::OFF_Q);
       uint32_t v[32];
       if (n > 0) tmem_ld_32_wait(tmem + lane_off + (wg == 0 ? C::TM_DV : C::TM_DK) + 32 * half, v);
+      if (a.kv_splits > 1) {  // fp32 parts [dV, dK][64 keys][D] over the Q and dO buffers
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int key = blk0 * kSpBlock + 32 * half + k;
-        if (key < a.N_K)
-          dst[((size_t)kv * a.N_K + key) * D + col] =
-              __float2bfloat16_rn(n > 0 ? __uint_as_float(v[k]) * f : 0.f);
+        for (int k = 0; k < 32; ++k)
+          part[(wg * 64 + 32 * half + k) * D + col] = n > 0 ? __uint_as_float(v[k]) : 0.f;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int key = blk0 * kSpBlock + 32 * half + k;
+          if (key < a.N_K)
+            dst[((size_t)kv * a.N_K + key) * D + col] =
+                __float2bfloat16_rn(n > 0 ? __uint_as_float(v[k]) * f : 0.f);
+        }
       }
     }
   } else if (warp == 16) {
@@ -542,8 +582,9 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
                     keep);
       }
     }
-    int n = 0;
+    int n = 0, rank = 0;
     auto push = [&](int tile, int p, const uint32_t (&u)[4]) -> bool {
+      if (tile >= 0 && a.kv_splits > 1 && rank++ % a.kv_splits != split) return true;
       bool fine = true;
       if (lane == 0) {
         // Entry n & 7 was last read for step n - 8; loads run at most NQ steps ahead of the
@@ -554,18 +595,20 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
         for (int k = 0; k < 4; ++k) f.w[k] = u[k];
         mbar_arrive(smem_u32(&bars->info_full[n & 7]));
-        if (tile >= 0) {
+        {
           const int sq = n % C::NQ, sd = n % C::ND, head = b * a.H + p * a.G;
+          const uint32_t qf = smem_u32(&bars->q_full[sq]);
           fine = mbar_wait(smem_u32(&bars->q_empty[sq]), ((n / C::NQ) & 1) ^ 1);
-          if (fine) {
-            const uint32_t qf = smem_u32(&bars->q_full[sq]);
+          if (fine && tile < 0) {
+            mbar_arrive(qf);  // the MMA thread learns of the end from q_full alone
+          } else if (fine) {
             mbar_arrive_expect_tx(qf, rows * D * 2);
             for (int blk = 0; blk < D / 64; ++blk)
               tma_load_3d(sb + C::off_q(n) + blk * (128 * 128), &map_q, qf, blk * 64, tile * a.Qn,
                           head, keep);
             fine = mbar_wait(smem_u32(&bars->do_empty[sd]), ((n / C::ND) & 1) ^ 1);
           }
-          if (fine) {
+          if (fine && tile >= 0) {
             const uint32_t df = smem_u32(&bars->do_full[sd]);
             mbar_arrive_expect_tx(df, rows * D * 2);
             for (int blk = 0; blk < D / 64; ++blk)
@@ -623,9 +666,8 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
     // S and dP of step n: 1, no such step: 0, a wait ran out: -1. Score buffer n & 1 was last
     // read for step n - 2, whose P and dS this thread has seen.
     auto scores = [&](int n) -> int {
-      if (!mbar_wait(smem_u32(&bars->info_full[n & 7]), (n >> 3) & 1)) return -1;
-      if (bars->info[n & 7].tile < 0) return 0;
       if (!mbar_wait(smem_u32(&bars->q_full[n % C::NQ]), (n / C::NQ) & 1)) return -1;
+      if (bars->info[n & 7].tile < 0) return 0;  // written before the arrival on q_full
       tc_fence_after();
       const uint32_t ds = tmem + C::TM_S + 128 * (n & 1);
       const uint32_t lq = sdesc_lo(sb + C::off_q(n), 16), ldo = sdesc_lo(sb + C::off_do(n), 16);
@@ -688,6 +730,29 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
   if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
+  }
+  if (a.kv_splits > 1) {
+    // Sums of the cluster's parts in rank order, one row (key of dV or dK) per warp.
+    __syncwarp();
+    cluster_sync();
+    for (int r = split + warp * a.kv_splits; r < 128; r += 18 * a.kv_splits) {
+      const int key = blk0 * kSpBlock + (r & 63);
+      if (key >= a.N_K) continue;
+      const float f = r < 64 ? 1.f : a.scale;
+      __nv_bfloat16* dst = (r < 64 ? a.dv : a.dk) + ((size_t)kv * a.N_K + key) * D;
+#pragma unroll
+      for (int k = lane * 2; k < D; k += 64) {
+        float x = 0.f, y = 0.f;
+        for (int p = 0; p < a.kv_splits; ++p) {
+          const float2 v = ld_cluster_f32x2(cluster_map(sb + C::OFF_Q + (r * D + k) * 4, p));
+          x += v.x;
+          y += v.y;
+        }
+        *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16x2(x * f, y * f);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // another CTA may still be reading this one's parts
   }
 }
 

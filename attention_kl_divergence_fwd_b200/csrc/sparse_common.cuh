@@ -28,7 +28,8 @@ struct SparseArgs {
   int Hkv, Hsel;           // K heads, selection heads (both divide P)
   int Qn, n_tiles;         // queries per 128-row tile, tiles per pack
   int causal, topk;
-  int splits;              // CTAs (one cluster) that share one tile's list (forward)
+  int splits;              // CTAs (one cluster) that share one tile's list (forward, dQ)
+  int kv_splits;           // the same for a block's tiles (dK, dV)
   int direct;              // forward of one query: blocks straight from the list
   float c, scale;          // |scale| * log2(e); signed scale
   const int* idx;          // [B, Hsel, N_Q, topk]

@@ -28,17 +28,11 @@
 // bit matrix, TMA), 9 MMA + TMEM.
 #pragma once
 
-#include "fwd_kernel.cuh"
 #include "sparse_common.cuh"
 
 namespace skl {
 
 constexpr int kSpThreads = 320;
-
-// Pairs of every 8 whose exponentials go to the FMA pipe, in blocks that every row reads whole.
-#ifndef SKL_SP_POLY
-#define SKL_SP_POLY 2
-#endif
 
 // One block as the producer announces it: which (-1 = end), and which queries list it.
 struct SpBlockInfo {
@@ -89,23 +83,18 @@ __device__ __forceinline__ void sp_zero_tail(uint8_t* buf, int first, int tid, i
         make_uint4(0u, 0u, 0u, 0u);
 }
 
-// 2^(v c + bias) of 32 scores as bf16 pairs, and their sum (two packed partial sums). POLY: a share
-// on the FMA pipe, for arguments known to be finite.
-template <bool POLY>
+// 2^(v c + bias) of 32 scores as bf16 pairs, and their sum (two packed partial sums). All on the
+// exponential unit: the loop is bound by issue slots, and a share of polynomial exponentials as in
+// the divergence's forward makes it slower (prompt of 16384 tokens: 660 us without, 686, 718 and
+// 737 us with 1, 2 and 3 of 8 pairs).
 __device__ __forceinline__ void sp_exp32(const uint32_t (&v)[32], uint64_t c2, uint64_t b2,
                                          uint64_t& acc0, uint64_t& acc1, uint32_t (&p)[16]) {
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
-    const uint64_t x =
-        f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, b2);
     float x0, x1;
-    if (POLY && poly_rank((k >> 1) & 7) < SKL_SP_POLY) {
-      f2_unpack(exp2_fma2(x), x0, x1);
-    } else {
-      f2_unpack(x, x0, x1);
-      x0 = ex2_approx(x0);
-      x1 = ex2_approx(x1);
-    }
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, b2), x0, x1);
+    x0 = ex2_approx(x0);
+    x1 = ex2_approx(x1);
     if (k & 2)
       acc1 = f2_add(acc1, f2_pack(x0, x1));
     else
@@ -310,16 +299,19 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           uint32_t v[32], p0[16], p1[16];  // 32 scores at a time: registers are short
           const uint64_t b2 = f2_pack(-m, -m);
           tmem_ld_32_wait(ts, v);
-          sp_exp32<true>(v, c2, b2, acc0, acc1, p0);
+          sp_exp32(v, c2, b2, acc0, acc1, p0);
           tmem_ld_32_wait(ts + 32, v);
-          sp_exp32<true>(v, c2, b2, acc0, acc1, p1);
+          sp_exp32(v, c2, b2, acc0, acc1, p1);
           float s0, s1;
           f2_unpack(f2_add(acc0, acc1), s0, s1);
           float sum = s0 + s1;
-          if (lim < 0) {  // this row does not list the block
-            sum = 0.f;
+          if (__any_sync(0xffffffffu, lim < 0)) {  // rows that do not list the block
+            if (lim < 0) sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) p0[k] = p1[k] = 0u;
+            for (int k = 0; k < 16; ++k) {
+              p0[k] = lim < 0 ? 0u : p0[k];
+              p1[k] = lim < 0 ? 0u : p1[k];
+            }
           }
           if (!reference()) { ok = false; break; }
           if (__all_sync(0xffffffffu, m0 == m && sum < 0x1p64f)) {
@@ -414,7 +406,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           for (int h = 0; h < 64; h += 32) {
             tmem_ld_32_wait(ts + h, v);
             if (single) mask(h);
-            sp_exp32<false>(v, c2, b2, acc0, acc1, p);
+            sp_exp32(v, c2, b2, acc0, acc1, p);
             tmem_st_16(ts + h / 2, p);
           }
         }
@@ -516,15 +508,17 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
         for (int k = 0; k < 4; ++k) f.w[k] = u[k];
         mbar_arrive(smem_u32(&bars->info_full[n & 7]));
-        if (c >= 0) {
+        {
           const int st = n % NST;
           const uint32_t kf = smem_u32(&bars->k_full[st]);
           fine = mbar_wait(smem_u32(&bars->k_empty[st]), ((n / NST) & 1) ^ 1);
-          if (fine) {
+          if (fine && c >= 0) {
             mbar_arrive_expect_tx(kf, C::SLOT);
             for (int blk = 0; blk < D / 64; ++blk)
               tma_load_3d(sb + C::OFF_K + st * C::SLOT + blk * (64 * 128), &map_k, kf, blk * 64,
                           c * kSpBlock, t.kv, keep);
+          } else if (fine) {
+            mbar_arrive(kf);  // the MMA thread learns of the end from k_full alone
           }
         }
         if (fine && n > 0) {
@@ -599,11 +593,11 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     const uint32_t lq = sdesc_lo(sb, 16), lk0 = sdesc_lo(sb + C::OFF_K, 16);
     const uint32_t lv0 = sdesc_lo(sb + C::OFF_V, 64 * 128);
     bool ok = mbar_wait(smem_u32(&bars->q_full), 0);
-    // Waits for K of step n: 1, no such step: 0, a wait ran out: -1.
+    // Waits for K of step n: 1, no such step: 0, a wait ran out: -1. The entry was written before
+    // the producer's arrival on k_full.
     auto keys = [&](int n) -> int {
-      if (!mbar_wait(smem_u32(&bars->info_full[n & 7]), (n >> 3) & 1)) return -1;
-      if (bars->info[n & 7].c < 0) return 0;
-      return mbar_wait(smem_u32(&bars->k_full[n % NST]), (n / NST) & 1) ? 1 : -1;
+      if (!mbar_wait(smem_u32(&bars->k_full[n % NST]), (n / NST) & 1)) return -1;
+      return bars->info[n & 7].c < 0 ? 0 : 1;
     };
     // S of step n. The buffer's last P has been handed to a product issued before.
     auto scores = [&](int n) {

@@ -150,6 +150,8 @@ ATTN = [
     (1, 70, 1, 1, 3, 129, 64, False, 2, None),
     (1, 128, 1, 1, 2, 190, 128, True, 3, None),
     (2, 4, 4, 1, 33, 1100, 128, True, 9, [1100, 40]),
+    (1, 4, 1, 1, 1200, 1200, 128, True, 4, None),   # few K heads: blocks split over clusters
+    (1, 4, 1, 1, 1100, 1250, 64, True, 4, [1190]),
 ]
 
 

@@ -127,7 +127,8 @@ streamkl_status ok_launch() {
 streamkl_status launch_mask(skl::SparseArgs& a, void* ws, cudaStream_t stream) {
   const long long grid = (long long)((a.N_Q + 31) / 32) * a.B * a.Hsel;
   uint32_t* mask = static_cast<uint32_t*>(ws);
-  skl::streamkl_sparse_mask_kernel<<<(unsigned)grid, 128, 0, stream>>>(a, mask);
+  const int smem = 4 * (a.NB < skl::kMaskChunk ? a.NB : skl::kMaskChunk);
+  skl::streamkl_sparse_mask_kernel<<<(unsigned)grid, 256, smem, stream>>>(a, mask);
   a.mask = mask;
   return ok_launch();
 }
@@ -191,7 +192,8 @@ streamkl_status launch_sparse_bwd(const skl::SparseArgs& a, const void* q, const
   const uint32_t i_s = skl::idesc_bf16_f32(128, 64, false, false, neg);
   const uint32_t i_dp = skl::idesc_bf16_f32(128, 64, false, false);
   const long long rows = (long long)a.B * a.H * a.N_Q;
-  skl::streamkl_sparse_rows_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(
+  constexpr int per_cta = 8 * 32 / (D / 8) * skl::kRowsPerGroup;
+  skl::streamkl_sparse_rows_kernel<D><<<(unsigned)((rows + per_cta - 1) / per_cta), 256, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout), lse, rows,
       a.rows);
   const streamkl_status st = launch_cluster(

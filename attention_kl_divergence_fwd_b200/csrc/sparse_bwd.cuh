@@ -16,26 +16,41 @@
 
 namespace skl {
 
-// rows[r] = {LSE * log2(e), sum_d out * dout}: one warp per row.
+// rows[r] = {LSE * log2(e), sum_d out * dout}: D / 8 lanes per row, 16 bytes each, several rows in
+// flight per lane. Bound by reading out and dout once.
+constexpr int kRowsPerGroup = 4;
 template <int D>
 __global__ void __launch_bounds__(256)
 streamkl_sparse_rows_kernel(const __nv_bfloat16* out, const __nv_bfloat16* dout, const float* lse,
                             long long rows, float2* dst) {
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  float acc = 0.f;
+  constexpr int L = D / 8;                       // lanes per row
+  constexpr int GROUPS = 256 / L;                // rows a CTA takes at once
+  const int at = threadIdx.x % L;
+  const long long row0 = (long long)blockIdx.x * (GROUPS * kRowsPerGroup) + threadIdx.x / L;
+  uint4 o[kRowsPerGroup], g[kRowsPerGroup];
 #pragma unroll
-  for (int k = 0; k < D / 64; ++k) {
-    const size_t at = (size_t)row * D + k * 64 + lane * 2;
-    const __nv_bfloat162 o = *reinterpret_cast<const __nv_bfloat162*>(out + at);
-    const __nv_bfloat162 g = *reinterpret_cast<const __nv_bfloat162*>(dout + at);
-    acc = fmaf(__low2float(o), __low2float(g), acc);
-    acc = fmaf(__high2float(o), __high2float(g), acc);
+  for (int k = 0; k < kRowsPerGroup; ++k) {
+    const long long row = row0 + k * GROUPS;
+    o[k] = g[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < rows) {
+      o[k] = __ldg(reinterpret_cast<const uint4*>(out + row * D) + at);
+      g[k] = __ldg(reinterpret_cast<const uint4*>(dout + row * D) + at);
+    }
   }
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
-  if (lane == 0) dst[row] = make_float2(lse[row] * 1.4426950408889634f, acc);
+  for (int k = 0; k < kRowsPerGroup; ++k) {
+    const uint32_t x[4] = {o[k].x, o[k].y, o[k].z, o[k].w}, y[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
+    float acc = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // a bf16 is the upper half of its fp32
+      acc = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), acc);
+      acc = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), acc);
+    }
+#pragma unroll
+    for (int s = L / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
+    const long long row = row0 + k * GROUPS;
+    if (at == 0 && row < rows) dst[row] = make_float2(__ldg(lse + row) * 1.4426950408889634f, acc);
+  }
 }
 
 // ------------------------------------------------------------------ dQ, query-major
@@ -237,30 +252,30 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
       }
     }
     const uint64_t keep = l2_policy_evict_last();
-    int n = 0, rank = 0;
-    auto push = [&](int c, const uint32_t (&u)[4]) -> bool {
-      if (c >= 0 && a.splits > 1 && rank++ % a.splits != split) return true;
-      bool fine = true;
+    SpScan scan;
+    bool ok = true;
+    int n = 0;
+    for (;;) {
+      uint32_t u[4] = {0u, 0u, 0u, 0u};
+      const int c = scan.next(a, t, nullptr, split, lane, u);
       if (lane == 0) {
         SpBlockInfo& f = bars->info[n & 3];
         f.c = c;
 #pragma unroll
         for (int k = 0; k < 4; ++k) f.w[k] = u[k];
         mbar_arrive(smem_u32(&bars->info_full[n & 3]));
-        {
-          const int ks = n % C::NK, vs = n % C::NV;
-          const uint32_t kf = smem_u32(&bars->k_full[ks]), vf = smem_u32(&bars->v_full[vs]);
-          fine = mbar_wait(smem_u32(&bars->k_empty[ks]), ((n / C::NK) & 1) ^ 1);
-          if (fine && c < 0) {
-            mbar_arrive(kf);  // the MMA thread learns of the end from k_full alone
-          } else if (fine) {
-            mbar_arrive_expect_tx(kf, C::SLOT);
-            for (int blk = 0; blk < D / 64; ++blk)
-              tma_load_3d(sb + C::OFF_K + ks * C::SLOT + blk * (64 * 128), &map_k, kf, blk * 64,
-                          c * kSpBlock, t.kv, keep);
-            fine = mbar_wait(smem_u32(&bars->v_empty[vs]), ((n / C::NV) & 1) ^ 1);
-          }
-          if (fine && c >= 0) {
+        const int ks = n % C::NK, vs = n % C::NV;
+        const uint32_t kf = smem_u32(&bars->k_full[ks]), vf = smem_u32(&bars->v_full[vs]);
+        ok = mbar_wait(smem_u32(&bars->k_empty[ks]), ((n / C::NK) & 1) ^ 1);
+        if (ok && c < 0) {
+          mbar_arrive(kf);  // the MMA thread learns of the end from k_full alone
+        } else if (ok) {
+          mbar_arrive_expect_tx(kf, C::SLOT);
+          for (int blk = 0; blk < D / 64; ++blk)
+            tma_load_3d(sb + C::OFF_K + ks * C::SLOT + blk * (64 * 128), &map_k, kf, blk * 64,
+                        c * kSpBlock, t.kv, keep);
+          ok = mbar_wait(smem_u32(&bars->v_empty[vs]), ((n / C::NV) & 1) ^ 1);
+          if (ok) {
             mbar_arrive_expect_tx(vf, C::SLOT);
             for (int blk = 0; blk < D / 64; ++blk)
               tma_load_3d(sb + C::OFF_V + vs * C::SLOT + blk * (64 * 128), &map_v, vf, blk * 64,
@@ -268,18 +283,16 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
           }
         }
       }
-      fine = __shfl_sync(0xffffffffu, fine ? 1 : 0, 0) != 0;
-      if (c >= 0) ++n;
-      return fine;
-    };
-    bool ok = sp_scan(a, t, lane, push);
-    const uint32_t none[4] = {0u, 0u, 0u, 0u};
-    if (ok) ok = push(-1, none);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (c < 0 || !ok) break;
+      ++n;
+    }
     if (!ok && lane == 0) {
       atomicOr(&g_skl_error, 2u);
       *abort_flag = 1;
       mbar_wait(smem_u32(&bars->q_full), 0);
-      for (int j = max(0, n - C::NK); j < n; ++j)
+      // Of step n itself K may not have been asked for; then its wait runs out.
+      for (int j = max(0, n + 1 - C::NK); j <= n; ++j)
         mbar_wait(smem_u32(&bars->k_full[j % C::NK]), (j / C::NK) & 1);
       for (int j = max(0, n - C::NV); j < n; ++j)
         mbar_wait(smem_u32(&bars->v_full[j % C::NV]), (j / C::NV) & 1);
@@ -582,10 +595,44 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
                     keep);
       }
     }
-    int n = 0, rank = 0;
-    auto push = [&](int tile, int p, const uint32_t (&u)[4]) -> bool {
-      if (tile >= 0 && a.kv_splits > 1 && rank++ % a.kv_splits != split) return true;
-      bool fine = true;
+    // The tiles of every pack whose word column lists this block, in turn for a cluster's CTAs; the
+    // end is a step without a tile.
+    const int iws = (a.N_Q + 31) >> 5;
+    bool ok = true;
+    int n = 0, turn = 0, p = p0, base = -32;
+    uint32_t nz = 0u, w[4] = {0u, 0u, 0u, 0u};
+    for (;;) {
+      int tile = -1;
+      uint32_t u[4] = {0u, 0u, 0u, 0u};
+      while (tile < 0) {
+        if (nz == 0u) {
+          base += 32;
+          if (base >= a.n_tiles) {
+            base = 0;
+            ++p;
+          }
+          if (p >= p0 + ppk) break;
+          const uint32_t* col =
+              a.mask + (size_t)(b * a.Hsel + p / (a.P / a.Hsel)) * iws * a.NB + blk0;
+          const int q0 = (base + lane) * a.Qn, iw = q0 >> 5;
+          const uint32_t tmask = a.Qn >= 32 ? 0xffffffffu : ((1u << a.Qn) - 1u) << (q0 & 31);
+          const int nw = base + lane >= a.n_tiles ? 0 : (a.Qn <= 32 ? 1 : min(a.Qn >> 5, iws - iw));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = k < nw ? __ldg(col + (size_t)(iw + k) * a.NB) & tmask : 0u;
+          nz = __ballot_sync(0xffffffffu, (w[0] | w[1] | w[2] | w[3]) != 0u);
+          continue;
+        }
+        const int pos = __ffs(nz) - 1;
+        nz &= nz - 1;
+        const bool mine = turn == split;
+        turn = turn + 1 == a.kv_splits ? 0 : turn + 1;
+        if (mine) {
+          tile = base + pos;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) u[k] = __shfl_sync(0xffffffffu, w[k], pos);
+        }
+      }
       if (lane == 0) {
         // Entry n & 7 was last read for step n - 8; loads run at most NQ steps ahead of the
         // products, which wait for the warps of their step.
@@ -595,20 +642,18 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
         for (int k = 0; k < 4; ++k) f.w[k] = u[k];
         mbar_arrive(smem_u32(&bars->info_full[n & 7]));
-        {
-          const int sq = n % C::NQ, sd = n % C::ND, head = b * a.H + p * a.G;
-          const uint32_t qf = smem_u32(&bars->q_full[sq]);
-          fine = mbar_wait(smem_u32(&bars->q_empty[sq]), ((n / C::NQ) & 1) ^ 1);
-          if (fine && tile < 0) {
-            mbar_arrive(qf);  // the MMA thread learns of the end from q_full alone
-          } else if (fine) {
-            mbar_arrive_expect_tx(qf, rows * D * 2);
-            for (int blk = 0; blk < D / 64; ++blk)
-              tma_load_3d(sb + C::off_q(n) + blk * (128 * 128), &map_q, qf, blk * 64, tile * a.Qn,
-                          head, keep);
-            fine = mbar_wait(smem_u32(&bars->do_empty[sd]), ((n / C::ND) & 1) ^ 1);
-          }
-          if (fine && tile >= 0) {
+        const int sq = n % C::NQ, sd = n % C::ND, head = b * a.H + p * a.G;
+        const uint32_t qf = smem_u32(&bars->q_full[sq]);
+        ok = mbar_wait(smem_u32(&bars->q_empty[sq]), ((n / C::NQ) & 1) ^ 1);
+        if (ok && tile < 0) {
+          mbar_arrive(qf);  // the MMA thread learns of the end from q_full alone
+        } else if (ok) {
+          mbar_arrive_expect_tx(qf, rows * D * 2);
+          for (int blk = 0; blk < D / 64; ++blk)
+            tma_load_3d(sb + C::off_q(n) + blk * (128 * 128), &map_q, qf, blk * 64, tile * a.Qn,
+                        head, keep);
+          ok = mbar_wait(smem_u32(&bars->do_empty[sd]), ((n / C::ND) & 1) ^ 1);
+          if (ok) {
             const uint32_t df = smem_u32(&bars->do_full[sd]);
             mbar_arrive_expect_tx(df, rows * D * 2);
             for (int blk = 0; blk < D / 64; ++blk)
@@ -617,43 +662,16 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
           }
         }
       }
-      fine = __shfl_sync(0xffffffffu, fine ? 1 : 0, 0) != 0;
-      if (tile >= 0) ++n;
-      return fine;
-    };
-    const int iws = (a.N_Q + 31) >> 5;
-    bool ok = true;
-    for (int p = p0; ok && p < p0 + ppk; ++p) {
-      const uint32_t* col =
-          a.mask + (size_t)(b * a.Hsel + p / (a.P / a.Hsel)) * iws * a.NB + blk0;
-      for (int base = 0; ok && base < a.n_tiles; base += 32) {
-        const int tile = base + lane, q0 = tile * a.Qn, iw = q0 >> 5;
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (tile < a.n_tiles) {
-          const uint32_t tmask = a.Qn >= 32 ? 0xffffffffu : ((1u << a.Qn) - 1u) << (q0 & 31);
-          const int nw = a.Qn <= 32 ? 1 : min(a.Qn >> 5, iws - iw);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < nw) w[k] = __ldg(col + (size_t)(iw + k) * a.NB) & tmask;
-        }
-        uint32_t nz = __ballot_sync(0xffffffffu, (w[0] | w[1] | w[2] | w[3]) != 0u);
-        while (ok && nz) {
-          const int pos = __ffs(nz) - 1;
-          nz &= nz - 1;
-          uint32_t u[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) u[k] = __shfl_sync(0xffffffffu, w[k], pos);
-          ok = push(base + pos, p, u);
-        }
-      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (tile < 0 || !ok) break;
+      ++n;
     }
-    const uint32_t none[4] = {0u, 0u, 0u, 0u};
-    if (ok) ok = push(-1, 0, none);
     if (lane == 0) mbar_wait(smem_u32(&bars->k_full), 0);
     if (!ok && lane == 0) {
       atomicOr(&g_skl_error, 2u);
       *abort_flag = 1;
-      for (int j = max(0, n - C::NQ); j < n; ++j)
+      // Of step n itself Q may not have been asked for; then its wait runs out.
+      for (int j = max(0, n + 1 - C::NQ); j <= n; ++j)
         mbar_wait(smem_u32(&bars->q_full[j % C::NQ]), (j / C::NQ) & 1);
       for (int j = max(0, n - C::ND); j < n; ++j)
         mbar_wait(smem_u32(&bars->do_full[j % C::ND]), (j / C::ND) & 1);

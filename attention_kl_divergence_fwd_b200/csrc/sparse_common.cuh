@@ -93,30 +93,43 @@ __host__ __device__ inline bool sp_quad(int Qn, int G) { return Qn * G <= 32; }
 
 // Builds the bit matrix: one CTA per 32 queries of a selection head. Entries that are
 // negative, beyond the last block, or of a block the query may not see set no bit.
-constexpr int kMaskChunk = 8192;  // blocks per pass (32 KB of shared memory)
-__global__ void __launch_bounds__(128)
+constexpr int kMaskChunk = 8192;  // blocks per pass (32 KB of shared memory at most)
+__global__ void __launch_bounds__(256)
 streamkl_sparse_mask_kernel(const SparseArgs a, uint32_t* mask) {
-  __shared__ uint32_t sm[kMaskChunk];
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint32_t* sm = reinterpret_cast<uint32_t*>(smem);
   const int iws = (a.N_Q + 31) >> 5;
   const int sel = blockIdx.x / iws, iw = blockIdx.x - sel * iws, b = sel / a.Hsel, i0 = iw * 32;
   const int nk = sp_len(a.lens, b, a.N_K);
   const int nq = min(32, a.N_Q - i0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int* idx = a.idx + ((size_t)sel * a.N_Q + i0) * a.topk;
   uint32_t* dst = mask + ((size_t)sel * iws + iw) * a.NB;
   for (int c0 = 0; c0 < a.NB; c0 += kMaskChunk) {
     const int n = min(kMaskChunk, a.NB - c0);
-    for (int c = threadIdx.x; c < n; c += blockDim.x) sm[c] = 0u;
+    // The first entries of the warp's four queries are read while shared memory is cleared.
+    int first[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int q = warp + 8 * k;
+      first[k] = q < nq && lane < a.topk ? __ldg(idx + (size_t)q * a.topk + lane) : -1;
+    }
+    for (int c = threadIdx.x; c < n; c += 256) sm[c] = 0u;
     __syncthreads();
-    const int total = nq * a.topk;  // at most 32 * topk, topk < 2^24
-    for (int e = threadIdx.x; e < total; e += blockDim.x) {
-      const int c = __ldg(idx + e), q = e / a.topk;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int q = warp + 8 * k;
+      if (q >= nq) continue;
       const int last = sp_last(i0 + q, nk, a.N_Q, a.causal);
-      // c <= last / 64 keeps c * 64 from being formed for wild entries
-      if (last >= 0 && c >= 0 && c <= last / kSpBlock && c >= c0 && c - c0 < n)
-        atomicOr(&sm[c - c0], 1u << q);
+      // Last block the query sees; c <= that keeps c * 64 from being formed for wild entries.
+      const int top = last < 0 ? -1 : last / kSpBlock;
+      for (int e = lane; e < a.topk; e += 32) {
+        const int c = e == lane ? first[k] : __ldg(idx + (size_t)q * a.topk + e);
+        if (c >= 0 && c <= top && c >= c0 && c - c0 < n) atomicOr(&sm[c - c0], 1u << q);
+      }
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < n; c += blockDim.x) dst[c0 + c] = sm[c];
+    for (int c = threadIdx.x; c < n; c += 256) dst[c0 + c] = sm[c];
     __syncthreads();
   }
 }

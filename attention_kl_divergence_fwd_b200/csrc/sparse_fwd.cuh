@@ -103,31 +103,46 @@ __device__ __forceinline__ void sp_exp32(const uint32_t (&v)[32], uint64_t c2, u
   }
 }
 
-// Producer's walk over the blocks of a tile's union, whole warp: emit(c, w0..w3) for each
-// (w in units of the tile's own bits), in ascending order.
-template <typename Emit>
-__device__ __forceinline__ bool sp_scan(const SparseArgs& a, const SpTile& t, int lane,
-                                        Emit&& emit) {
-  const uint32_t tmask = a.Qn >= 32 ? 0xffffffffu : ((1u << a.Qn) - 1u) << t.bit0;
-  for (int base = 0; base < a.NB; base += 32) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (base + lane < a.NB) {
+// Producer's walk over the blocks of a tile's union, whole warp, in ascending order; of a cluster's
+// CTAs each takes every `splits`-th block. next() returns the block (-1 at the end) and its words;
+// it is called in one place, so that its state stays in registers.
+struct SpScan {
+  int base = -32, turn = 0;
+  uint32_t nz = 0u, w[4] = {0u, 0u, 0u, 0u};
+
+  // bits: the blocks of a single query as a bitmap in shared memory, or null (the bit matrix).
+  __device__ __forceinline__ int next(const SparseArgs& a, const SpTile& t, const uint32_t* bits,
+                                      int split, int lane, uint32_t (&u)[4]) {
+    const uint32_t tmask = a.Qn >= 32 ? 0xffffffffu : ((1u << a.Qn) - 1u) << t.bit0;
+    for (;;) {
+      while (nz == 0u) {
+        base += 32;
+        if (base >= a.NB) return -1;
+        if (bits != nullptr) {
+          nz = bits[base >> 5];
+          w[0] = (nz >> lane) & 1u;
+        } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < t.nwords) w[k] = __ldg(t.words + (size_t)k * a.NB + base + lane) & tmask;
-    }
-    uint32_t nz = __ballot_sync(0xffffffffu, (w[0] | w[1] | w[2] | w[3]) != 0u);
-    while (nz) {
+          for (int k = 0; k < 4; ++k) {
+            w[k] = 0u;
+            if (base + lane < a.NB && k < t.nwords)
+              w[k] = __ldg(t.words + (size_t)k * a.NB + base + lane) & tmask;
+          }
+          nz = __ballot_sync(0xffffffffu, (w[0] | w[1] | w[2] | w[3]) != 0u);
+        }
+      }
       const int pos = __ffs(nz) - 1;
       nz &= nz - 1;
-      uint32_t u[4];
+      const bool mine = turn == split;
+      turn = turn + 1 == a.splits ? 0 : turn + 1;
+      if (mine) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) u[k] = __shfl_sync(0xffffffffu, w[k], pos);
-      if (!emit(base + pos, u)) return false;
+        for (int k = 0; k < 4; ++k) u[k] = __shfl_sync(0xffffffffu, w[k], pos);
+        return base + pos;
+      }
     }
   }
-  return true;
-}
+};
 
 // Joins the partial rows of this cluster's CTAs (and of the four quarters): every source holds
 // rows normalised by its own sum, with stage[slot * (D + 4)] and the base-2 log-sum-exps in l2;
@@ -141,27 +156,40 @@ __device__ __forceinline__ void sp_join(const SparseArgs& a, const SpTile& t, ui
   for (int r = split + warp * a.splits; r < rows; r += 8 * a.splits) {
     const int g = r / a.Qn, i = t.q0 + r - g * a.Qn;
     if (i >= a.N_Q) continue;
+    // At most 8 CTAs x 4 quarters: lane s takes the weight of source s.
     const int srcs = a.splits * NS;
-    float mx = -INFINITY;
-    for (int s = lane; s < srcs; s += 32)
-      mx = fmaxf(mx, ld_cluster_f32(cluster_map(l2 + ((s % NS) * 32 + r) * 4, s / NS)));
+    const float mine =
+        lane < srcs ? ld_cluster_f32(cluster_map(l2 + ((lane % NS) * 32 + r) * 4, lane / NS))
+                    : -INFINITY;
+    float mx = mine;
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-    float acc[D / 32], tot = 0.f;
+    const float w = mx > -INFINITY ? ex2_approx(mine - mx) : 0.f;
+    float tot = w;
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, k);
+    float acc[D / 32];
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
-    if (mx > -INFINITY) {
-#pragma unroll 4
-      for (int s = 0; s < srcs; ++s) {
-        const int slot = (s % NS) * 32 + r;
-        const float w = ex2_approx(ld_cluster_f32(cluster_map(l2 + slot * 4, s / NS)) - mx);
-        tot += w;
-        const uint32_t src = cluster_map(stage + slot * (D + 4) * 4, s / NS);
+    for (int s0 = 0; s0 < srcs; s0 += 8) {
+      float2 o[8][D / 64];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {  // the reads of eight sources in flight
+        const int s = min(s0 + e, srcs - 1);
+        const uint32_t src =
+            cluster_map(stage + ((s % NS) * 32 + r) * (D + 4) * 4, s / NS) + lane * 8;
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) o[e][k] = ld_cluster_f32x2(src + k * 256);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float ws = __shfl_sync(0xffffffffu, w, (s0 + e) & 31);
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {
-          const float2 o = ld_cluster_f32x2(src + (k * 64 + lane * 2) * 4);
-          acc[2 * k] = fmaf(w, o.x, acc[2 * k]);
-          acc[2 * k + 1] = fmaf(w, o.y, acc[2 * k + 1]);
+          if (s0 + e < srcs) {
+            acc[2 * k] = fmaf(ws, o[e][k].x, acc[2 * k]);
+            acc[2 * k + 1] = fmaf(ws, o[e][k].y, acc[2 * k + 1]);
+          }
         }
       }
     }
@@ -491,15 +519,32 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
                       t.h0, l2_policy_evict_first());
     }
     const uint64_t keep = l2_policy_evict_last();
+    // One query: its list as a bitmap over the blocks, in the rows 16-31 of the Q buffer that
+    // the pack's at most 16 rows leave unused (2 KB: 16384 blocks).
+    uint32_t* bits = nullptr;
+    if (a.direct) {
+      bits = reinterpret_cast<uint32_t*>(smem + 16 * 128);
+      const int sel = t.b * a.Hsel + t.p / (a.P / a.Hsel);
+      const int* idx = a.idx + (size_t)sel * a.topk;
+      const int lastkey = sp_last(0, t.nk, 1, a.causal);
+      const int top = lastkey < 0 ? -1 : lastkey / kSpBlock;
+      for (int w = lane; w < (a.NB + 31) / 32; w += 32) bits[w] = 0u;
+      __syncwarp();
+      for (int e = lane; e < a.topk; e += 32) {
+        const int c = __ldg(idx + e);
+        if (c >= 0 && c <= top) atomicOr(&bits[c >> 5], 1u << (c & 31));
+      }
+      __syncwarp();
+    }
+    // Step n: announces the next block and loads its K, then V of the step before: K's slot is free
+    // as soon as S(n - NST) is done, V's only after the product of step n - 1 - NST, and waiting
+    // for that first would hold K back. The end is a step without a block.
+    SpScan scan;
     bool ok = true;
-    int n = 0, rank = 0;
-    // Announces block c as step n and loads its K, then V of the step before: K's slot is free as
-    // soon as S(n - NST) is done, V's only after the product of step n - 1 - NST, and waiting for
-    // that first would hold K back (-1: the end, only V of the last step).
-    int c_prev = -1;
-    auto push = [&](int c, const uint32_t (&u)[4]) -> bool {
-      if (c >= 0 && a.splits > 1 && rank++ % a.splits != split) return true;
-      bool fine = true;
+    int n = 0, c_prev = -1;
+    for (;;) {
+      uint32_t u[4] = {0u, 0u, 0u, 0u};
+      const int c = scan.next(a, t, bits, split, lane, u);
       if (lane == 0) {
         // Entry n & 7 was last read for step n - 8: loads run at most NST + 3 steps ahead of
         // the products, which wait for every softmax warp.
@@ -508,24 +553,21 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
         for (int k = 0; k < 4; ++k) f.w[k] = u[k];
         mbar_arrive(smem_u32(&bars->info_full[n & 7]));
-        {
-          const int st = n % NST;
-          const uint32_t kf = smem_u32(&bars->k_full[st]);
-          fine = mbar_wait(smem_u32(&bars->k_empty[st]), ((n / NST) & 1) ^ 1);
-          if (fine && c >= 0) {
-            mbar_arrive_expect_tx(kf, C::SLOT);
-            for (int blk = 0; blk < D / 64; ++blk)
-              tma_load_3d(sb + C::OFF_K + st * C::SLOT + blk * (64 * 128), &map_k, kf, blk * 64,
-                          c * kSpBlock, t.kv, keep);
-          } else if (fine) {
-            mbar_arrive(kf);  // the MMA thread learns of the end from k_full alone
-          }
+        const uint32_t kf = smem_u32(&bars->k_full[n % NST]);
+        ok = mbar_wait(smem_u32(&bars->k_empty[n % NST]), ((n / NST) & 1) ^ 1);
+        if (ok && c >= 0) {
+          mbar_arrive_expect_tx(kf, C::SLOT);
+          for (int blk = 0; blk < D / 64; ++blk)
+            tma_load_3d(sb + C::OFF_K + (n % NST) * C::SLOT + blk * (64 * 128), &map_k, kf, blk * 64,
+                        c * kSpBlock, t.kv, keep);
+        } else if (ok) {
+          mbar_arrive(kf);  // the MMA thread learns of the end from k_full alone
         }
-        if (fine && n > 0) {
+        if (ok && n > 0) {
           const int st = (n - 1) % NST;
           const uint32_t vf = smem_u32(&bars->v_full[st]);
-          fine = mbar_wait(smem_u32(&bars->v_empty[st]), (((n - 1) / NST) & 1) ^ 1);
-          if (fine) {
+          ok = mbar_wait(smem_u32(&bars->v_empty[st]), (((n - 1) / NST) & 1) ^ 1);
+          if (ok) {
             mbar_arrive_expect_tx(vf, C::SLOT);
             for (int blk = 0; blk < D / 64; ++blk)
               tma_load_3d(sb + C::OFF_V + st * C::SLOT + blk * (64 * 128), &map_v, vf, blk * 64,
@@ -533,54 +575,20 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           }
         }
       }
-      fine = __shfl_sync(0xffffffffu, fine ? 1 : 0, 0) != 0;
-      if (c >= 0) {
-        c_prev = c;
-        ++n;
-      }
-      return fine;
-    };
-    if (a.direct) {
-      // One query: its list as a bitmap over the blocks, in the rows 16-31 of the Q buffer that
-      // the pack's at most 16 rows leave unused (2 KB: 16384 blocks).
-      uint32_t* bits = reinterpret_cast<uint32_t*>(smem + 16 * 128);
-      const int sel = t.b * a.Hsel + t.p / (a.P / a.Hsel);
-      const int* idx = a.idx + (size_t)sel * a.topk;
-      const int lastkey = sp_last(0, t.nk, 1, a.causal);
-      for (int w = lane; w < (a.NB + 31) / 32; w += 32) bits[w] = 0u;
-      __syncwarp();
-      for (int e = lane; e < a.topk; e += 32) {
-        const int c = __ldg(idx + e);
-        if (lastkey >= 0 && c >= 0 && c <= lastkey / kSpBlock) atomicOr(&bits[c >> 5], 1u << (c & 31));
-      }
-      __syncwarp();
-      const uint32_t one[4] = {1u, 0u, 0u, 0u};
-      for (int w0 = 0; ok && w0 < (a.NB + 31) / 32; w0 += 32) {
-        const uint32_t mine = w0 + lane < (a.NB + 31) / 32 ? bits[w0 + lane] : 0u;
-        uint32_t lanes = __ballot_sync(0xffffffffu, mine != 0u);
-        while (ok && lanes) {
-          const int src = __ffs(lanes) - 1;
-          lanes &= lanes - 1;
-          uint32_t w = __shfl_sync(0xffffffffu, mine, src);
-          while (ok && w) {
-            ok = push((w0 + src) * 32 + __ffs(w) - 1, one);
-            w &= w - 1;
-          }
-        }
-      }
-    } else {
-      ok = sp_scan(a, t, lane, push);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (c < 0 || !ok) break;
+      c_prev = c;
+      ++n;
     }
-    const uint32_t none[4] = {0u, 0u, 0u, 0u};
-    if (ok) ok = push(-1, none);
     if (!ok && lane == 0) {
       atomicOr(&g_skl_error, 1u);
       *abort_flag = 1;
       // Let the copies in flight land before the CTA can exit (each wait is bounded).
       mbar_wait(smem_u32(&bars->q_full), 0);
-      for (int j = max(0, n - NST); j < n; ++j) {
+      // Of step n itself K may not have been asked for; then its wait runs out.
+      for (int j = max(0, n + 1 - NST); j <= n; ++j) {
         mbar_wait(smem_u32(&bars->k_full[j % NST]), (j / NST) & 1);
-        if (j < n - 1) mbar_wait(smem_u32(&bars->v_full[j % NST]), (j / NST) & 1);
+        if (j < n) mbar_wait(smem_u32(&bars->v_full[j % NST]), (j / NST) & 1);
       }
     }
     // With no block nothing else waits for the Q copy.

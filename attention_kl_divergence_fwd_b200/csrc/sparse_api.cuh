@@ -111,7 +111,7 @@ int sparse_kv_splits(const skl::SparseArgs& a) {
 }
 
 bool sparse_direct(const skl::SparseArgs& a) {
-  return a.N_Q == 1 && a.G <= 16 && a.NB <= 16384;
+  return a.N_Q == 1 && a.G <= 16 && a.NB <= 16384 && a.topk <= 512;
 }
 
 long long fwd_ws_bytes(const skl::SparseArgs& a) { return sparse_direct(a) ? 0 : mask_bytes(a); }

@@ -257,7 +257,7 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
     int n = 0;
     for (;;) {
       uint32_t u[4] = {0u, 0u, 0u, 0u};
-      const int c = scan.next(a, t, nullptr, split, lane, u);
+      const int c = scan.next(a, t, split, lane, u);
       if (lane == 0) {
         SpBlockInfo& f = bars->info[n & 3];
         f.c = c;

@@ -110,26 +110,20 @@ struct SpScan {
   int base = -32, turn = 0;
   uint32_t nz = 0u, w[4] = {0u, 0u, 0u, 0u};
 
-  // bits: the blocks of a single query as a bitmap in shared memory, or null (the bit matrix).
-  __device__ __forceinline__ int next(const SparseArgs& a, const SpTile& t, const uint32_t* bits,
-                                      int split, int lane, uint32_t (&u)[4]) {
+  __device__ __forceinline__ int next(const SparseArgs& a, const SpTile& t, int split, int lane,
+                                      uint32_t (&u)[4]) {
     const uint32_t tmask = a.Qn >= 32 ? 0xffffffffu : ((1u << a.Qn) - 1u) << t.bit0;
     for (;;) {
       while (nz == 0u) {
         base += 32;
         if (base >= a.NB) return -1;
-        if (bits != nullptr) {
-          nz = bits[base >> 5];
-          w[0] = (nz >> lane) & 1u;
-        } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            w[k] = 0u;
-            if (base + lane < a.NB && k < t.nwords)
-              w[k] = __ldg(t.words + (size_t)k * a.NB + base + lane) & tmask;
-          }
-          nz = __ballot_sync(0xffffffffu, (w[0] | w[1] | w[2] | w[3]) != 0u);
+        for (int k = 0; k < 4; ++k) {
+          w[k] = 0u;
+          if (base + lane < a.NB && k < t.nwords)
+            w[k] = __ldg(t.words + (size_t)k * a.NB + base + lane) & tmask;
         }
+        nz = __ballot_sync(0xffffffffu, (w[0] | w[1] | w[2] | w[3]) != 0u);
       }
       const int pos = __ffs(nz) - 1;
       nz &= nz - 1;
@@ -144,64 +138,94 @@ struct SpScan {
   }
 };
 
-// Joins the partial rows of this cluster's CTAs (and of the four quarters): every source holds
-// rows normalised by its own sum, with stage[slot * (D + 4)] and the base-2 log-sum-exps in l2;
-// out = sum_s 2^(l_s - L) o_s, L = log2 sum_s 2^(l_s). Row r is joined by CTA r % splits, one
-// warp per row.
+// One row from `srcs` partial ones (at most 8), each normalised by its own sum: out =
+// sum_s 2^(l_s - L) o_s, L = log2 sum_s 2^(l_s). Source s's row and log-sum-exp are at the shared
+// addresses row_at(s) and l2_at(s) (of any CTA of the cluster). One warp; lane holds the columns
+// 2 lane, 2 lane + 1 of every 64. All reads are in flight at once.
+template <int D, typename RowAt, typename L2At>
+__device__ __forceinline__ float sp_join_row(int srcs, int lane, RowAt row_at, L2At l2_at,
+                                             float (&acc)[D / 32]) {
+  const float mine = lane < srcs ? ld_cluster_f32(l2_at(lane)) : -INFINITY;
+  float2 o[8][D / 64];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+      if (e < srcs) o[e][k] = ld_cluster_f32x2(row_at(e) + k * 256 + lane * 8);
+  }
+  float mx = mine;
+#pragma unroll
+  for (int k = 4; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+  mx = __shfl_sync(0xffffffffu, mx, 0);
+  float w = mx > -INFINITY ? ex2_approx(mine - mx) : 0.f, tot = w;
+#pragma unroll
+  for (int k = 4; k > 0; k >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, k);
+  tot = __shfl_sync(0xffffffffu, tot, 0);
+  w *= tot > 0.f ? 1.f / tot : 0.f;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float ws = __shfl_sync(0xffffffffu, w, e);
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+      if (e < srcs) {
+        acc[2 * k] = fmaf(ws, o[e][k].x, acc[2 * k]);
+        acc[2 * k + 1] = fmaf(ws, o[e][k].y, acc[2 * k + 1]);
+      }
+  }
+  return tot > 0.f ? mx + log2f(tot) : -INFINITY;
+}
+
+// Joins the partial rows of this CTA's four quarters (QUAD), then those of the cluster's CTAs:
+// row r is joined by CTA r % splits. Slot s of a CTA is at stage + s * (D + 4) floats.
 template <int D, bool QUAD>
 __device__ __forceinline__ void sp_join(const SparseArgs& a, const SpTile& t, uint32_t stage,
-                                        uint32_t l2, int split, int warp, int lane) {
-  constexpr int NS = QUAD ? 4 : 1;
+                                        float* l2, int split, int warp, int lane) {
   const int rows = a.Qn * a.G;
-  for (int r = split + warp * a.splits; r < rows; r += 8 * a.splits) {
+  const uint32_t l2a = smem_u32(l2);
+  float acc[D / 32];
+  auto write = [&](int r, float l) {
     const int g = r / a.Qn, i = t.q0 + r - g * a.Qn;
-    if (i >= a.N_Q) continue;
-    // At most 8 CTAs x 4 quarters: lane s takes the weight of source s.
-    const int srcs = a.splits * NS;
-    const float mine =
-        lane < srcs ? ld_cluster_f32(cluster_map(l2 + ((lane % NS) * 32 + r) * 4, lane / NS))
-                    : -INFINITY;
-    float mx = mine;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-    const float w = mx > -INFINITY ? ex2_approx(mine - mx) : 0.f;
-    float tot = w;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, k);
-    float acc[D / 32];
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
-    for (int s0 = 0; s0 < srcs; s0 += 8) {
-      float2 o[8][D / 64];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {  // the reads of eight sources in flight
-        const int s = min(s0 + e, srcs - 1);
-        const uint32_t src =
-            cluster_map(stage + ((s % NS) * 32 + r) * (D + 4) * 4, s / NS) + lane * 8;
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) o[e][k] = ld_cluster_f32x2(src + k * 256);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float ws = __shfl_sync(0xffffffffu, w, (s0 + e) & 31);
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) {
-          if (s0 + e < srcs) {
-            acc[2 * k] = fmaf(ws, o[e][k].x, acc[2 * k]);
-            acc[2 * k + 1] = fmaf(ws, o[e][k].y, acc[2 * k + 1]);
-          }
-        }
-      }
-    }
-    const float inv = tot > 0.f ? 1.f / tot : 0.f;
+    if (i >= a.N_Q) return;
     const size_t row = (size_t)(t.h0 + g) * a.N_Q + i;
 #pragma unroll
     for (int k = 0; k < D / 64; ++k)
       *reinterpret_cast<uint32_t*>(a.out + row * D + k * 64 + lane * 2) =
-          pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    if (lane == 0)
-      a.lse[row] = tot > 0.f ? (mx + log2f(tot)) * 0.69314718055994530942f : -INFINITY;
+          pack_bf16x2(acc[2 * k], acc[2 * k + 1]);
+    if (lane == 0) a.lse[row] = l * 0.69314718055994530942f;
+  };
+  if (QUAD && warp < 8) {
+    for (int r = warp; r < rows; r += 8) {
+      const float l = sp_join_row<D>(
+          4, lane, [&](int s) { return stage + (s * 32 + r) * (D + 4) * 4; },
+          [&](int s) { return l2a + (s * 32 + r) * 4; }, acc);
+      if (a.splits == 1) {
+        write(r, l);
+        continue;
+      }
+      float* dst = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(l2) + (stage - l2a)) +
+                   r * (D + 4);
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k)
+        *reinterpret_cast<float2*>(dst + k * 64 + lane * 2) = make_float2(acc[2 * k], acc[2 * k + 1]);
+      if (lane == 0) l2[r] = l;
+    }
   }
+  if (a.splits == 1) return;
+  __syncwarp();
+  cluster_sync();
+  if (warp < 8) {
+    for (int r = split + warp * a.splits; r < rows; r += 8 * a.splits) {
+      const float l = sp_join_row<D>(
+          a.splits, lane, [&](int s) { return cluster_map(stage + r * (D + 4) * 4, s); },
+          [&](int s) { return cluster_map(l2a + r * 4, s); }, acc);
+      write(r, l);
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // another CTA may still be reading this one's rows
 }
 
 template <int D, bool QUAD>
@@ -519,21 +543,39 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
                       t.h0, l2_policy_evict_first());
     }
     const uint64_t keep = l2_policy_evict_last();
-    // One query: its list as a bitmap over the blocks, in the rows 16-31 of the Q buffer that
-    // the pack's at most 16 rows leave unused (2 KB: 16384 blocks).
-    uint32_t* bits = nullptr;
+    // One query: its list becomes a bitmap over the blocks (repeats fall away) and that the
+    // ascending list of this CTA's share, both in rows of the Q buffer that the copies of the
+    // pack's at most 16 rows leave unused: 16-31 (2 KB: 16384 blocks) and 48-63 (512 entries).
+    int* list = reinterpret_cast<int*>(smem + 48 * 128);
+    int listed = 0;
     if (a.direct) {
-      bits = reinterpret_cast<uint32_t*>(smem + 16 * 128);
+      uint32_t* bits = reinterpret_cast<uint32_t*>(smem + 16 * 128);
       const int sel = t.b * a.Hsel + t.p / (a.P / a.Hsel);
       const int* idx = a.idx + (size_t)sel * a.topk;
       const int lastkey = sp_last(0, t.nk, 1, a.causal);
       const int top = lastkey < 0 ? -1 : lastkey / kSpBlock;
-      for (int w = lane; w < (a.NB + 31) / 32; w += 32) bits[w] = 0u;
+      const int words = (a.NB + 31) / 32;
+      for (int w = lane; w < words; w += 32) bits[w] = 0u;
       __syncwarp();
       for (int e = lane; e < a.topk; e += 32) {
         const int c = __ldg(idx + e);
         if (c >= 0 && c <= top) atomicOr(&bits[c >> 5], 1u << (c & 31));
       }
+      __syncwarp();
+      int before = 0;  // blocks of earlier words
+      for (int w0 = 0; w0 < words; w0 += 32) {
+        uint32_t mine = w0 + lane < words ? bits[w0 + lane] : 0u;
+        int upto = __popc(mine);
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, upto, k);
+          upto += lane >= k ? x : 0;
+        }
+        for (int rank = before + upto - __popc(mine); mine != 0u; ++rank, mine &= mine - 1)
+          if (rank % a.splits == split) list[rank / a.splits] = (w0 + lane) * 32 + __ffs(mine) - 1;
+        before += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      listed = (before - split + a.splits - 1) / a.splits;  // before >= 0, split < splits
       __syncwarp();
     }
     // Step n: announces the next block and loads its K, then V of the step before: K's slot is free
@@ -544,7 +586,13 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     int n = 0, c_prev = -1;
     for (;;) {
       uint32_t u[4] = {0u, 0u, 0u, 0u};
-      const int c = scan.next(a, t, bits, split, lane, u);
+      int c;
+      if (a.direct) {
+        c = n < listed ? list[n] : -1;
+        u[0] = 1u;
+      } else {
+        c = scan.next(a, t, split, lane, u);
+      }
       if (lane == 0) {
         // Entry n & 7 was last read for step n - 8: loads run at most NST + 3 steps ahead of
         // the products, which wait for every softmax warp.
@@ -663,12 +711,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
-  __syncwarp();
-  if (a.splits > 1) cluster_sync();
-  if ((QUAD || a.splits > 1) && warp < 8)
-    sp_join<D, QUAD>(a, t, sb, smem_u32(bars->l2), split, warp, lane);
-  __syncwarp();
-  if (a.splits > 1) cluster_sync();  // another CTA may still be reading this one's rows
+  if (QUAD || a.splits > 1) sp_join<D, QUAD>(a, t, sb, bars->l2, split, warp, lane);
 }
 
 }  // namespace skl

@@ -36,7 +36,7 @@ EXPORTS = ("streamkl_fwd", "streamkl_bwd", "streamkl_bwd_teacher", "streamkl_fwd
            "streamkl_bwd_varlen", "streamkl_bwd_teacher_varlen", "streamkl_fwd_partial",
            "streamkl_merge_partial", "streamkl_bwd_shard", "streamkl_bwd_teacher_shard",
            "streamkl_watchdog_selftest", "streamkl_exp2_eval", "streamkl_sm_clock_probe",
-           "streamkl_block_mass", "streamkl_block_select", "streamkl_sparse_attn_workspace",
+           "streamkl_block_mass", "streamkl_block_mass_workspace", "streamkl_block_select", "streamkl_sparse_attn_workspace",
            "streamkl_sparse_attn_fwd", "streamkl_sparse_attn_bwd",
            "streamkl_status_string",
            "streamkl_device_status", "streamkl_version")
@@ -101,6 +101,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     ll = ctypes.c_longlong
     lib.streamkl_block_mass.argtypes = [vp] * 3 + [i] * 6 + [f, i, vp, vp, ll, vp, vp]
     lib.streamkl_block_mass.restype = i
+    lib.streamkl_block_mass_workspace.argtypes = [i] * 6
+    lib.streamkl_block_mass_workspace.restype = ll
     lib.streamkl_block_select.argtypes = [vp, vp] + [i] * 8 + [vp, vp]
     lib.streamkl_block_select.restype = i
     lib.streamkl_sparse_attn_workspace.argtypes = [i] * 9

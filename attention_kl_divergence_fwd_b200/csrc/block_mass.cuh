@@ -8,10 +8,15 @@
 // score buffers; one thread per row reduces each block's 64 scores to one number. The row
 // numbers of 32 blocks are staged in shared memory, summed over the heads of the group and
 // written as 128 contiguous bytes per query.
-// With the LSEs at hand (the divergence's forward has them) that is the result. Without them
-// (NORM = false) the kernel writes per head the block's base-2 log-sum-exp, and a second kernel
-// sums those to the row's LSE: the scores of a block need no running maximum across blocks,
-// so the keys of one query can be spread over as many CTAs as there are pairs of blocks.
+// Three forms (MODE):
+//   kMassNorm   the rows' LSEs are given (the divergence's forward has them): that is the result;
+//   kMassParts  per head the block's base-2 log-sum-exp is written, and a second kernel sums those
+//               to the row's LSE and normalises;
+//   kMassFused  (QUAD) a cluster shares a tile's blocks, keeps the block log-sum-exps in shared
+//               memory, exchanges the rows' sums through distributed shared memory and writes
+//               normalised masses: single tokens in one launch without a workspace.
+// The scores of a block need no running maximum across blocks, so the keys of one query can be
+// spread over as many CTAs as there are pairs of blocks.
 // Bound by the exponential unit (one exponential per pair) for many queries, by reading K for
 // few. Two CTAs per SM.
 //
@@ -27,13 +32,16 @@
 
 namespace skl {
 
+constexpr int kMassNorm = 0, kMassParts = 1, kMassFused = 2;
+constexpr int kMassStage = 128 * 33;  // staged values (floats)
+
 struct MassArgs {
   SparseArgs s;         // P = K heads of the map, G = query heads per K head
   int bpc;              // blocks per CTA (a multiple of 2), n_chunks = ceil(NB / bpc)
   int n_chunks;
-  const float* row_lse; // [B, H, N_Q] (NORM)
-  float* mass;          // [B, P, N_Q, NB] (NORM)
-  float* blse;          // [B, H, N_Q, NB] base-2 log-sum-exp of each visible block (!NORM)
+  const float* row_lse; // [B, H, N_Q] (kMassNorm)
+  float* mass;          // [B, P, N_Q, NB]
+  float* blse;          // [B, H, N_Q, NB] base-2 log-sum-exp of each visible block (kMassParts)
 };
 
 template <int D>
@@ -44,8 +52,8 @@ struct MassCfg {
   static constexpr int NST = D == 128 ? 2 : 4;
   static constexpr int OFF_K = QBYTES;
   static constexpr int OFF_STG = OFF_K + NST * KBYTES;  // [128 rows][33] floats
-  static constexpr int OFF_BAR = OFF_STG + 128 * 33 * 4;
-  static constexpr int SMEM = OFF_BAR + 256;
+  static constexpr int OFF_BAR = OFF_STG + kMassStage * 4;
+  static constexpr int SMEM = OFF_BAR + 512;
   static constexpr int TM_COLS = 256;
   static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs per SM");
 };
@@ -57,8 +65,9 @@ struct MassBars {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
+  float2 row[32];  // kMassFused: {maximum, sum relative to it} of this CTA's blocks, per row
 };
-static_assert(sizeof(MassBars) <= 256, "barrier block");
+static_assert(sizeof(MassBars) <= 512, "barrier block");
 
 constexpr int kMassThreads = 320;
 
@@ -120,12 +129,14 @@ __device__ __forceinline__ float mass_block(const uint32_t (&v)[N], float c, flo
   return NORM ? sum : log2f(sum) - bias;
 }
 
-template <int D, bool NORM, bool QUAD>
+template <int D, int MODE, bool QUAD>
 __global__ void __launch_bounds__(kMassThreads, 2)
 streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k, const MassArgs ma,
                            const uint32_t idesc) {
   using C = MassCfg<D>;
+  constexpr bool NORM = MODE == kMassNorm;
+  static_assert(MODE != kMassFused || QUAD, "the fused form is for tiles of few rows");
   const SparseArgs& a = ma.s;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
@@ -148,7 +159,7 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
   const int last_tile = sp_last(min(q0 + a.Qn, a.N_Q) - 1, nk, a.N_Q, a.causal);
   const int n_vis = min(c_end, last_tile / kSpBlock + (last_tile >= 0 ? 1 : 0)) - c_begin;
   const int steps = n_vis > 0 ? (n_vis + 1) / 2 : 0;
-  if (!NORM && steps == 0) return;
+  if (MODE == kMassParts && steps == 0) return;
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->q_full), 1);
@@ -189,6 +200,7 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
       row_on = l != -INFINITY;
       nl = row_on ? -l * 1.4426950408889634f : 0.f;
     }
+    const int rows = a.Qn * a.G;
     // Queries of this tile that exist; rows are written for those only.
     const int nq = min(a.Qn, a.N_Q - q0);
     const float inv_g = 1.f / (float)a.G;
@@ -240,7 +252,11 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
             const float z = mass_block<NORM, 32>(v, c, nl, 31);
             x = lim >= 31 ? z : (lim >= 0 ? y : x);
           }
-          stage[((quarter & 1) * 32 + r) * 33 + ((cb + (quarter >> 1)) & 31)] = x;
+          if constexpr (MODE == kMassFused) {
+            if (valid) stage[((quarter & 1) * rows + r) * (ma.bpc + 1) + cb + (quarter >> 1)] = x;
+          } else {
+            stage[((quarter & 1) * 32 + r) * 33 + ((cb + (quarter >> 1)) & 31)] = x;
+          }
         } else {
           if (warp_live) {
             uint32_t v[64];
@@ -261,7 +277,7 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[s & 1]));
       }
-      if (((cb + 2) & 31) == 0 || s == steps - 1) {
+      if (MODE != kMassFused && (((cb + 2) & 31) == 0 || s == steps - 1)) {
         const int cg = cb & ~31;
         flush(c_begin + cg, min(cb + 2, n_blocks) - cg);
       }
@@ -269,6 +285,34 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
     if (!ok) {
       atomicOr(&g_skl_error, 1u);
       *abort_flag = 1;
+    }
+    if constexpr (MODE == kMassFused) {
+      // Per row: the two halves of every block joined into the first, and the chunk's sum.
+      named_bar_sync(1, 256);
+      const int ld = ma.bpc + 1, have = min(2 * steps, max(n_blocks, 0));
+      for (int row = warp; row < rows; row += 8) {
+        float* x = stage + row * ld;
+        const float* y = stage + (rows + row) * ld;
+        float m = -INFINITY, sum = 0.f;
+        for (int k = lane; k < have; k += 32) {
+          const float lo = x[k], hi = y[k], t = fmaxf(lo, hi);
+          const float v = t == -INFINITY ? t : t + log2f(exp2f(lo - t) + exp2f(hi - t));
+          x[k] = v;
+          if (v > m) {
+            sum = sum * exp2f(m - v) + 1.f;
+            m = v;
+          } else if (v > -INFINITY) {
+            sum += exp2f(v - m);
+          }
+        }
+        float mx = m;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+        sum = m > -INFINITY ? sum * exp2f(m - mx) : 0.f;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        if (lane == 0) bars->row[row] = make_float2(mx, sum);
+      }
     }
     if (NORM) {  // blocks that no query of the tile sees
       const int z0 = c_begin + min(2 * steps, n_blocks);
@@ -339,9 +383,48 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
+  if constexpr (MODE == kMassFused) {
+    // The rows' log-sum-exps over the whole cluster, then mass = 1/G sum_g 2^(x_g - L_g).
+    __syncwarp();
+    cluster_sync();
+    if (warp < 8) {
+      const int rows = a.Qn * a.G, ld = ma.bpc + 1;
+      const int have = min(2 * steps, max(c_end - c_begin, 0));
+      float big = 0.f;  // lane = row
+      if (lane < rows) {
+        float2 part[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          part[e] = e < ma.n_chunks ? ld_cluster_f32x2(cluster_map(smem_u32(&bars->row[lane]), e))
+                                    : make_float2(-INFINITY, 0.f);
+        float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, part[e].x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (part[e].x > -INFINITY) sum += part[e].y * exp2f(part[e].x - mx);
+        big = sum > 0.f ? mx + log2f(sum) : 0.f;  // a row without keys: every x is -inf
+      }
+      const float inv_g = 1.f / (float)a.G;
+      const int nq = min(a.Qn, a.N_Q - q0);
+      float* dst = ma.mass + ((size_t)bp * a.N_Q + q0) * a.NB + c_begin;
+      for (int q = 0; q < nq; ++q)
+        for (int k0 = warp * 32; k0 < c_end - c_begin; k0 += 256) {
+          const int k = k0 + lane;
+          float s = 0.f;
+          for (int g = 0; g < a.G; ++g) {
+            const float l = __shfl_sync(0xffffffffu, big, g * a.Qn + q);
+            if (k < have) s += exp2f(stage[(g * a.Qn + q) * ld + k] - l);
+          }
+          if (k < c_end - c_begin) dst[(size_t)q * a.NB + k] = s * inv_g;
+        }
+    }
+    __syncwarp();
+    cluster_sync();  // another CTA may still be reading this one's rows
+  }
 }
 
-// Second kernel of the form without LSEs: mass[c] = 1/G sum_g 2^(x_gc - L_g), with
+// Second kernel of kMassParts: mass[c] = 1/G sum_g 2^(x_gc - L_g), with
 // L_g = log2 sum_c 2^(x_gc) over the row's visible blocks. One CTA per (K head, query): each warp
 // takes the sums of every eighth head, then all threads the blocks.
 __global__ void __launch_bounds__(256) streamkl_block_norm_kernel(const MassArgs ma) {

@@ -205,7 +205,24 @@ streamkl_status launch_sparse_bwd(const skl::SparseArgs& a, const void* q, const
                         skl::idesc_bf16_f32(128, D, false, true));
 }
 
-template <int D, bool NORM, bool QUAD>
+// CTAs of the cluster that normalises a tile of few rows on chip (kMassFused), 0 for the two-kernel
+// form: as many as the portable cluster size allows while every CTA gets a pair of blocks. Only
+// while all clusters fit on the chip at once (two CTAs per SM) and a CTA's share of the values
+// fits its shared memory: 16 sequences of up to 32768 keys and 8 K heads (1024 CTAs) take 93 us
+// in clusters, where CTAs without keys hold their SM until the cluster ends, and 73 us as two
+// kernels; one sequence of 4097 keys 7.3 us and one launch instead of 7.2 us and two.
+int mass_fused(const skl::SparseArgs& a) {
+  if (!skl::sp_quad(a.Qn, a.G)) return 0;
+  int s = (a.NB + 1) / 2;
+  s = s > 8 ? 8 : s;
+  if ((long long)a.B * a.P * a.n_tiles * s > 2ll * sm_count()) return 0;
+  const long long bpc = ((a.NB + s - 1) / s + 1) / 2 * 2;
+  return 2ll * a.Qn * a.G * (bpc + 1) <= skl::kMassStage ? s : 0;
+}
+
+long long mass_ws_bytes(const skl::SparseArgs& a) { return 4ll * a.B * a.H * a.N_Q * a.NB; }
+
+template <int D, int MODE, bool QUAD>
 streamkl_status launch_mass(const skl::MassArgs& ma, const void* q, const void* k,
                             cudaStream_t stream) {
   using C = skl::MassCfg<D>;
@@ -214,16 +231,15 @@ streamkl_status launch_mass(const skl::MassArgs& ma, const void* q, const void* 
   if (!make_map_heads(&mq, q, D, a.N_Q, (long long)a.B * a.H, a.Qn, a.G) ||
       !make_map_heads(&mk, k, D, a.N_K, (long long)a.B * a.P, 128, 1))
     return STREAMKL_ERR_LAUNCH;
-  auto kern = skl::streamkl_block_mass_kernel<D, NORM, QUAD>;
+  auto kern = skl::streamkl_block_mass_kernel<D, MODE, QUAD>;
   static std::atomic<bool> done[64] = {};
   if (!set_smem_once(kern, C::SMEM, done)) return STREAMKL_ERR_LAUNCH;
-  const long long grid = (long long)a.B * a.P * a.n_tiles * ma.n_chunks;
-  if (grid >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
-  kern<<<(unsigned)grid, skl::kMassThreads, C::SMEM, stream>>>(
-      mq, mk, ma, skl::idesc_bf16_f32(128, 128, false, false, a.scale < 0.f));
-  if (!NORM)
-    skl::streamkl_block_norm_kernel<<<(unsigned)((long long)a.B * a.P * a.N_Q), 256, 0, stream>>>(
-        ma);
+  const streamkl_status st = launch_cluster(
+      kern, (long long)a.B * a.P * a.n_tiles * (MODE == skl::kMassFused ? 1 : ma.n_chunks),
+      MODE == skl::kMassFused ? ma.n_chunks : 1, skl::kMassThreads, C::SMEM, stream, mq, mk, ma,
+      skl::idesc_bf16_f32(128, 128, false, false, a.scale < 0.f));
+  if (st != STREAMKL_OK || MODE != skl::kMassParts) return st;
+  skl::streamkl_block_norm_kernel<<<(unsigned)((long long)a.B * a.P * a.N_Q), 256, 0, stream>>>(ma);
   return ok_launch();
 }
 
@@ -241,6 +257,12 @@ long long streamkl_sparse_attn_workspace(int B, int H, int H_kv, int H_sel, int 
   return backward ? bwd_ws_bytes(a) : fwd_ws_bytes(a);
 }
 
+long long streamkl_block_mass_workspace(int B, int H, int H_kv, int N_Q, int N_K, int d) {
+  skl::SparseArgs a{};
+  if (sparse_problem(a, nullptr, B, H, H_kv, H_kv, N_Q, N_K, d, 1.f, 0) != STREAMKL_OK) return -1;
+  return mass_fused(a) ? 0 : mass_ws_bytes(a);
+}
+
 streamkl_status streamkl_sparse_attn_fwd(const void* q, const void* k, const void* v,
                                          const int* block_idx, const int* seqlens_k, int B, int H,
                                          int H_kv, int H_sel, int N_Q, int N_K, int d, int topk,
@@ -251,7 +273,7 @@ streamkl_status streamkl_sparse_attn_fwd(const void* q, const void* k, const voi
   const streamkl_status st =
       sparse_problem(a, seqlens_k, B, H, H_kv, H_sel, N_Q, N_K, d, scale, causal);
   if (st != STREAMKL_OK) return st;
-  if (topk < 1 || !q || !k || !v || !block_idx || !out || !lse) return STREAMKL_ERR_INVALID_ARG;
+  if (topk < 1 || !q || !k || !v || !block_idx || !out) return STREAMKL_ERR_INVALID_ARG;
   if (topk > kMaxTopk) return STREAMKL_ERR_UNSUPPORTED;
   a.topk = topk;
   const long long need = fwd_ws_bytes(a);
@@ -319,33 +341,38 @@ streamkl_status streamkl_block_mass(const void* q, const void* k, const int* seq
   if (st != STREAMKL_OK) return st;
   const skl::SparseArgs& a = ma.s;
   if (!q || !k || !mass) return STREAMKL_ERR_INVALID_ARG;
-  if (!lse && (!workspace || workspace_bytes < 4ll * B * H * N_Q * a.NB))
+  const int fused = lse ? 0 : mass_fused(a);
+  if (!lse && !fused && (!workspace || workspace_bytes < mass_ws_bytes(a)))
     return STREAMKL_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(mass) || !aligned16(lse) ||
       !aligned16(workspace))
     return STREAMKL_ERR_MISALIGNED;
   ma.row_lse = lse;
   ma.mass = mass;
-  ma.blse = lse ? nullptr : static_cast<float*>(workspace);
+  ma.blse = lse || fused ? nullptr : static_cast<float*>(workspace);
   // A tile's blocks are spread over CTAs while there are fewer than about four waves of them
   // (two per SM; the tail of a wave and padded sequences' early ends even out); a CTA takes at
   // least one pair.
   const long long tiles = (long long)a.B * a.P * a.n_tiles, want = 8ll * sm_count();
-  const long long chunks = want / tiles > 1 ? want / tiles : 1;
+  const long long chunks = fused ? fused : (want / tiles > 1 ? want / tiles : 1);
   const long long bpc = ((a.NB + chunks - 1) / chunks + 1) / 2 * 2;
   ma.bpc = (int)bpc;
   ma.n_chunks = (int)((a.NB + bpc - 1) / bpc);
+  if (fused) ma.n_chunks = fused;  // the cluster's last CTAs may have no block
   const bool quad = skl::sp_quad(a.Qn, a.G);
   auto go = [&](auto dim, auto norm) {
     constexpr int D = decltype(dim)::value;
-    constexpr bool N = decltype(norm)::value;
+    constexpr int N = decltype(norm)::value;
     return quad ? launch_mass<D, N, true>(ma, q, k, stream)
                 : launch_mass<D, N, false>(ma, q, k, stream);
   };
-  using I64 = std::integral_constant<int, 64>;
-  using I128 = std::integral_constant<int, 128>;
-  if (d == 128) return lse ? go(I128{}, std::true_type{}) : go(I128{}, std::false_type{});
-  return lse ? go(I64{}, std::true_type{}) : go(I64{}, std::false_type{});
+  auto pick = [&](auto dim) {
+    if (lse) return go(dim, std::integral_constant<int, skl::kMassNorm>{});
+    if (fused)
+      return launch_mass<decltype(dim)::value, skl::kMassFused, true>(ma, q, k, stream);
+    return go(dim, std::integral_constant<int, skl::kMassParts>{});
+  };
+  return d == 128 ? pick(std::integral_constant<int, 128>{}) : pick(std::integral_constant<int, 64>{});
 }
 
 streamkl_status streamkl_block_select(const float* mass, const int* seqlens_k, int B, int H_sel,

@@ -37,7 +37,7 @@ struct SparseArgs {
   const uint32_t* mask;    // [B * Hsel, ceil(N_Q / 32), NB]
   float2* rows;            // backward: {LSE * log2(e), sum_d out * dout} per row
   __nv_bfloat16* out;      // forward
-  float* lse;
+  float* lse;              // may be null
   __nv_bfloat16* dq;       // backward
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;

@@ -193,7 +193,7 @@ __device__ __forceinline__ void sp_join(const SparseArgs& a, const SpTile& t, ui
     for (int k = 0; k < D / 64; ++k)
       *reinterpret_cast<uint32_t*>(a.out + row * D + k * 64 + lane * 2) =
           pack_bf16x2(acc[2 * k], acc[2 * k + 1]);
-    if (lane == 0) a.lse[row] = l * 0.69314718055994530942f;
+    if (lane == 0 && a.lse) a.lse[row] = l * 0.69314718055994530942f;
   };
   if (QUAD && warp < 8) {
     for (int r = warp; r < rows; r += 8) {
@@ -527,7 +527,7 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           }
         }
       }
-      if (!parts && valid && grp == 0) a.lse[row] = l2 * 0.69314718055994530942f;
+      if (!parts && valid && grp == 0 && a.lse) a.lse[row] = l2 * 0.69314718055994530942f;
     }
   } else if (warp == 8) {
     // ---------------------------------------------------- producer (whole warp scans)

@@ -31,6 +31,7 @@ BLOCK = 64  # keys per block
 
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_NO_LSE = object()
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -126,14 +127,15 @@ def streamkl_block_mass(q_s, k_s, scale_S: float, causal: bool, lse_s=None, seql
         mass = q_s.new_empty((B, h_kv, n_q, nb), dtype=_F32)
     else:
         _typed("mass", mass, dev, _F32, (B, h_kv, n_q, nb))
+    lib = load_library()
     nbytes = ws = lse = 0
     keep = None
     if lse_s is None:
-        nbytes = 4 * B * H * n_q * nb
+        nbytes = lib.streamkl_block_mass_workspace(B, H, h_kv, n_q, n_k, d)
         keep, ws = _workspace(nbytes, q_s, stream)
     else:
         lse = _typed("lse_s", lse_s, dev, _F32, (B, H, n_q)).data_ptr()
-    st = load_library().streamkl_block_mass(
+    st = lib.streamkl_block_mass(
         q_s.data_ptr(), k_s.data_ptr(), _lens(seqlens_k, dev, B), B, H, h_kv, n_q, n_k, d,
         scale_S, bool(causal), lse, ws, nbytes, mass.data_ptr(), _stream_ptr(stream, dev))
     _check(st, "streamkl_block_mass")
@@ -163,30 +165,36 @@ def streamkl_block_select(mass, n_k: int, causal: bool, topk: int, n_first: int 
     return block_idx
 
 
-@_on_device
-def streamkl_sparse_attn_fwd(q, k, v, block_idx, scale: float, causal: bool, seqlens_k=None,
-                             out=None, lse=None, stream=None):
-    """Attention of every query over its listed blocks: out bf16 [B, H, N_Q, d] and the
-    log-sum-exps fp32 [B, H, N_Q]."""
+def _attn_fwd(q, k, v, block_idx, scale, causal, seqlens_k, out, lse, stream):
+    """The forward on the current device; lse = _NO_LSE leaves the log-sum-exps out."""
     dev = q.get_device()
     B, H, h_kv, h_sel, n_q, n_k, d, topk = _qkv_shape(q, k, v, block_idx, dev)
-    lib = load_library()
     if out is None:
         out = torch.empty_like(q)
     else:
         _bf16("out", out, dev, q.shape)
     if lse is None:
         lse = q.new_empty((B, H, n_q), dtype=_F32)
-    else:
+    elif lse is not _NO_LSE:
         _typed("lse", lse, dev, _F32, (B, H, n_q))
+    lib = load_library()
     nbytes = lib.streamkl_sparse_attn_workspace(B, H, h_kv, h_sel, n_q, n_k, d, topk, 0)
     keep, ws = _workspace(nbytes, q, stream)
     st = lib.streamkl_sparse_attn_fwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), block_idx.data_ptr(), _lens(seqlens_k, dev, B), B, H,
-        h_kv, h_sel, n_q, n_k, d, topk, scale, bool(causal), ws, nbytes,
-        out.data_ptr(), lse.data_ptr(), _stream_ptr(stream, dev))
-    _check(st, "streamkl_sparse_attn_fwd")
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), block_idx.data_ptr(), _lens(seqlens_k, dev, B), B,
+        H, h_kv, h_sel, n_q, n_k, d, topk, scale, causal, ws, nbytes, out.data_ptr(),
+        0 if lse is _NO_LSE else lse.data_ptr(), _stream_ptr(stream, dev))
+    if st:
+        _check(st, "streamkl_sparse_attn_fwd")
     return out, lse
+
+
+@_on_device
+def streamkl_sparse_attn_fwd(q, k, v, block_idx, scale: float, causal: bool, seqlens_k=None,
+                             out=None, lse=None, stream=None):
+    """Attention of every query over its listed blocks: out bf16 [B, H, N_Q, d] and the
+    log-sum-exps fp32 [B, H, N_Q]."""
+    return _attn_fwd(q, k, v, block_idx, scale, bool(causal), seqlens_k, out, lse, stream)
 
 
 @_on_device
@@ -292,11 +300,16 @@ def sparse_attention(q, k, v, block_idx, scale: Optional[float] = None, causal: 
     block_idx, lens = block_idx.contiguous(), _lens_arg(seqlens_k)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         out, lse = SparseAttentionFunction.apply(q, k, v, block_idx, lens, scale, bool(causal))
-    else:
-        out, lse = streamkl_sparse_attn_fwd(q, k, v, block_idx, scale, causal, lens)
-        if autograd._check_status:
-            autograd._after_launch("sparse_attention forward", q.device)
+        return (out, lse) if return_lse else out
+    out, lse = _infer(q, k, v, block_idx, scale, bool(causal), lens, None if return_lse else _NO_LSE)
+    if autograd._check_status:
+        autograd._after_launch("sparse_attention forward", q.device)
     return (out, lse) if return_lse else out
+
+
+@_on_device
+def _infer(q, k, v, block_idx, scale, causal, lens, lse):
+    return _attn_fwd(q, k, v, block_idx, scale, causal, lens, None, lse, None)
 
 
 def student_sparse_attention(q, k, v, q_s, k_s, topk: int, scale: Optional[float] = None,

@@ -271,9 +271,12 @@ streamkl_status streamkl_bwd_teacher_shard(const void* q_t, const void* k_t, con
  * Block mass: k [B,H_kv,N_K,d], G = H / H_kv query heads share a K head,
  *   mass[b,hk,i,c] = 1/G sum_{h in group hk} sum_{j in block c, allowed} exp(s[h,i,j] - lse[h,i])
  * (fp32 [B,H_kv,N_Q,NB], fully overwritten). lse [B,H,N_Q] is streamkl_fwd's lse_s when the
- * divergence has been computed; with lse = null the rows are normalised by their own sum, which
- * takes a workspace of 4 * B * H * N_Q * NB bytes.
+ * divergence has been computed (another map's give no probabilities); with lse = null the rows are
+ * normalised by their own sum, which for more than a few queries takes a workspace of
+ * streamkl_block_mass_workspace() bytes (0 for single tokens; -1 for sizes that are rejected).
  */
+long long streamkl_block_mass_workspace(int B, int H, int H_kv, int N_Q, int N_K, int d);
+
 streamkl_status streamkl_block_mass(const void* q, const void* k, const int* seqlens_k, int B,
                                     int H, int H_kv, int N_Q, int N_K, int d, float scale,
                                     int causal, const float* lse, void* workspace,
@@ -304,7 +307,7 @@ long long streamkl_sparse_attn_workspace(int B, int H, int H_kv, int H_sel, int 
  * H / max(H_kv, H_sel) <= 128. A list is a set: any order, repeated entries count once, entries
  * outside 0 .. NB-1 are ignored.
  *   out (bf16 [B,H,N_Q,d]) = softmax over the listed, allowed keys of scale <q, k>, times v
- *   lse (fp32 [B,H,N_Q])   = log-sum-exp of those scores
+ *   lse (fp32 [B,H,N_Q])   = log-sum-exp of those scores; may be null (the backward needs it)
  * The workspace holds one bit per query, block and selection head (none for single tokens).
  */
 streamkl_status streamkl_sparse_attn_fwd(const void* q, const void* k, const void* v,

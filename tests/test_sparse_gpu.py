@@ -83,6 +83,8 @@ MASS = [
     (1, 5, 5, 300, 100, 64, True, None),       # the first queries see no key
     (3, 4, 4, 40, 190, 64, True, [190, 0, 41]),
     (1, 128, 1, 3, 129, 64, False, None),
+    (1, 8, 2, 2, 5000, 128, True, [4700]),     # few rows: a cluster normalises on chip
+    (40, 8, 4, 1, 900, 64, True, [900 - 22 * b for b in range(40)]),  # many: two kernels
 ]
 
 

@@ -74,7 +74,7 @@ def test_select_refusals(lib):
 
 @pytest.mark.parametrize("backward", [False, True])
 def test_attention_refusals(lib, backward):
-    null = ["q", "k", "v", "idx", "out", "lse"] + (["dout", "dq", "dk", "dv"] if backward else [])
+    null = ["q", "k", "v", "idx", "out"] + (["lse", "dout", "dq", "dk", "dv"] if backward else [])
     for name in null:
         assert call_attn(lib, backward, **{name: 0}) == 1, name
     for kw in (dict(topk=0), dict(B=0), dict(scale=float("inf")), dict(ws=0), dict(wsb=16)):
@@ -92,7 +92,12 @@ def test_workspace_sizes(lib):
     # The bit matrix: one bit per query, block and selection head, 32 queries to a word.
     assert ws(2, 16, 4, 4, 4096, 4096, 128, 16, 0) >= 2 * 4 * 4096 // 8 * 64
     assert ws(2, 16, 4, 4, 4096, 4096, 128, 16, 1) >= 2 * 4 * 4096 // 8 * 64 + 8 * 2 * 16 * 4096
+    assert ws(1, 4, 2, 2, 1, 4096, 64, 4, 0) == 0
     assert ws(1, 4, 2, 2, 100, 200, 96, 4, 0) == -1
+    assert lib.streamkl_block_mass_workspace(1, 4, 2, 100, 200, 64) == 4 * 4 * 100 * 4
+    assert lib.streamkl_block_mass_workspace(1, 32, 8, 1, 8192, 64) == 0
+    assert lib.streamkl_block_mass_workspace(64, 32, 8, 1, 8192, 64) == 4 * 64 * 32 * 128
+    assert lib.streamkl_block_mass_workspace(1, 4, 2, 100, 200, 96) == -1
     assert ws(1, 4, 2, 2, 100, 200, 64, 0, 0) == -1
 
 

@@ -22,7 +22,6 @@ struct SelectArgs {
   const float* mass;  // [B, Hsel, N_Q, NB]
   const int* lens;
   int* idx;           // [B, Hsel, N_Q, topk]
-  long long rows;     // B * Hsel * N_Q
   int Hsel, N_Q, N_K, NB, causal, topk, n_first, n_last;
 };
 
@@ -62,37 +61,64 @@ __device__ __forceinline__ void select_row(const SelectArgs& a, long long row, i
   auto add = [](uint32_t x, uint32_t y) { return x + y; };
   auto lesser = [](uint32_t x, uint32_t y) { return min(x, y); };
   auto larger = [](uint32_t x, uint32_t y) { return max(x, y); };
-  uint32_t key[V], kmin = 0xffffffffu, kmax = 0u;
+  float x[V];
+  uint32_t key[V];
+  bool plain = true;  // masses that are >= 0 (not NaN) need only their sign bit set
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = base + k * 32 + lane;
-    key[k] = c < n ? mass_key(__ldg(src + c)) : 0u;
+    x[k] = c < n ? __ldg(src + c) : 0.f;
   }
 #pragma unroll
+  for (int k = 0; k < V; ++k) plain = plain && x[k] >= 0.f;
+  if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) key[k] = __float_as_uint(x[k]) | 0x80000000u;  // -0 equals 0
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) key[k] = mass_key(x[k]);
+  }
+  uint32_t kmax = 0u, lane_max = 0u;  // of the free blocks; of all visible ones of this lane
+#pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = base + k * 32 + lane;
-    if (c < n) {
-      if (c < a.n_first || c >= n - a.n_last) {
-        key[k] = 0xffffffffu;
-      } else {
-        kmin = min(kmin, key[k]);
-        kmax = max(kmax, key[k]);
-      }
+    const int c0 = base + k * 32, c = c0 + lane;
+    if (c0 + 32 > n && c >= n) key[k] = 0u;
+    // Registers without a forced block (most) skip the per-lane tests.
+    if (c0 < a.n_first || c0 + 32 > n - a.n_last) {
+      const bool force = c < n && (c < a.n_first || c >= n - a.n_last);
+      kmax = force ? kmax : max(kmax, key[k]);
+      key[k] = force ? 0xffffffffu : key[k];
+    } else {
+      kmax = max(kmax, key[k]);
     }
+    lane_max = max(lane_max, key[k]);
   }
   uint32_t thr = 1u;  // taken: keys above thr, and the first `ties` equal to it
   int ties = a.topk;
+  bool exact = true;  // every key that reaches thr is taken
   if (n > a.topk) {
     // count(key >= lo) >= topk > count(key >= hi); forced keys reach every threshold.
-    const int forced = min(a.n_first, n) + a.n_last;  // n > topk >= n_first + n_last
+    const int forced = a.n_first + a.n_last;  // n > topk >= n_first + n_last: they are distinct
     if (forced == a.topk) {
       thr = 0xfffffffeu;  // no free key is taken (masses' keys end below)
     } else {
-      kmin = select_join<WARPS>(__reduce_min_sync(0xffffffffu, kmin), red, turn, warp, lane, lesser);
       kmax = select_join<WARPS>(__reduce_max_sync(0xffffffffu, kmax), red, turn, warp, lane, larger);
-      uint32_t lo = kmin, hi = kmax + 1u;
-      int reach = n;  // keys >= lo
-      while (hi - lo > 1u) {
+      // The least of the lanes' largest keys is reached by 32 keys per warp that holds 32 visible
+      // blocks; else the least key of all.
+      uint32_t lo;
+      if (a.topk <= 32 && n >= 32) {
+        lo = n >= base + 32 ? __reduce_min_sync(0xffffffffu, lane_max) : 0u;
+        lo = select_join<WARPS>(lo, red, turn, warp, lane, larger);
+      } else {
+        uint32_t kmin = 0xffffffffu;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (base + k * 32 + lane < n) kmin = min(kmin, key[k]);
+        lo = select_join<WARPS>(__reduce_min_sync(0xffffffffu, kmin), red, turn, warp, lane, lesser);
+      }
+      uint32_t hi = kmax + 1u;
+      int reach = a.topk + 1;  // keys >= lo: exactly topk once found so, else more (or ties)
+      while (hi - lo > 1u && hi > lo) {
         const uint32_t mid = lo + ((hi - lo) >> 1);
         uint32_t cnt = 0;
 #pragma unroll
@@ -107,7 +133,8 @@ __device__ __forceinline__ void select_row(const SelectArgs& a, long long row, i
         }
       }
       thr = lo;
-      if (reach > a.topk) {
+      if (reach != a.topk) {
+        exact = false;
         uint32_t cnt = 0;
 #pragma unroll
         for (int k = 0; k < V; ++k) cnt += key[k] > thr ? 1u : 0u;
@@ -134,14 +161,24 @@ __device__ __forceinline__ void select_row(const SelectArgs& a, long long row, i
   }
   int at = gt0 + min(eq0, ties);
   const uint32_t below = (1u << lane) - 1u;
+  if (exact) {
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const uint32_t eq = __ballot_sync(0xffffffffu, key[k] == thr);
-    const bool take = key[k] > thr || (key[k] == thr && eq0 + __popc(eq & below) < ties);
-    const uint32_t taken = __ballot_sync(0xffffffffu, take);
-    if (take) dst[at + __popc(taken & below)] = base + k * 32 + lane;
-    at += __popc(taken);
-    eq0 += __popc(eq);
+    for (int k = 0; k < V; ++k) {
+      const bool take = key[k] >= thr;
+      const uint32_t taken = __ballot_sync(0xffffffffu, take);
+      if (take) dst[at + __popc(taken & below)] = base + k * 32 + lane;
+      at += __popc(taken);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const uint32_t eq = __ballot_sync(0xffffffffu, key[k] == thr);
+      const bool take = key[k] > thr || (key[k] == thr && eq0 + __popc(eq & below) < ties);
+      const uint32_t taken = __ballot_sync(0xffffffffu, take);
+      if (take) dst[at + __popc(taken & below)] = base + k * 32 + lane;
+      at += __popc(taken);
+      eq0 += __popc(eq);
+    }
   }
   const int have = min(n, a.topk);
   for (int e = have + (WARPS == 1 ? lane : (int)threadIdx.x); e < a.topk;
@@ -150,28 +187,32 @@ __device__ __forceinline__ void select_row(const SelectArgs& a, long long row, i
 }
 
 // WARPS = 1: four rows per CTA, one warp each, with the fewest registers that hold the row's
-// visible blocks (causal rows see half of them on average). WARPS > 1: one row per CTA.
+// visible blocks (causal rows see half of them on average). WARPS > 1: one row per CTA. The grid is
+// (selection heads, rows), so that no row needs a division.
 template <int V, int WARPS>
 __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS)
 streamkl_block_select_kernel(const SelectArgs a) {
   __shared__ uint32_t red[2][8];
+  constexpr int ROWS = WARPS == 1 ? 4 : 1;
   const int lane = threadIdx.x & 31;
   const int warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
-  const unsigned row = WARPS == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-  if (row >= (unsigned long long)a.rows) return;  // rows < 2^31
-  const unsigned bh = row / (unsigned)a.N_Q;
-  const int i = (int)(row - bh * (unsigned)a.N_Q), b = (int)(bh / (unsigned)a.Hsel);
-  const int nk = sp_len(a.lens, b, a.N_K);
-  const int last = sp_last(i, nk, a.N_Q, a.causal);
-  const int n = last < 0 ? 0 : last / kSpBlock + 1;
-  if (WARPS == 1 && V > 2 && n <= 64)
-    select_row<2, WARPS>(a, row, n, red, warp, lane);
-  else if (WARPS == 1 && V > 4 && n <= 128)
-    select_row<4, WARPS>(a, row, n, red, warp, lane);
-  else if (WARPS == 1 && V == 8 && n <= 192)
-    select_row<6, WARPS>(a, row, n, red, warp, lane);
-  else
-    select_row<V, WARPS>(a, row, n, red, warp, lane);
+  const int bh = blockIdx.x;
+  const int nk = a.lens == nullptr ? a.N_K : sp_len(a.lens, bh / a.Hsel, a.N_K);
+  for (int i = blockIdx.y * ROWS + (WARPS == 1 ? threadIdx.x >> 5 : 0); i < a.N_Q;
+       i += gridDim.y * ROWS) {
+    const long long row = (long long)bh * a.N_Q + i;
+    const int last = sp_last(i, nk, a.N_Q, a.causal);
+    const int n = last < 0 ? 0 : last / kSpBlock + 1;
+    if (WARPS == 1 && V > 2 && n <= 64)
+      select_row<2, WARPS>(a, row, n, red, warp, lane);
+    else if (WARPS == 1 && V > 4 && n <= 128)
+      select_row<4, WARPS>(a, row, n, red, warp, lane);
+    else if (WARPS == 1 && V == 8 && n <= 192)
+      select_row<6, WARPS>(a, row, n, red, warp, lane);
+    else
+      select_row<V, WARPS>(a, row, n, red, warp, lane);
+    if (WARPS > 1) __syncthreads();  // the next row starts over with the reduction buffers
+  }
 }
 
 }  // namespace skl

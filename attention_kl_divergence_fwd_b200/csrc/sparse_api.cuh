@@ -387,22 +387,26 @@ streamkl_status streamkl_block_select(const float* mass, const int* seqlens_k, i
     return STREAMKL_ERR_UNSUPPORTED;
   if (!aligned16(mass) || !aligned16(block_idx) || misaligned4(seqlens_k))
     return STREAMKL_ERR_MISALIGNED;
-  const skl::SelectArgs a{mass, seqlens_k, block_idx, rows,   H_sel,   N_Q,
-                          N_K,  nb,        causal ? 1 : 0, topk, n_first, n_last};
-  const unsigned warp_grid = (unsigned)((rows + 3) / 4), cta_grid = (unsigned)rows;
-  // Few rows leave the SMs idle: then a row's blocks are spread over four or eight warps (512 rows
-  // of 1024 blocks: 14 us with one warp each, see block_select.cuh for the spread form).
+  const skl::SelectArgs a{mass, seqlens_k, block_idx, H_sel, N_Q, N_K, nb, causal ? 1 : 0, topk,
+                          n_first, n_last};
+  // (selection heads, rows): y is limited to 65535, beyond that a CTA takes several rows.
+  auto grid = [&](int rows_per_cta) {
+    const int y = (N_Q + rows_per_cta - 1) / rows_per_cta;
+    return dim3((unsigned)(B * H_sel), (unsigned)(y < 65535 ? y : 65535));
+  };
+  // Few rows leave the SMs idle: then a row's blocks are spread over eight warps (512 rows of 1024
+  // blocks: 14.3 us with one warp each, 6.6 us with eight).
   const bool few = rows < 16ll * sm_count();
   if (nb <= 64)
-    skl::streamkl_block_select_kernel<2, 1><<<warp_grid, 128, 0, stream>>>(a);
+    skl::streamkl_block_select_kernel<2, 1><<<grid(4), 128, 0, stream>>>(a);
   else if (nb <= 256)
-    skl::streamkl_block_select_kernel<8, 1><<<warp_grid, 128, 0, stream>>>(a);
+    skl::streamkl_block_select_kernel<8, 1><<<grid(4), 128, 0, stream>>>(a);
   else if (nb <= 1024 && few)
-    skl::streamkl_block_select_kernel<4, 8><<<cta_grid, 256, 0, stream>>>(a);
+    skl::streamkl_block_select_kernel<4, 8><<<grid(1), 256, 0, stream>>>(a);
   else if (nb <= 1024)
-    skl::streamkl_block_select_kernel<32, 1><<<warp_grid, 128, 0, stream>>>(a);
+    skl::streamkl_block_select_kernel<32, 1><<<grid(4), 128, 0, stream>>>(a);
   else
-    skl::streamkl_block_select_kernel<32, 8><<<cta_grid, 256, 0, stream>>>(a);
+    skl::streamkl_block_select_kernel<32, 8><<<grid(1), 256, 0, stream>>>(a);
   return ok_launch();
 }
 

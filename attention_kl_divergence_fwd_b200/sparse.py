@@ -32,8 +32,10 @@ BLOCK = 64  # keys per block
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _NO_LSE = object()
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# The raw lookups behind torch.cuda.current_device() and current_stream().cuda_stream.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _on_device(fn):
@@ -84,14 +86,18 @@ def _lens(seqlens_k, dev, B):
     return _typed("seqlens_k", seqlens_k, dev, _I32, (B,)).data_ptr()
 
 
+def _new(t, stream):
+    """Memory that a call allocates: on another stream than the current one it is not handed out
+    again before that stream is past the call."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _workspace(nbytes, like, stream):
-    """Scratch of one call; on another stream than the current one it is kept until that
-    stream is past the call."""
     if nbytes <= 0:
         return None, 0
-    ws = like.new_empty(nbytes, dtype=torch.uint8)
-    if stream is not None:
-        ws.record_stream(stream)
+    ws = _new(like.new_empty(nbytes, dtype=torch.uint8), stream)
     return ws, ws.data_ptr()
 
 
@@ -124,7 +130,7 @@ def streamkl_block_mass(q_s, k_s, scale_S: float, causal: bool, lse_s=None, seql
     B, H, h_kv, n_q, n_k, d = _qk_shape(q_s, k_s, dev)
     nb = num_blocks(n_k)
     if mass is None:
-        mass = q_s.new_empty((B, h_kv, n_q, nb), dtype=_F32)
+        mass = _new(q_s.new_empty((B, h_kv, n_q, nb), dtype=_F32), stream)
     else:
         _typed("mass", mass, dev, _F32, (B, h_kv, n_q, nb))
     lib = load_library()
@@ -155,7 +161,7 @@ def streamkl_block_select(mass, n_k: int, causal: bool, topk: int, n_first: int 
     if num_blocks(n_k) != nb:
         raise ValueError(f"mass has {nb} blocks, n_k = {n_k} keys make {num_blocks(n_k)}")
     if block_idx is None:
-        block_idx = mass.new_empty((B, h_sel, n_q, max(topk, 0)), dtype=_I32)
+        block_idx = _new(mass.new_empty((B, h_sel, n_q, max(topk, 0)), dtype=_I32), stream)
     else:
         _typed("block_idx", block_idx, dev, _I32, (B, h_sel, n_q, topk))
     st = load_library().streamkl_block_select(
@@ -170,11 +176,11 @@ def _attn_fwd(q, k, v, block_idx, scale, causal, seqlens_k, out, lse, stream):
     dev = q.get_device()
     B, H, h_kv, h_sel, n_q, n_k, d, topk = _qkv_shape(q, k, v, block_idx, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(torch.empty_like(q), stream)
     else:
         _bf16("out", out, dev, q.shape)
     if lse is None:
-        lse = q.new_empty((B, H, n_q), dtype=_F32)
+        lse = _new(q.new_empty((B, H, n_q), dtype=_F32), stream)
     elif lse is not _NO_LSE:
         _typed("lse", lse, dev, _F32, (B, H, n_q))
     lib = load_library()
@@ -209,7 +215,7 @@ def streamkl_sparse_attn_bwd(q, k, v, out, lse, dout, block_idx, scale: float, c
     grads = []
     for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if g is None:
-            g = torch.empty_like(like)
+            g = _new(torch.empty_like(like), stream)
         else:
             _bf16(name, g, dev, like.shape)
         grads.append(g)

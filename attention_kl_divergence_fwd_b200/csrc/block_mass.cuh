@@ -104,7 +104,7 @@ __device__ __forceinline__ float mass_block(const uint32_t (&v)[N], float c, flo
           f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, b2);
       uint64_t e;
       if (poly_rank((k >> 1) & 7) < SKL_MASS_POLY) {
-        e = exp2_fma2(x);
+        e = exp2_fma2_low(x);
       } else {
         float x0, x1;
         f2_unpack(x, x0, x1);

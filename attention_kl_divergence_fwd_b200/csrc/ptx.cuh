@@ -570,6 +570,27 @@ __device__ __forceinline__ uint64_t exp2_fma2(uint64_t x) {
                  __int_as_float(__float_as_int(p1) + (__float_as_int(y1) << 23)));
 }
 
+// exp2_fma2 for arguments below 64 (probabilities: at most about 0), without the upper clamp.
+__device__ __forceinline__ uint64_t exp2_fma2_low(uint64_t x) {
+  float x0, x1;
+  f2_unpack(x, x0, x1);
+  x = f2_pack(fmaxf(x0, -125.0f), fmaxf(x1, -125.0f));
+  const uint64_t kShift = f2_pack(12582912.0f, 12582912.0f);
+  const uint64_t y = f2_add(x, kShift);
+  const uint64_t f = f2_sub(x, f2_sub(y, kShift));
+  uint64_t p = f2_pack(0.001325405784882605f, 0.001325405784882605f);
+  p = f2_fma(p, f, f2_pack(0.00967527274042368f, 0.00967527274042368f));
+  p = f2_fma(p, f, f2_pack(0.055507827550172806f, 0.055507827550172806f));
+  p = f2_fma(p, f, f2_pack(0.2402212917804718f, 0.2402212917804718f));
+  p = f2_fma(p, f, f2_pack(0.6931469440460205f, 0.6931469440460205f));
+  p = f2_fma(p, f, f2_pack(1.0000001192092896f, 1.0000001192092896f));
+  float p0, p1, y0, y1;
+  f2_unpack(p, p0, p1);
+  f2_unpack(y, y0, y1);
+  return f2_pack(__int_as_float(__float_as_int(p0) + (__float_as_int(y0) << 23)),
+                 __int_as_float(__float_as_int(p1) + (__float_as_int(y1) << 23)));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

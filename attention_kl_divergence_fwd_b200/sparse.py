@@ -19,6 +19,7 @@ safe to capture into a CUDA graph. The selection has no gradient.
 from __future__ import annotations
 
 import functools
+import inspect
 import math
 from typing import Optional
 
@@ -41,15 +42,17 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 def _on_device(fn):
     """Runs an entry point on the device of its first tensor, made current when it is not.
     Single-token calls take a few microseconds on the GPU, so the common path costs one lookup."""
+    name = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
-    def wrapper(first, *args, **kwargs):
-        dev = first.get_device()
+    def wrapper(*args, **kwargs):
+        dev = (args[0] if args else kwargs[name]).get_device()
         if dev < 0:
             raise ValueError(f"{fn.__name__}: tensors must be on a CUDA device")
         if dev == _current_device():
-            return fn(first, *args, **kwargs)
+            return fn(*args, **kwargs)
         with torch.cuda.device(dev):
-            return fn(first, *args, **kwargs)
+            return fn(*args, **kwargs)
     return wrapper
 
 

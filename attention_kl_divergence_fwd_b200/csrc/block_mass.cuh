@@ -161,27 +161,25 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
   const int steps = n_vis > 0 ? (n_vis + 1) / 2 : 0;
   if (MODE == kMassParts && steps == 0) return;
 
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bars->q_full), 1);
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(smem_u32(&bars->k_full[s]), 1);
-      mbar_init(smem_u32(&bars->k_empty[s]), 1);
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_q);
+      tma_prefetch_desc(&map_k);
+      bars->abort_flag = 0;
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&bars->s_full[s]), 1);
-      mbar_init(smem_u32(&bars->s_free[s]), QUAD ? 4 : 8);
+    constexpr int S_FREE = offsetof(MassBars, s_free) / 8, LAST = offsetof(MassBars, drain) / 8;
+    sp_init_barriers(&bars->q_full, LAST + 1, kMassThreads, lane, [](int i) {
+      return i == S_FREE || i == S_FREE + 1 ? (QUAD ? 4 : 8) : 1;
+    });
+  } else {
+    if (warp == 9) {
+      tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
+      tmem_relinquish();
     }
-    mbar_init(smem_u32(&bars->drain), 1);
-    bars->abort_flag = 0;
-    fence_mbar_init();
+    tc_fence_before();
+    named_bar_sync(15, kMassThreads);
+    tc_fence_after();
   }
-  if (warp == 9) {
-    tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
   if (warp < 8) {
@@ -322,8 +320,6 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
     }
   } else if (warp == 8) {
     if (lane == 0 && steps > 0) {
-      tma_prefetch_desc(&map_q);
-      tma_prefetch_desc(&map_k);
       const uint64_t keep = l2_policy_evict_last();
       const uint32_t qb = smem_u32(&bars->q_full);
       mbar_arrive_expect_tx(qb, (QUAD ? 4 : 1) * a.Qn * a.G * D * 2);

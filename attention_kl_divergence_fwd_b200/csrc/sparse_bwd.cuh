@@ -137,28 +137,26 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
   const int bp = unit / a.n_tiles;
   const SpTile t = sp_tile(a, bp, a.n_tiles - 1 - unit % a.n_tiles);
 
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bars->q_full), 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&bars->k_full[s]), 1);
-      mbar_init(smem_u32(&bars->k_empty[s]), 1);
-      mbar_init(smem_u32(&bars->v_full[s]), 1);
-      mbar_init(smem_u32(&bars->v_empty[s]), 1);
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_q);
+      tma_prefetch_desc(&map_do);
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+      bars->abort_flag = 0;
     }
-    for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
-    mbar_init(smem_u32(&bars->s_full), 1);
-    mbar_init(smem_u32(&bars->ds_full), 8);
-    mbar_init(smem_u32(&bars->dq_full), 1);
-    bars->abort_flag = 0;
-    fence_mbar_init();
+    constexpr int DS_FULL = offsetof(SpDqBars, ds_full) / 8, LAST = offsetof(SpDqBars, dq_full) / 8;
+    sp_init_barriers(&bars->q_full, LAST + 1, kSpDqThreads, lane,
+                     [](int i) { return i == DS_FULL ? 8 : 1; });
+  } else {
+    if (warp == 9) {
+      tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    named_bar_sync(15, kSpDqThreads);
+    tc_fence_after();
   }
-  if (warp == 9) {
-    tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
   if (warp < 8) {
@@ -238,10 +236,6 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
     }
   } else if (warp == 8) {
     if (lane == 0) {
-      tma_prefetch_desc(&map_q);
-      tma_prefetch_desc(&map_do);
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
       const uint32_t qb = smem_u32(&bars->q_full);
       mbar_arrive_expect_tx(qb, 2 * a.Qn * a.G * D * 2);
       for (int blk = 0; blk < D / 64; ++blk) {
@@ -468,40 +462,36 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
   const int p0 = (kv - b * a.Hkv) * ppk;
   const int rows = a.Qn * a.G;               // rows of a tile that TMA writes
 
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bars->k_full), 1);
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(smem_u32(&bars->q_full[s]), 1);
-      mbar_init(smem_u32(&bars->q_empty[s]), 1);
-      mbar_init(smem_u32(&bars->do_full[s]), 1);
-      mbar_init(smem_u32(&bars->do_empty[s]), 1);
+  if (warp == 16) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_q);
+      tma_prefetch_desc(&map_do);
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+      bars->abort_flag = 0;
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&bars->s_full[s]), 1);
-      mbar_init(smem_u32(&bars->ds_full[s]), 8);
-      mbar_init(smem_u32(&bars->ds_empty[s]), 1);
+    constexpr int DS_FULL = offsetof(SpDkvBars, ds_full) / 8;
+    constexpr int LAST = offsetof(SpDkvBars, acc_full) / 8;
+    sp_init_barriers(&bars->k_full, LAST + 1, kSpDkvThreads, lane,
+                     [](int i) { return i == DS_FULL || i == DS_FULL + 1 ? 8 : 1; });
+  } else {
+    if (warp == 17) {
+      tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
+      tmem_relinquish();
     }
-    for (int s = 0; s < 8; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
-    mbar_init(smem_u32(&bars->acc_full), 1);
-    bars->abort_flag = 0;
-    fence_mbar_init();
+    // Rows of the Q and dO buffers that no copy writes enter the row sums of dV and dK with a
+    // factor of 0 and must be finite: zero them once.
+    if (rows < 128 && warp < 16) {
+      const int per = (128 - rows) * 8;
+      for (int e = threadIdx.x; e < per * (C::NQ + C::ND) * (D / 64); e += 512)
+        *reinterpret_cast<uint4*>(smem + C::OFF_Q + (e / per) * (128 * 128) + rows * 128 +
+                                  (e % per) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      fence_async_smem();
+    }
+    tc_fence_before();
+    named_bar_sync(15, kSpDkvThreads);
+    tc_fence_after();
   }
-  if (warp == 17) {
-    tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
-    tmem_relinquish();
-  }
-  // Rows of the Q and dO buffers that no copy writes enter the row sums of dV and dK with a
-  // factor of 0 and must be finite: zero them once.
-  if (rows < 128) {
-    const int per = (128 - rows) * 8;
-    for (int e = threadIdx.x; e < per * (C::NQ + C::ND) * (D / 64); e += kSpDkvThreads)
-      *reinterpret_cast<uint4*>(smem + C::OFF_Q + (e / per) * (128 * 128) + rows * 128 +
-                                (e % per) * 16) = make_uint4(0u, 0u, 0u, 0u);
-    fence_async_smem();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
   if (warp < 16) {
@@ -585,8 +575,6 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
   } else if (warp == 16) {
     const uint64_t keep = l2_policy_evict_last();
     if (lane == 0) {
-      tma_prefetch_desc(&map_q);
-      tma_prefetch_desc(&map_do);
       const uint32_t kf = smem_u32(&bars->k_full);
       mbar_arrive_expect_tx(kf, 2 * C::SLOT);
       for (int blk = 0; blk < D / 64; ++blk) {

@@ -16,6 +16,8 @@
 // key-major backward scans a column.
 #pragma once
 
+#include <cstddef>
+
 #include "ptx.cuh"
 
 namespace skl {
@@ -90,6 +92,19 @@ __device__ __forceinline__ SpTile sp_tile(const SparseArgs& a, int bp, int tile)
 // tile's columns. TMEM lets a warp read only its own 32 lanes, so without the copies one warp
 // would do all of the tile's exponentials while three sit idle.
 __host__ __device__ inline bool sp_quad(int Qn, int G) { return Qn * G <= 32; }
+
+// Start of a kernel's CTA. The producer warp initialises the barriers (an array of `n` at the start
+// of the barrier block, `arrivals(i)` each), announces that and goes on to its first loads; the
+// other warps come here after their own preparations and wait for the barriers (and for the TMEM
+// address). Named barrier 15 of `threads` threads.
+template <typename Arrivals>
+__device__ __forceinline__ void sp_init_barriers(uint64_t* bars, int n, int threads, int lane,
+                                                 Arrivals arrivals) {
+  for (int i = lane; i < n; i += 32) mbar_init(smem_u32(bars + i), arrivals(i));
+  fence_mbar_init();
+  __syncwarp();
+  named_bar_arrive(15, threads);
+}
 
 // Builds the bit matrix: one CTA per 32 queries of a selection head. Entries that are
 // negative, beyond the last block, or of a block the query may not see set no bit.

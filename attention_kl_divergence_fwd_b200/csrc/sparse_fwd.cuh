@@ -253,33 +253,26 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   const int bp = unit / a.n_tiles;
   const SpTile t = sp_tile(a, bp, a.n_tiles - 1 - unit % a.n_tiles);
 
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bars->q_full), 1);
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(smem_u32(&bars->k_full[s]), 1);
-      mbar_init(smem_u32(&bars->k_empty[s]), 1);
-      mbar_init(smem_u32(&bars->v_full[s]), 1);
-      mbar_init(smem_u32(&bars->v_empty[s]), 1);
-      mbar_init(smem_u32(&bars->m_pass[s][0]), 1);
-      mbar_init(smem_u32(&bars->m_pass[s][1]), 1);
-      mbar_init(smem_u32(&bars->pair[s]), 2);
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_q);
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+      bars->abort_flag = 0;
     }
-    for (int s = 0; s < 8; ++s) mbar_init(smem_u32(&bars->info_full[s]), 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&bars->s_full[s]), 1);
-      mbar_init(smem_u32(&bars->p_full[s]), 4);
+    constexpr int P_FULL = offsetof(SpFwdBars, p_full) / 8, PAIR = offsetof(SpFwdBars, pair) / 8;
+    sp_init_barriers(&bars->q_full, PAIR + 4, kSpThreads, lane, [](int i) {
+      return i == P_FULL || i == P_FULL + 1 ? 4 : (i >= PAIR ? 2 : 1);
+    });
+  } else {
+    if (warp == 9) {
+      tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
+      tmem_relinquish();
     }
-    mbar_init(smem_u32(&bars->o_full), 1);
-    bars->abort_flag = 0;
-    fence_mbar_init();
+    tc_fence_before();
+    named_bar_sync(15, kSpThreads);
+    tc_fence_after();
   }
-  if (warp == 9) {
-    tmem_alloc(smem_u32(&bars->tmem_base), C::TM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
   if (warp < 8) {
@@ -532,9 +525,6 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   } else if (warp == 8) {
     // ---------------------------------------------------- producer (whole warp scans)
     if (lane == 0) {
-      tma_prefetch_desc(&map_q);
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
       const uint32_t qb = smem_u32(&bars->q_full);
       mbar_arrive_expect_tx(qb, (QUAD ? 4 : 1) * a.Qn * a.G * D * 2);
       for (int blk = 0; blk < D / 64; ++blk)

@@ -320,7 +320,8 @@ streamkl_block_mass_kernel(const __grid_constant__ CUtensorMap map_q,
     }
   } else if (warp == 8) {
     if (lane == 0 && steps > 0) {
-      const uint64_t keep = l2_policy_evict_last();
+      // A tile that is the only one of its K head is the only reader of that K.
+      const uint64_t keep = a.n_tiles == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
       const uint32_t qb = smem_u32(&bars->q_full);
       mbar_arrive_expect_tx(qb, (QUAD ? 4 : 1) * a.Qn * a.G * D * 2);
       for (int blk = 0; blk < D / 64; ++blk)

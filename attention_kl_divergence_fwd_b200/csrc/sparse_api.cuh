@@ -196,6 +196,18 @@ streamkl_status launch_sparse_bwd(const skl::SparseArgs& a, const void* q, const
   skl::streamkl_sparse_rows_kernel<D><<<(unsigned)((rows + per_cta - 1) / per_cta), 256, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout), lse, rows,
       a.rows);
+  // Rows that see one block at most: the first ones of a causal sequence, or all rows of a short
+  // one. Without padded lengths the host knows whether there are any.
+  if (a.lens || (a.causal ? a.N_K - a.N_Q < skl::kSpBlock : a.N_K <= skl::kSpBlock)) {
+    // Causal without lengths: the last such query is N_Q - N_K + 63.
+    long long n = a.N_Q;
+    if (!a.lens && a.causal && n > (long long)a.N_Q - a.N_K + 64) n = (long long)a.N_Q - a.N_K + 64;
+    const long long y = (n + 7) / 8;
+    const dim3 grid((unsigned)(a.B * a.H), (unsigned)(y < 65535 ? y : 65535));
+    skl::streamkl_sparse_short_rows_kernel<D><<<grid, 256, 0, stream>>>(
+        a, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+        static_cast<const __nv_bfloat16*>(v), static_cast<const __nv_bfloat16*>(dout));
+  }
   const streamkl_status st = launch_cluster(
       kk, (long long)a.B * a.Hkv * a.NB, a.kv_splits, skl::kSpDkvThreads, CK::SMEM, stream, mq, mdo,
       mk, mv, a, i_s, i_dp, skl::idesc_bf16_f32(128, 64, true, true));

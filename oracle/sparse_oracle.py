@@ -141,8 +141,10 @@ def oracle_sparse_attn(q, k, v, block_idx, scale, causal, seqlens_k=None, dout=N
             dq[b, h] = ds @ kk * scale
             dk[b, h // G] += ds.T @ qq * scale
             # dS: its rounding, the relative error of p, fp32 errors of dP and D, and D formed
-            # from the rounded out.
+            # from the rounded out, except where a query sees one block at most (D from its keys).
             e_d = (do.abs() * e_o).sum(-1, keepdim=True)
+            own = 3 * e_s[:, None] * (p * dP.abs()).sum(-1, keepdim=True)
+            e_d = torch.where(base.sum(-1, keepdim=True) <= BLOCK, own, e_d)
             f32 = d * 2.0 ** -23 * (do.abs() @ vv.abs().T + (do * o).abs().sum(-1, keepdim=True))
             e_ds = half * ds.abs() + 3 * e_s[:, None] * p * (dP.abs() + D.abs()) \
                 + (1 + half) * p * (e_d + f32) + tiny * (1 + dP.abs() + D.abs())

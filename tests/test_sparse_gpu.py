@@ -290,6 +290,31 @@ def test_as_a_user_trains_and_serves():
     close(tok, r, tol["out"], "token")
 
 
+@pytest.mark.parametrize("nq,nk,causal,lens", [(64, 64, True, None), (40, 70, True, None),
+                                               (150, 60, False, None), (90, 300, True, [300, 64]),
+                                               (200, 150, True, [20, 150])], ids=str)
+def test_gradients_of_queries_with_few_keys(nq, nk, causal, lens):
+    """Rows that see one block at most take sum_d out dout from their keys: dS is then good to its
+    own rounding, which the bounds require of these rows. Large values make that rounding of out
+    the larger part otherwise."""
+    B, Hs = 2, 1
+    q, k, v, do = inputs(B, 6, 3, nq, nk, 64, seed=21)
+    v = (v.float() + 4).to(torch.bfloat16)  # out and dout share a direction: D is large
+    do = (do.float() + 2).to(torch.bfloat16)
+    if lens:
+        k, v = pad_nan(k, lens), pad_nan(v, lens)
+    lt = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+    idx = lists(B, Hs, nq, nk, 3, seed=3, wild=False)
+    idx[..., 0] = 0
+    idx[0, 0, 5] = -1
+    tol = {}
+    ref = oracle_sparse_attn(q, k, v, idx, 0.125, causal, lt, do, tol)
+    qg, kg, vg = (t.cuda().requires_grad_() for t in (q, k, v))
+    out = sparse.sparse_attention(qg, kg, vg, idx.cuda(), 0.125, causal, None if lt is None else lt.cuda())
+    for name, x, r in zip(("dq", "dk", "dv"), torch.autograd.grad(out, (qg, kg, vg), do.cuda()), ref[2:]):
+        close(x, r, tol[name], name)
+
+
 def test_graph_capture_streams_and_other_layouts():
     q, k, v, do = (t.cuda() for t in inputs(2, 4, 2, 70, 300, 64, seed=8))
     idx = lists(2, 2, 70, 300, 4, seed=8).cuda()

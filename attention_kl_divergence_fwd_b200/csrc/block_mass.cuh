@@ -18,7 +18,10 @@
 // The scores of a block need no running maximum across blocks, so the keys of one query can be
 // spread over as many CTAs as there are pairs of blocks.
 // Bound by the exponential unit (one exponential per pair) for many queries, by reading K for
-// few. Two CTAs per SM.
+// few. Two CTAs per SM. Measured on a B200: 32 heads, 16384 tokens, d = 64, causal: 1011 us (the
+// unit alone would take 923 us; a quarter of the exponentials runs on the FMA pipe, 1196, 1095,
+// 1027 and 1117 us with 0, 1, 2 and 3 of 8 pairs); one token of 16 sequences of up to 32768 keys:
+// 72 us, K read at 4.8 TB/s.
 //
 // QUAD: tiles of at most 32 rows, four copies, each row warp 32 of a pair's 128 keys (sp_quad);
 // a block's two halves are joined when the staged values are written.
@@ -73,9 +76,7 @@ constexpr int kMassThreads = 320;
 
 // Exponentials of a block on the FMA pipe, of every 8 pairs of keys (the rest on the
 // exponential unit, which otherwise bounds the kernel).
-#ifndef SKL_MASS_POLY
-#define SKL_MASS_POLY 2
-#endif
+constexpr int kMassPoly = 2;
 
 // Value of a row over N keys: sum 2^(s c - lse2) (NORM) or log2 sum 2^(s c); keys past lim are
 // left out.
@@ -103,7 +104,7 @@ __device__ __forceinline__ float mass_block(const uint32_t (&v)[N], float c, flo
       const uint64_t x =
           f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, b2);
       uint64_t e;
-      if (poly_rank((k >> 1) & 7) < SKL_MASS_POLY) {
+      if (poly_rank((k >> 1) & 7) < kMassPoly) {
         e = exp2_fma2_low(x);
       } else {
         float x0, x1;

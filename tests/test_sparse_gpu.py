@@ -154,6 +154,9 @@ ATTN = [
     (2, 4, 4, 1, 33, 1100, 128, True, 9, [1100, 40]),
     (1, 4, 1, 1, 1200, 1200, 128, True, 4, None),   # few K heads: blocks split over clusters
     (1, 4, 1, 1, 1100, 1250, 64, True, 4, [1190]),
+    (2, 40, 2, 1, 1, 700, 64, True, 5, [700, 65]),  # one query, more heads than a copied tile holds
+    (1, 8, 2, 2, 1, 1300, 128, True, 600, None),    # one query, a list longer than the blocks
+    (2, 16, 16, 16, 4, 800, 64, False, 3, [800, 3]),
 ]
 
 
@@ -352,6 +355,57 @@ def test_graph_capture_streams_and_other_layouts():
     ones = torch.ones_like(out)
     assert torch.equal(qt.grad, skl.sparse.streamkl_sparse_attn_bwd(q, k, v, out, lse, ones, idx,
                                                                     0.125, True)[0])
+    assert skl.device_status() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    jobs = []
+    for j in range(2):
+        q, k, v, do = (t.cuda() for t in inputs(1, 8, 2, 600, 900, 128, seed=30 + j))
+        idx = lists(1, 2, 600, 900, 6, seed=j).cuda()
+        jobs.append((q, k, v, do, idx))
+
+    def run(q, k, v, do, idx, stream=None):
+        out, lse = sparse.streamkl_sparse_attn_fwd(q, k, v, idx, 0.1, True, stream=stream)
+        g = sparse.streamkl_sparse_attn_bwd(q, k, v, out, lse, do, idx, 0.1, True, stream=stream)
+        m = sparse.streamkl_block_mass(q, k, 0.1, True, stream=stream)
+        i = sparse.streamkl_block_select(m, 900, True, 5, stream=stream)
+        return [out, lse, *g, m, i]
+
+    alone = [run(*job) for job in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        both = [run(*job, stream=s) for job, s in zip(jobs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert skl.device_status() == 0
+
+
+def test_offsets_past_32_bits():
+    """A cache whose last heads lie beyond 2^31 elements: token attention with its gradients, block
+    masses and selection of the last head against the oracle on that head alone."""
+    H, n, d = 128, 132000, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k = torch.empty(1, H, n, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    v = torch.empty_like(k).normal_(generator=g)
+    assert k.numel() > 2 ** 31
+    q = torch.empty(1, H, 1, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    do = torch.empty_like(q).normal_(generator=g)
+    mass = sparse.block_mass(q, k, 0.088, True)
+    idx = sparse.select_blocks(mass, n, 6, True, 1, 2)
+    last = [t[:, -1:].cpu() for t in (q, k, v, do, idx, mass)]
+    ref_mass = oracle_block_mass(last[0], last[1], 0.088, True)
+    close(last[5], ref_mass, mass_tol(last[0], last[1], 0.088, ref_mass, True), "mass")
+    assert torch.equal(last[4], oracle_block_select(last[5], n, 6, True, 1, 2))
+    out, lse = sparse.streamkl_sparse_attn_fwd(q, k, v, idx, 0.088, True)
+    tol = {}
+    ref = oracle_sparse_attn(*last[:3], last[4], 0.088, True, None, last[3], tol)
+    close(out[:, -1:], ref[0], tol["out"], "out")
+    dq, dk, dv = sparse.streamkl_sparse_attn_bwd(q, k, v, out, lse, do, idx, 0.088, True)
+    for name, x, r in zip(("dq", "dk", "dv"), (dq, dk, dv), ref[2:]):
+        close(x[:, -1:], r, tol[name], name)
     assert skl.device_status() == 0
 
 

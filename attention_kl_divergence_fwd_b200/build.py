@@ -6,6 +6,9 @@ Compiles csrc/streamkl_api.cu (which includes every kernel) with nvcc into
 ``attention_kl_divergence_fwd_b200/lib/libstreamkl.so``. The CUDA runtime is linked
 statically and the driver API is reached through the runtime's entry-point query,
 so the library loads on hosts without a GPU driver (only launching needs a GPU).
+
+csrc/sparse_dispatch.cpp, the PyTorch side of the block-sparse calls, becomes
+``lib/_sparse_dispatch.so``; it reaches the library through addresses handed over at run time.
 """
 from __future__ import annotations
 
@@ -13,14 +16,17 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libstreamkl.so")
 SOURCES = [os.path.join(PKG, "csrc", "streamkl_api.cu")]
-DEPS = [os.path.join(PKG, "csrc", f) for f in os.listdir(os.path.join(PKG, "csrc"))] + [
-    os.path.join(ROOT, "include", "streamkl.h")]
+DISPATCH = os.path.join(LIB_DIR, "_sparse_dispatch.so")
+DISPATCH_SOURCE = os.path.join(PKG, "csrc", "sparse_dispatch.cpp")
+DEPS = [os.path.join(PKG, "csrc", f) for f in os.listdir(os.path.join(PKG, "csrc"))
+        if not f.endswith(".cpp")] + [os.path.join(ROOT, "include", "streamkl.h")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -44,7 +50,40 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in DEPS if os.path.exists(p))
 
 
+def build_dispatch(force: bool = False, verbose: bool = False) -> str:
+    deps = [DISPATCH_SOURCE, os.path.join(ROOT, "include", "streamkl.h")]
+    if not force and os.path.exists(DISPATCH) and all(
+            os.path.getmtime(p) <= os.path.getmtime(DISPATCH) for p in deps):
+        return DISPATCH
+    import torch
+    base = os.path.dirname(torch.__file__)
+    include = [os.path.join(base, "include"),
+               os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+               os.path.join(ROOT, "include")]
+    lib = os.path.join(base, "lib")
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = DISPATCH + ".tmp"
+    # The compiler that nvcc uses: one that links libstdc++ statically would put a second copy
+    # beside PyTorch's, and the two break each other's streams.
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-DTORCH_EXTENSION_NAME=_sparse_dispatch", "-DTORCH_API_INCLUDE_EXTENSION_H",
+           *(f"-I{p}" for p in include), DISPATCH_SOURCE, "-o", tmp, f"-L{lib}", "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"{cmd[0]} failed with exit code {res.returncode}")
+    os.replace(tmp, DISPATCH)
+    return DISPATCH
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_dispatch(force, verbose)
     if not force and up_to_date():
         return LIB
     os.makedirs(LIB_DIR, exist_ok=True)

@@ -15,26 +15,31 @@ Tensors are bf16 [B, heads, N, d] on one CUDA device, d in {64, 128}; K heads ma
 group of query heads, and one selection may serve several K heads. Calls run on the current (or
 the given) stream and allocate outputs and workspace from PyTorch's allocator, which makes them
 safe to capture into a CUDA graph (a backward through ``torch.autograd.grad``: ``.backward()``
-accumulates into leaves on the stream where eager code first used them). The selection has no
-gradient.
+accumulates into leaves on the stream where eager code first used them; leaves whose eager graph
+from the default stream still lives are refused while capturing). With status checks on
+(``autograd.set_check_status``, read by the forward for its backward too) every call waits for
+its kernels and raises their errors. The selection has no gradient, and the attention's gradients
+are not differentiable again.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
+import importlib.util
 import inspect
 import math
+import os
 from typing import Optional
 
 import torch
-from torch.autograd.function import once_differentiable
 
-from . import _check, autograd, load_library
+from . import LIB_PATH, StreamKLError, _check, autograd, load_library
 
 BLOCK = 64  # keys per block
+DISPATCH_PATH = os.path.join(os.path.dirname(LIB_PATH), "_sparse_dispatch.so")
 
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
-_NO_LSE = object()
 # The raw lookups behind torch.cuda.current_device() and current_stream().cuda_stream.
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -176,8 +181,11 @@ def streamkl_block_select(mass, n_k: int, causal: bool, topk: int, n_first: int 
     return block_idx
 
 
-def _attn_fwd(q, k, v, block_idx, scale, causal, seqlens_k, out, lse, stream):
-    """The forward on the current device; lse = _NO_LSE leaves the log-sum-exps out."""
+@_on_device
+def streamkl_sparse_attn_fwd(q, k, v, block_idx, scale: float, causal: bool, seqlens_k=None,
+                             out=None, lse=None, stream=None):
+    """Attention of every query over its listed blocks: out bf16 [B, H, N_Q, d] and the
+    log-sum-exps fp32 [B, H, N_Q]."""
     dev = q.get_device()
     B, H, h_kv, h_sel, n_q, n_k, d, topk = _qkv_shape(q, k, v, block_idx, dev)
     if out is None:
@@ -186,26 +194,17 @@ def _attn_fwd(q, k, v, block_idx, scale, causal, seqlens_k, out, lse, stream):
         _bf16("out", out, dev, q.shape)
     if lse is None:
         lse = _new(q.new_empty((B, H, n_q), dtype=_F32), stream)
-    elif lse is not _NO_LSE:
+    else:
         _typed("lse", lse, dev, _F32, (B, H, n_q))
     lib = load_library()
     nbytes = lib.streamkl_sparse_attn_workspace(B, H, h_kv, h_sel, n_q, n_k, d, topk, 0)
     keep, ws = _workspace(nbytes, q, stream)
     st = lib.streamkl_sparse_attn_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), block_idx.data_ptr(), _lens(seqlens_k, dev, B), B,
-        H, h_kv, h_sel, n_q, n_k, d, topk, scale, causal, ws, nbytes, out.data_ptr(),
-        0 if lse is _NO_LSE else lse.data_ptr(), _stream_ptr(stream, dev))
-    if st:
-        _check(st, "streamkl_sparse_attn_fwd")
+        H, h_kv, h_sel, n_q, n_k, d, topk, scale, bool(causal), ws, nbytes, out.data_ptr(),
+        lse.data_ptr(), _stream_ptr(stream, dev))
+    _check(st, "streamkl_sparse_attn_fwd")
     return out, lse
-
-
-@_on_device
-def streamkl_sparse_attn_fwd(q, k, v, block_idx, scale: float, causal: bool, seqlens_k=None,
-                             out=None, lse=None, stream=None):
-    """Attention of every query over its listed blocks: out bf16 [B, H, N_Q, d] and the
-    log-sum-exps fp32 [B, H, N_Q]."""
-    return _attn_fwd(q, k, v, block_idx, scale, bool(causal), seqlens_k, out, lse, stream)
 
 
 @_on_device
@@ -237,36 +236,28 @@ def streamkl_sparse_attn_bwd(q, k, v, out, lse, dout, block_idx, scale: float, c
     return dq, dk, dv
 
 
-def _after_launch(where, device):
-    if autograd._check_status:
-        autograd._after_launch(where, device)
+_dispatch = None
 
 
-class SparseAttentionFunction(torch.autograd.Function):
-    """Attention over selected blocks; gradients flow to q, k and v."""
-
-    @staticmethod
-    def forward(ctx, q, k, v, block_idx, seqlens_k, scale: float, causal: bool):
-        out, lse = streamkl_sparse_attn_fwd(q, k, v, block_idx, scale, causal, seqlens_k)
-        _after_launch("sparse_attention forward", q.device)
-        ctx.save_for_backward(q, k, v, out, lse, block_idx, seqlens_k)
-        ctx.params = (scale, causal)
-        ctx.mark_non_differentiable(lse)
-        ctx.set_materialize_grads(False)
-        return out, lse
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, g_out, _g_lse=None):
-        q, k, v, out, lse, block_idx, seqlens_k = ctx.saved_tensors
-        scale, causal = ctx.params
-        if g_out is None:
-            return (None,) * 7
-        dout = g_out.to(torch.bfloat16).contiguous()
-        dq, dk, dv = streamkl_sparse_attn_bwd(q, k, v, out, lse, dout, block_idx, scale, causal,
-                                              seqlens_k)
-        _after_launch("sparse_attention backward", q.device)
-        return dq, dk, dv, None, None, None, None
+def _ext():
+    """The C++ side of the calls below (raises OSError if it has not been built): checks,
+    allocations and the autograd node without Python's share of a short call."""
+    global _dispatch
+    if _dispatch is None:
+        lib = load_library()
+        if not os.path.exists(DISPATCH_PATH):
+            raise OSError(f"block-sparse dispatch not built: {DISPATCH_PATH} "
+                          "(run python -m attention_kl_divergence_fwd_b200.build)")
+        spec = importlib.util.spec_from_file_location("_sparse_dispatch", DISPATCH_PATH)
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+        ext.bind([ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.streamkl_block_mass, lib.streamkl_block_mass_workspace, lib.streamkl_block_select,
+            lib.streamkl_sparse_attn_workspace, lib.streamkl_sparse_attn_fwd,
+            lib.streamkl_sparse_attn_bwd, lib.streamkl_status_string, lib.streamkl_device_status)])
+        ext.raise_as(StreamKLError)
+        _dispatch = ext
+    return _dispatch
 
 
 def _lens_arg(seqlens_k):
@@ -283,9 +274,12 @@ def block_mass(q_s, k_s, scale: Optional[float] = None, causal: bool = False, ls
     ``lse`` are the map's row log-sum-exps [B, H, N_Q] (``streamkl_fwd``'s lse_s) when they are
     at hand; without them the rows are normalised by their own sums. The default scale is
     1/sqrt(d). Not differentiable: the map is trained by its divergence."""
-    scale = 1.0 / math.sqrt(q_s.shape[-1]) if scale is None else float(scale)
-    return streamkl_block_mass(q_s.contiguous(), k_s.contiguous(), scale, causal,
-                               None if lse is None else lse.contiguous(), _lens_arg(seqlens_k))
+    if scale is None:
+        scale = 1.0 / math.sqrt(q_s.shape[-1])
+    if lse is not None:
+        lse = lse.detach().contiguous()
+    return _ext().block_mass(q_s.detach().contiguous(), k_s.detach().contiguous(), scale, causal, lse,
+                             _lens_arg(seqlens_k), autograd._check_status)
 
 
 def select_blocks(mass, n_k: int, topk: int, causal: bool = False, n_first: int = 1,
@@ -293,8 +287,8 @@ def select_blocks(mass, n_k: int, topk: int, causal: bool = False, n_first: int 
     """Of the blocks a query sees: the first ``n_first``, the last ``n_last`` and the heaviest of
     the rest, ``topk`` in all: int32 [B, H_sel, N_Q, topk], ascending, -1 behind the last.
     Equal masses go to the lower index, NaN ranks below every number."""
-    return streamkl_block_select(mass.contiguous(), n_k, causal, topk, n_first, n_last,
-                                 _lens_arg(seqlens_k))
+    return _ext().select_blocks(mass.contiguous(), n_k, topk, causal, n_first, n_last,
+                                _lens_arg(seqlens_k), autograd._check_status)
 
 
 def sparse_attention(q, k, v, block_idx, scale: Optional[float] = None, causal: bool = False,
@@ -306,21 +300,11 @@ def sparse_attention(q, k, v, block_idx, scale: Optional[float] = None, causal: 
     block_idx int32 [B, H_sel, N_Q, topk]: a set per query (order and repeats do not matter,
     entries outside 0 .. NB-1 select nothing); query head h reads list h // (H // H_sel). A query
     with nothing to read gets 0 (log-sum-exp -inf) and passes no gradient."""
-    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
-    q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-    block_idx, lens = block_idx.contiguous(), _lens_arg(seqlens_k)
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
-        out, lse = SparseAttentionFunction.apply(q, k, v, block_idx, lens, scale, bool(causal))
-        return (out, lse) if return_lse else out
-    out, lse = _infer(q, k, v, block_idx, scale, bool(causal), lens, None if return_lse else _NO_LSE)
-    if autograd._check_status:
-        autograd._after_launch("sparse_attention forward", q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    out, lse = _ext().sparse_attention(q, k, v, block_idx, _lens_arg(seqlens_k), scale, causal,
+                                       return_lse, autograd._check_status)
     return (out, lse) if return_lse else out
-
-
-@_on_device
-def _infer(q, k, v, block_idx, scale, causal, lens, lse):
-    return _attn_fwd(q, k, v, block_idx, scale, causal, lens, None, lse, None)
 
 
 def student_sparse_attention(q, k, v, q_s, k_s, topk: int, scale: Optional[float] = None,

@@ -12,7 +12,7 @@ import torch
 
 import attention_kl_divergence_fwd_b200 as skl
 from attention_kl_divergence_fwd_b200 import sparse
-from attention_kl_divergence_fwd_b200.autograd import attention_kl_loss
+from attention_kl_divergence_fwd_b200.autograd import attention_kl_loss, set_check_status
 from oracle import oracle_block_mass, oracle_block_select, oracle_sparse_attn
 
 pytestmark = pytest.mark.gpu
@@ -427,3 +427,55 @@ def test_bad_lengths_are_reported_and_read_as_empty():
         sparse.select_blocks(torch.zeros(1, 1, 1, 3, device="cuda"), 64, 1)
     with pytest.raises(skl.StreamKLError):
         sparse.select_blocks(torch.zeros(1, 1, 1, 1, device="cuda"), 64, 1, n_first=1, n_last=1)
+
+
+def test_backward_reports_a_length_that_went_bad_after_the_forward():
+    q, k, v, do = (t.cuda() for t in inputs(2, 4, 2, 3, 130, 64, seed=9))
+    idx = torch.zeros(2, 2, 3, 1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([130, 70], dtype=torch.int32, device="cuda")
+    leaves = [t.requires_grad_() for t in (q, k, v)]
+    try:
+        set_check_status(True)
+        out = sparse.sparse_attention(*leaves, idx, causal=True, seqlens_k=lens)
+        lens.data.fill_(131)
+        with pytest.raises(skl.StreamKLError, match="backward"):
+            out.backward(do)
+    finally:
+        set_check_status(False)
+    assert all(t.grad is None for t in leaves) and skl.device_status() == 0
+
+
+def test_captured_step_of_a_user():
+    q, k, v, do = (t.cuda() for t in inputs(1, 4, 2, 70, 300, 64, seed=11))
+    idx = lists(1, 2, 70, 300, 4, seed=11).cuda()
+    eager = [t.clone().requires_grad_() for t in (q, k, v)]
+    out = sparse.sparse_attention(*eager, idx, causal=True)
+    ref = torch.autograd.grad(out, eager, do, retain_graph=True)
+    fresh = [t.clone().requires_grad_() for t in (q, k, v)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        # The leaves of the graph that still lives are refused, its detached ones are not.
+        with pytest.raises(RuntimeError, match="q is part of a graph made on the default stream"):
+            sparse.sparse_attention(*eager, idx, causal=True)
+        with pytest.raises(RuntimeError, match="v is part of a graph"):
+            sparse.sparse_attention(*fresh[:2], eager[2], idx, causal=True)
+        o = sparse.sparse_attention(*fresh, idx, causal=True)
+        d = torch.autograd.grad(o, fresh, do)
+    for t in (o, *d):
+        t.detach().zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, out) and all(torch.equal(a, b) for a, b in zip(d, ref))
+    assert skl.device_status() == 0
+
+
+def test_gradients_are_not_differentiated_again():
+    q, k, v, do = (t.cuda() for t in inputs(1, 4, 2, 20, 130, 64, seed=12))
+    idx = lists(1, 2, 20, 130, 2, seed=12).cuda()
+    leaves = [t.requires_grad_() for t in (q, k, v)]
+    out = sparse.sparse_attention(*leaves, idx, causal=True)
+    once = torch.autograd.grad(out, leaves, do, retain_graph=True)
+    kept = torch.autograd.grad(out, leaves, do, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(once, kept))
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        kept[0].sum().backward()

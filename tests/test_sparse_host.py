@@ -113,6 +113,15 @@ def test_wrappers_reject_cpu_and_wrong_tensors():
     assert [sparse.num_blocks(n) for n in (1, 64, 65)] == [1, 1, 2]
 
 
+def test_dispatch_raises_the_library_error():
+    with pytest.raises(skl.StreamKLError) as e:
+        sparse._ext().check(3, "some call")
+    assert e.value.status == 3 and "some call" in str(e.value)
+    sparse._ext().check(0, "some call")
+    with pytest.raises(ValueError, match="mass has 3 blocks, n_k = 64 keys make 1"):
+        sparse.select_blocks(torch.zeros(1, 1, 1, 3), 64, 1)
+
+
 # ------------------------------------------------------------------ oracle pins
 
 

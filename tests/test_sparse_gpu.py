@@ -6,6 +6,7 @@ and exponents at their steps. Masses are fp32: a score's error (d products at 2^
 absolute sum, the exponent's argument at 4 steps) moves a mass by that relative amount. Lists
 are compared exactly."""
 import math
+import threading
 
 import pytest
 import torch
@@ -479,3 +480,23 @@ def test_gradients_are_not_differentiated_again():
     assert all(torch.equal(a, b) for a, b in zip(once, kept))
     with pytest.raises(RuntimeError, match="differentiable once"):
         kept[0].sum().backward()
+
+
+def test_calls_on_a_fresh_thread():
+    """A serving thread's first CUDA work may be a single-token call."""
+    q, k, v, _ = (t.cuda() for t in inputs(2, 4, 2, 1, 300, 64, seed=13))
+    idx = lists(2, 2, 1, 300, 3, seed=13).cuda()
+    lse = sparse.streamkl_sparse_attn_fwd(q, k, v, idx, 0.125, True)[1]
+    calls = [lambda: sparse.sparse_attention(q, k, v, idx, causal=True),
+             lambda: sparse.block_mass(q, k, causal=True),
+             lambda: sparse.block_mass(q, k, causal=True, lse=lse),
+             lambda: sparse.select_blocks(torch.zeros(1, 1, 1, 5, device="cuda"), 300, 3)]
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        got = []
+        thread = threading.Thread(target=lambda: got.append(call()))
+        thread.start()
+        thread.join()
+        torch.cuda.synchronize()
+        assert got and torch.equal(got[0], want)

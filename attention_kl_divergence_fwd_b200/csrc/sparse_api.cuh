@@ -132,33 +132,50 @@ streamkl_status ok_launch() {
   return cudaGetLastError() == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_LAUNCH;
 }
 
-streamkl_status launch_mask(skl::SparseArgs& a, void* ws, cudaStream_t stream) {
-  const long long grid = (long long)((a.N_Q + 31) / 32) * a.B * a.Hsel;
-  uint32_t* mask = static_cast<uint32_t*>(ws);
-  const int smem = 4 * (a.NB < skl::kMaskChunk ? a.NB : skl::kMaskChunk);
-  skl::streamkl_sparse_mask_kernel<<<(unsigned)grid, 256, smem, stream>>>(a, mask);
-  a.mask = mask;
-  return ok_launch();
-}
-
-// Launches units * cluster CTAs in clusters (plain CTAs for a cluster of one).
+// Launches a grid, in clusters along x for cluster > 1; overlap: beside the tail of the stream's
+// previous kernel (grid_allow_next in sparse_common.cuh).
 template <typename... Params, typename... Args>
-streamkl_status launch_cluster(void (*kern)(Params...), long long units, int cluster, int threads,
-                               int smem, cudaStream_t stream, const Args&... args) {
-  if (units * cluster >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
+streamkl_status launch(void (*kern)(Params...), dim3 grid, int cluster, int threads, int smem,
+                       bool overlap, cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(units * cluster));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n++].val.clusterDim = {(unsigned)cluster, 1, 1};
+  }
+  if (overlap) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cfg.numAttrs = n;
   if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return STREAMKL_OK;
   cudaGetLastError();
   return STREAMKL_ERR_LAUNCH;
+}
+
+// units * cluster CTAs (plain CTAs for a cluster of one).
+template <typename... Params, typename... Args>
+streamkl_status launch_cluster(void (*kern)(Params...), long long units, int cluster, int threads,
+                               int smem, bool overlap, cudaStream_t stream, const Args&... args) {
+  if (units * cluster >= (1ll << 31)) return STREAMKL_ERR_UNSUPPORTED;
+  return launch(kern, dim3((unsigned)(units * cluster)), cluster, threads, smem, overlap, stream,
+                args...);
+}
+
+streamkl_status launch_mask(skl::SparseArgs& a, void* ws, bool overlap, cudaStream_t stream) {
+  const long long grid = (long long)((a.N_Q + 31) / 32) * a.B * a.Hsel;
+  uint32_t* mask = static_cast<uint32_t*>(ws);
+  const int smem = 4 * (a.NB < skl::kMaskChunk ? a.NB : skl::kMaskChunk);
+  const streamkl_status st = launch_cluster(skl::streamkl_sparse_mask_kernel, grid, 1, 256, smem,
+                                            overlap, stream, a, mask);
+  a.mask = mask;
+  return st;
 }
 
 template <int D, bool QUAD>
@@ -175,14 +192,15 @@ streamkl_status launch_sparse_fwd(const skl::SparseArgs& a, const void* q, const
   if (!set_smem_once(kern, C::SMEM, done)) return STREAMKL_ERR_LAUNCH;
   const bool neg = a.scale < 0.f;
   return launch_cluster(kern, (long long)a.B * a.P * a.n_tiles, a.splits, skl::kSpThreads, C::SMEM,
-                        stream, mq, mk, mv, a, skl::idesc_bf16_f32(128, 64, false, false, neg),
+                        !a.direct, stream, mq, mk, mv, a,
+                        skl::idesc_bf16_f32(128, 64, false, false, neg),
                         skl::idesc_bf16_f32(128, D, false, true));
 }
 
 template <int D>
-streamkl_status launch_sparse_bwd(const skl::SparseArgs& a, const void* q, const void* k,
+streamkl_status launch_sparse_bwd(skl::SparseArgs& a, const void* q, const void* k,
                                   const void* v, const void* out, const float* lse,
-                                  const void* dout, cudaStream_t stream) {
+                                  const void* dout, void* ws, cudaStream_t stream) {
   using CQ = skl::SpDqCfg<D>;
   using CK = skl::SpDkvCfg<D>;
   CUtensorMap mq, mdo, mk, mv;
@@ -201,27 +219,35 @@ streamkl_status launch_sparse_bwd(const skl::SparseArgs& a, const void* q, const
   const uint32_t i_dp = skl::idesc_bf16_f32(128, 64, false, false);
   const long long rows = (long long)a.B * a.H * a.N_Q;
   constexpr int per_cta = 8 * 32 / (D / 8) * skl::kRowsPerGroup;
-  skl::streamkl_sparse_rows_kernel<D><<<(unsigned)((rows + per_cta - 1) / per_cta), 256, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout), lse, rows,
-      a.rows);
   // Rows that see one block at most: the first ones of a causal sequence, or all rows of a short
   // one. Without padded lengths the host knows whether there are any.
-  if (a.lens || (a.causal ? a.N_K - a.N_Q < skl::kSpBlock : a.N_K <= skl::kSpBlock)) {
+  const bool any_short =
+      a.lens || (a.causal ? a.N_K - a.N_Q < skl::kSpBlock : a.N_K <= skl::kSpBlock);
+  const auto* o16 = static_cast<const __nv_bfloat16*>(out);
+  const auto* do16 = static_cast<const __nv_bfloat16*>(dout);
+  streamkl_status st = STREAMKL_OK;
+  if (any_short) {
     // Causal without lengths: the last such query is N_Q - N_K + 63.
     long long n = a.N_Q;
     if (!a.lens && a.causal && n > (long long)a.N_Q - a.N_K + 64) n = (long long)a.N_Q - a.N_K + 64;
     const long long y = (n + 7) / 8;
     const dim3 grid((unsigned)(a.B * a.H), (unsigned)(y < 65535 ? y : 65535));
-    skl::streamkl_sparse_short_rows_kernel<D><<<grid, 256, 0, stream>>>(
-        a, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-        static_cast<const __nv_bfloat16*>(v), static_cast<const __nv_bfloat16*>(dout));
+    st = launch(skl::streamkl_sparse_short_rows_kernel<D>, grid, 1, 256, 0, false, stream, a,
+                static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+                static_cast<const __nv_bfloat16*>(v), do16, lse);
   }
-  const streamkl_status st = launch_cluster(
-      kk, (long long)a.B * a.Hkv * a.NB, a.kv_splits, skl::kSpDkvThreads, CK::SMEM, stream, mq, mdo,
-      mk, mv, a, i_s, i_dp, skl::idesc_bf16_f32(128, 64, true, true));
+  if (st == STREAMKL_OK)
+    st = launch(skl::streamkl_sparse_rows_kernel<D>, dim3((unsigned)((rows + per_cta - 1) / per_cta)), 1,
+                256, 0, any_short, stream, a, o16, do16, lse, rows, any_short);
+  if (st == STREAMKL_OK) st = launch_mask(a, ws, true, stream);
   if (st != STREAMKL_OK) return st;
+  st = launch_cluster(
+      kk, (long long)a.B * a.Hkv * a.NB, a.kv_splits, skl::kSpDkvThreads, CK::SMEM, false, stream, mq,
+      mdo, mk, mv, a, i_s, i_dp, skl::idesc_bf16_f32(128, 64, true, true));
+  if (st != STREAMKL_OK) return st;
+  // Beside dK and dV's tail: neither reads the other's results.
   return launch_cluster(kq, (long long)a.B * a.P * a.n_tiles, a.splits, skl::kSpDqThreads, CQ::SMEM,
-                        stream, mq, mdo, mk, mv, a, i_s, i_dp,
+                        true, stream, mq, mdo, mk, mv, a, i_s, i_dp,
                         skl::idesc_bf16_f32(128, D, false, true));
 }
 
@@ -256,7 +282,7 @@ streamkl_status launch_mass(const skl::MassArgs& ma, const void* q, const void* 
   if (!set_smem_once(kern, C::SMEM, done)) return STREAMKL_ERR_LAUNCH;
   const streamkl_status st = launch_cluster(
       kern, (long long)a.B * a.P * a.n_tiles * (MODE == skl::kMassFused ? 1 : ma.n_chunks),
-      MODE == skl::kMassFused ? ma.n_chunks : 1, skl::kMassThreads, C::SMEM, stream, mq, mk, ma,
+      MODE == skl::kMassFused ? ma.n_chunks : 1, skl::kMassThreads, C::SMEM, false, stream, mq, mk, ma,
       skl::idesc_bf16_f32(128, 128, false, false, a.scale < 0.f));
   if (st != STREAMKL_OK || MODE != skl::kMassParts) return st;
   skl::streamkl_block_norm_kernel<<<(unsigned)((long long)a.B * a.P * a.N_Q), 256, 0, stream>>>(ma);
@@ -307,7 +333,7 @@ streamkl_status streamkl_sparse_attn_fwd(const void* q, const void* k, const voi
   a.splits = sparse_splits(a);
   a.direct = sparse_direct(a) ? 1 : 0;
   if (!a.direct) {
-    const streamkl_status sm = launch_mask(a, workspace, stream);
+    const streamkl_status sm = launch_mask(a, workspace, false, stream);
     if (sm != STREAMKL_OK) return sm;
   }
   if (skl::sp_quad(a.Qn, a.G))
@@ -345,10 +371,8 @@ streamkl_status streamkl_sparse_attn_bwd(const void* q, const void* k, const voi
   a.rows = reinterpret_cast<float2*>(ws + mask_bytes(a));
   a.splits = sparse_splits(a);
   a.kv_splits = sparse_kv_splits(a);
-  const streamkl_status sm = launch_mask(a, ws, stream);
-  if (sm != STREAMKL_OK) return sm;
-  return d == 128 ? launch_sparse_bwd<128>(a, q, k, v, out, lse, dout, stream)
-                  : launch_sparse_bwd<64>(a, q, k, v, out, lse, dout, stream);
+  return d == 128 ? launch_sparse_bwd<128>(a, q, k, v, out, lse, dout, ws, stream)
+                  : launch_sparse_bwd<64>(a, q, k, v, out, lse, dout, ws, stream);
 }
 
 streamkl_status streamkl_block_mass(const void* q, const void* k, const int* seqlens_k, int B,

@@ -3,7 +3,8 @@
 // With p_ij = exp(s_ij - LSE_i) recomputed tile by tile, D_i = sum_d out_i dout_i and
 //   dP_ij = <dout_i, v_j>,  dS_ij = p_ij (dP_ij - D_i):
 //   dV_j = sum_i p_ij dout_i,  dK_j = scale sum_i dS_ij q_i,  dQ_i = scale sum_j dS_ij k_j.
-// Two kernels, one per direction of the bit matrix, so that every sum has one owner: no
+// Two kernels (the second starts in the first one's tail: 1337 tokens 101 -> 91 us, 2 x 4096 tokens
+// 420 -> 404), one per direction of the bit matrix, so that every sum has one owner: no
 // atomics, the same bits every time, and K heads shared by a group of query heads are summed
 // inside one CTA (a tile's rows are the whole group). Recomputing S and dP in both costs 7
 // products per tile pair instead of 5; adding dQ parts (or dK and dV parts) through L2 instead
@@ -29,12 +30,15 @@ __device__ __forceinline__ float dot8(const uint4& u, const uint4& v, float acc)
 
 // rows[r] = {LSE * log2(e), D_r = sum_d out * dout}: D / 8 lanes per row, 16 bytes each, several
 // rows in flight per lane. Bound by reading out and dout once (2 x 16 heads x 4096 rows of 128:
-// 67 MB in 10.8 us, 6.2 TB/s).
+// 67 MB in 10.8 us, 6.2 TB/s). Rows that see one block are left to the kernel below
+// (skip_short).
 constexpr int kRowsPerGroup = 4;
 template <int D>
 __global__ void __launch_bounds__(256)
-streamkl_sparse_rows_kernel(const __nv_bfloat16* out, const __nv_bfloat16* dout, const float* lse,
-                            long long rows, float2* dst) {
+streamkl_sparse_rows_kernel(const SparseArgs a, const __nv_bfloat16* out,
+                            const __nv_bfloat16* dout, const float* lse, long long rows,
+                            bool skip_short) {
+  grid_allow_next();
   constexpr int L = D / 8;                       // lanes per row
   constexpr int GROUPS = 256 / L;                // rows a CTA takes at once
   const int at = threadIdx.x % L;
@@ -55,8 +59,17 @@ streamkl_sparse_rows_kernel(const __nv_bfloat16* out, const __nv_bfloat16* dout,
 #pragma unroll
     for (int s = L / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
     const long long row = row0 + k * GROUPS;
-    if (at == 0 && row < rows) dst[row] = make_float2(__ldg(lse + row) * 1.4426950408889634f, acc);
+    if (at == 0 && row < rows) {
+      if (skip_short) {
+        const int bh = (int)(row / a.N_Q);
+        const int last = sp_last((int)(row - (long long)bh * a.N_Q),
+                                 sp_len(a.lens, bh / a.H, a.N_K), a.N_Q, a.causal);
+        if (last >= 0 && last < kSpBlock) continue;
+      }
+      a.rows[row] = make_float2(__ldg(lse + row) * 1.4426950408889634f, acc);
+    }
   }
+  grid_end_after_previous();
 }
 
 // D_r = sum_j p_rj <dout_r, v_j> in fp32 for the rows that see at most one block. out carries the
@@ -64,19 +77,25 @@ streamkl_sparse_rows_kernel(const __nv_bfloat16* out, const __nv_bfloat16* dout,
 // for n keys of like weight, so much as dS's own rounding when n is small (a step over 200 tokens:
 // dQ and dK 2.7e-3 off in norm with the sum above, 2.4e-3 with this).
 // CTA = 8 queries of one head (one warp each, two keys per lane); K and V of block 0 in shared
-// memory.
+// memory. It reads the lists and LSEs itself and writes rows[] for these rows, so that it, the
+// kernel above and the one that builds the bit matrix run beside one another (training step of
+// 2 x 16 heads x 4096 tokens 402 -> 397 us).
 template <int D>
 __global__ void __launch_bounds__(256)
 streamkl_sparse_short_rows_kernel(const SparseArgs a, const __nv_bfloat16* q,
                                   const __nv_bfloat16* kk, const __nv_bfloat16* v,
-                                  const __nv_bfloat16* dout) {
+                                  const __nv_bfloat16* dout, const float* lse) {
+  grid_allow_next();
   constexpr int PITCH = D / 8 + 1;  // 16-byte pieces; the odd pitch spreads a column over banks
   __shared__ uint4 sk[kSpBlock * PITCH], sv[kSpBlock * PITCH];
   const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
   const int nk = sp_len(a.lens, b, a.N_K);
   // Rows see more keys as i grows: this CTA has short rows only if its first row is one (or sees
   // none). The grid covers at most 65535 * 8 rows at once.
-  if (nk < 1 || sp_last(blockIdx.y * 8, nk, a.N_Q, a.causal) >= kSpBlock) return;
+  if (nk < 1 || sp_last(blockIdx.y * 8, nk, a.N_Q, a.causal) >= kSpBlock) {
+    grid_end_after_previous();
+    return;
+  }
   const size_t kv0 = (size_t)(b * a.Hkv + h / (a.H / a.Hkv)) * a.N_K * D;
   for (int e = threadIdx.x; e < min(nk, kSpBlock) * (D / 8); e += 256) {
     const int j = e / (D / 8), ch = e % (D / 8);
@@ -84,13 +103,16 @@ streamkl_sparse_short_rows_kernel(const SparseArgs a, const __nv_bfloat16* q,
     sv[j * PITCH + ch] = __ldg(reinterpret_cast<const uint4*>(v + kv0) + e);
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31, sel = b * a.Hsel + h / (a.H / a.Hsel), iws = (a.N_Q + 31) >> 5;
+  const int lane = threadIdx.x & 31, sel = b * a.Hsel + h / (a.H / a.Hsel);
   const float c = a.scale * 1.4426950408889634f;
   for (long long at = blockIdx.y * 8 + (threadIdx.x >> 5); at < a.N_Q; at += 8ll * gridDim.y) {
     const int i = (int)at, last = sp_last(i, nk, a.N_Q, a.causal);
     if (last >= kSpBlock) break;
-    const uint32_t word = __ldg(a.mask + ((size_t)sel * iws + (i >> 5)) * a.NB);
-    if (last < 0 || !((word >> (i & 31)) & 1u)) continue;
+    if (last < 0) continue;
+    const int* idx = a.idx + ((size_t)sel * a.N_Q + i) * a.topk;
+    bool listed = false;
+    for (int e = lane; e < a.topk; e += 32) listed |= __ldg(idx + e) == 0;
+    listed = __any_sync(0xffffffffu, listed);
     const size_t row = (size_t)blockIdx.x * a.N_Q + i;
     const uint4* qr = reinterpret_cast<const uint4*>(q + row * D);
     const uint4* gr = reinterpret_cast<const uint4*>(dout + row * D);
@@ -105,13 +127,14 @@ streamkl_sparse_short_rows_kernel(const SparseArgs a, const __nv_bfloat16* q,
       d0 = dot8(y, sv[j0 + ch], d0);
       d1 = dot8(y, sv[j1 + ch], d1);
     }
-    const float nl = -a.rows[row].x;
+    const float x = __ldg(lse + row) * 1.4426950408889634f, nl = -x;
     float acc = lane <= last ? ex2_approx(fmaf(s0, c, nl)) * d0 : 0.f;
     acc += lane + 32 <= last ? ex2_approx(fmaf(s1, c, nl)) * d1 : 0.f;
 #pragma unroll
     for (int e = 16; e > 0; e >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, e);
-    if (lane == 0) a.rows[row].y = acc;
+    if (lane == 0) a.rows[row] = make_float2(x, listed ? acc : 0.f);
   }
+  grid_end_after_previous();
 }
 
 // ------------------------------------------------------------------ dQ, query-major
@@ -439,6 +462,7 @@ streamkl_sparse_dq_kernel(const __grid_constant__ CUtensorMap map_q,
     __syncwarp();
     cluster_sync();  // another CTA may still be reading this one's rows
   }
+  grid_end_after_previous();
 }
 
 // ------------------------------------------------------------------ dK, dV, key-major
@@ -519,6 +543,7 @@ streamkl_sparse_dkv_kernel(const __grid_constant__ CUtensorMap map_q,
   SpDkvBars* bars = reinterpret_cast<SpDkvBars*>(smem + C::OFF_BAR);
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_allow_next();
   // Block 0 of every head first: causal maps list the early blocks most.
   const int split = blockIdx.x % a.kv_splits, unit = blockIdx.x / a.kv_splits;
   const int kv = unit % (a.B * a.Hkv), blk0 = unit / (a.B * a.Hkv);

@@ -106,6 +106,21 @@ __device__ __forceinline__ void sp_init_barriers(uint64_t* bars, int n, int thre
   named_bar_arrive(15, threads);
 }
 
+// Programmatic launches. The next kernel of the stream, launched with the overlap attribute, starts
+// once every CTA of this one has called grid_allow_next (or ended), and takes the SMs that its last
+// CTAs leave free. grid_wait_previous waits for that earlier kernel's end and its writes.
+__device__ __forceinline__ void grid_allow_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// At the end of a kernel that runs beside an earlier one without reading what that writes: its last
+// CTA waits for the earlier kernel, so that what follows in the stream follows both.
+__device__ __forceinline__ void grid_end_after_previous() {
+  if (blockIdx.x == gridDim.x - 1) grid_wait_previous();
+}
+
 // Builds the bit matrix: one CTA per 32 queries of a selection head. Entries that are
 // negative, beyond the last block, or of a block the query may not see set no bit. Bound by the
 // latency of its reads (8 heads x 16384 queries x 32 entries: 15 us).
@@ -113,6 +128,7 @@ constexpr int kMaskChunk = 8192;  // blocks per pass (32 KB of shared memory at 
 __global__ void __launch_bounds__(256)
 streamkl_sparse_mask_kernel(const SparseArgs a, uint32_t* mask) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  grid_allow_next();
   uint32_t* sm = reinterpret_cast<uint32_t*>(smem);
   const int iws = (a.N_Q + 31) >> 5;
   const int sel = blockIdx.x / iws, iw = blockIdx.x - sel * iws, b = sel / a.Hsel, i0 = iw * 32;
@@ -148,6 +164,7 @@ streamkl_sparse_mask_kernel(const SparseArgs a, uint32_t* mask) {
     for (int c = threadIdx.x; c < n; c += 256) dst[c0 + c] = sm[c];
     __syncthreads();
   }
+  grid_end_after_previous();
 }
 
 }  // namespace skl

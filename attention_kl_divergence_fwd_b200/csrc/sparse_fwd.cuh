@@ -575,6 +575,8 @@ streamkl_sparse_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       }
       listed = (before - split + a.splits - 1) / a.splits;  // before >= 0, split < splits
       __syncwarp();
+    } else {
+      grid_wait_previous();  // launched beside the end of the kernel that builds the bit matrix
     }
     // Step n: announces the next block and loads its K, then V of the step before: K's slot is free
     // as soon as S(n - NST) is done, V's only after the product of step n - 1 - NST, and waiting

@@ -141,9 +141,10 @@ streamkl_sparse_short_rows_kernel(const SparseArgs a, const __nv_bfloat16* q,
 //
 // CTA = one 128-row tile, as in the forward; key tiles are single blocks. Per block:
 // S = Q K^T and dP = dO V^T into TMEM, two threads per row form dS and write it over S as
-// bf16, dQ += dS K. 256 TMEM columns and 113 KB: two CTAs per SM. Bound by the products' operand
-// reads: about 1024 of 1440 cycles per block and SM (16 heads over 4, 16384 tokens, 32 blocks per
-// query: 456 us).
+// bf16, dQ += dS K. 256 TMEM columns and 113 KB: two CTAs per SM. Bound by the chain of a
+// step (scores 768 cycles, dS 900, product 256, hand-overs; 2880 per step and CTA, the products'
+// operand reads 1024 of 1440 per block and SM; 16 heads over 4, 16384 tokens, 32 blocks per query:
+// 456 us). One CTA per SM with Q and dO in TMEM and two score buffers took 460.
 // Warps: 0-7 rows (warp w: lane quarter w & 3, keys 32 (w >> 2) .. +31), 8 producer, 9 MMA.
 constexpr int kSpDqThreads = 320;
 template <int D>

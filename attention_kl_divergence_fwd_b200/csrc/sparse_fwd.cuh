@@ -24,12 +24,14 @@
 // QUAD: tiles of at most 32 rows, four copies, each warp a quarter of the block's keys (sp_quad);
 // the four quarters are joined like splits.
 //
-// Bound by the tensor pipe's operand reads: a block's S (N = 64, both operands in shared memory)
-// takes 384 cycles instead of 256, O += P V 256, of about 1040 per block and SM in all; the rest is
-// the fold's issue slots (41 %) and a CTA's start and end. Measured on a B200, kernel only: 32 heads
-// over 8, 16384 tokens, 32 blocks per query: 630 us (818 TFLOP/s of the queries' own blocks,
-// 1090 of the tiles' unions); one token of 32 sequences, 16 blocks: 29.4 us (4.6 TB/s); one token
-// of a 65536-key sequence, 32 blocks: 10.4 us.
+// Bound by the chain of a block: S (N = 64 with both operands in shared memory: 384 cycles), the
+// fold (600 to 900), O += P V (256) and the hand-overs between them, about 2000 cycles per block and
+// CTA. No single unit is full (tensor pipe 640 and exponentials 512 of about 1040 cycles per block
+// and SM, issue slots 41 %); without exponentials a prompt takes 6 % less, with half of the S products
+// 6 %, without loads 2 %.
+// Measured on a B200, kernel only: 32 heads over 8, 16384 tokens, 32 blocks per query: 630 us
+// (818 TFLOP/s of the queries' own blocks, 1090 of the tiles' unions); one token of 32 sequences,
+// 16 blocks: 29.4 us (4.6 TB/s); one token of a 65536-key sequence, 32 blocks: 10.4 us.
 //
 // Warps: 0-7 softmax (warp w: lane quarter w & 3, blocks of parity w >> 2), 8 producer (scans the
 // bit matrix, TMA), 9 MMA + TMEM.

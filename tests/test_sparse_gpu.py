@@ -500,3 +500,30 @@ def test_calls_on_a_fresh_thread():
         thread.join()
         torch.cuda.synchronize()
         assert got and torch.equal(got[0], want)
+
+
+def test_what_follows_in_the_stream_follows_every_kernel_of_the_call():
+    """Kernels of a call overlap: one block that every query lists keeps dK and dV busy long after
+    dQ is done, and one query that lists every block keeps the last tile of dQ busy."""
+    q, k, v, do = (t.cuda() for t in inputs(1, 4, 1, 6000, 6000, 128, seed=14))
+    one = torch.zeros(1, 1, 6000, 94, dtype=torch.int32, device="cuda")
+    all_ = torch.arange(94, dtype=torch.int32, device="cuda").expand(1, 1, 6000, 94).contiguous()
+    idx = torch.empty_like(one)
+    wants = []
+    for lists_ in (one, all_):
+        out, lse = sparse.streamkl_sparse_attn_fwd(q, k, v, lists_, 0.1, False)
+        g = sparse.streamkl_sparse_attn_bwd(q, k, v, out, lse, do, lists_, 0.1, False)
+        torch.cuda.synchronize()
+        wants.append([out, lse, *g])
+    for _ in range(3):
+        for lists_, want in zip((one, all_), wants):
+            idx.copy_(lists_)  # a kernel right before the call writes what it reads
+            out, lse = sparse.streamkl_sparse_attn_fwd(q, k, v, idx, 0.1, False)
+            grads = [torch.full_like(t, NAN) for t in (q, k, v)]
+            sparse.streamkl_sparse_attn_bwd(q, k, v, out, lse, do, idx, 0.1, False, dq=grads[0],
+                                            dk=grads[1], dv=grads[2])
+            early = [t.clone() for t in (out, lse, *grads)]  # and kernels right after read it
+            idx.fill_(-1)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(early, want))
+    assert skl.device_status() == 0

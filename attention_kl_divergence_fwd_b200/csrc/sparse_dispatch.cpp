@@ -10,6 +10,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -77,6 +78,14 @@ void want(const char* name, const Tensor& t, at::ScalarType type, const at::Devi
 
 void want_shape(const char* name, const Tensor& t, at::IntArrayRef shape) {
   TORCH_CHECK_VALUE(t.sizes() == shape, name, " must have shape ", shape, ", got ", t.sizes());
+}
+
+// Neither the forward nor the backward has a derivative in forward mode: a tangent would be lost.
+void refuse_tangent(const Tensor& t, const char* name) {
+  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
+  TORCH_CHECK_NOT_IMPLEMENTED(!t._fw_grad(0).defined(), "sparse_attention: ", name,
+                              " carries a forward-mode tangent; only reverse-mode gradients are "
+                              "implemented");
 }
 
 int narrow(int64_t n) {
@@ -206,6 +215,7 @@ struct SparseAttention : torch::autograd::Function<SparseAttention> {
                                                  torch::autograd::variable_list grads) {
     torch::autograd::variable_list none(8);
     if (!grads[0].defined()) return none;
+    refuse_tangent(grads[0], "dout");
     const auto saved = ctx->get_saved_variables();
     const Tensor &q = saved[0], &k = saved[1], &v = saved[2], &out = saved[3], &lse = saved[4],
                  &idx = saved[5];
@@ -251,6 +261,9 @@ void check_capture(const Tensor& t, const char* name) {
 std::tuple<Tensor, Tensor> sparse_attention(const Tensor& q, const Tensor& k, const Tensor& v,
                                             const Tensor& idx, const OptTensor& lens, double scale,
                                             bool causal, bool with_lse, bool check_status) {
+  refuse_tangent(q, "q");
+  refuse_tangent(k, "k");
+  refuse_tangent(v, "v");
   const Tensor qc = q.contiguous(), kc = k.contiguous(), vc = v.contiguous(), ic = idx.contiguous();
   if (at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad() || v.requires_grad())) {
     const c10::OptionalDeviceGuard guard(q.device());

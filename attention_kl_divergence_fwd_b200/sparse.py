@@ -18,8 +18,9 @@ safe to capture into a CUDA graph (a backward through ``torch.autograd.grad``: `
 accumulates into leaves on the stream where eager code first used them; leaves whose eager graph
 from the default stream still lives are refused while capturing). With status checks on
 (``autograd.set_check_status``, read by the forward for its backward too) every call waits for
-its kernels and raises their errors. The selection has no gradient, and the attention's gradients
-are not differentiable again.
+its kernels and raises their errors. The selection has no gradient, the attention's gradients
+are not differentiable again, and forward-mode derivatives (``torch.autograd.forward_ad``) through
+the attention are refused.
 """
 from __future__ import annotations
 

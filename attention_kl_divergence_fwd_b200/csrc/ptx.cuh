@@ -698,6 +698,13 @@ __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
   return v;
 }
 
+// A coherent load that stays behind the fences and waits before it.
+__device__ __forceinline__ uint32_t ld_global_u32(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // 16 columns of this warp's 32 lanes: registers -> tensor memory (no wait).
 __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(

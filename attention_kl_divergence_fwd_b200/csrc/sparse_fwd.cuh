@@ -114,7 +114,10 @@ __device__ __forceinline__ void sp_exp32(const uint32_t (&v)[32], uint64_t c2, u
 
 // Producer's walk over the blocks of a tile's union, whole warp, in ascending order; of a cluster's
 // CTAs each takes every `splits`-th block. next() returns the block (-1 at the end) and its words;
-// it is called in one place, so that its state stays in registers.
+// it is called in one place, so that its state stays in registers. The words are read with ordinary
+// loads: the forward starts beside the kernel that writes them, and only its wait for that kernel
+// (grid_wait_previous) orders the two. A read through the read-only path (__ldg) would promise
+// memory that nothing writes while this kernel runs, and could be moved ahead of the wait.
 struct SpScan {
   int base = -32, turn = 0;
   uint32_t nz = 0u, w[4] = {0u, 0u, 0u, 0u};
@@ -130,7 +133,7 @@ struct SpScan {
         for (int k = 0; k < 4; ++k) {
           w[k] = 0u;
           if (base + lane < a.NB && k < t.nwords)
-            w[k] = __ldg(t.words + (size_t)k * a.NB + base + lane) & tmask;
+            w[k] = ld_global_u32(t.words + (size_t)k * a.NB + base + lane) & tmask;
         }
         nz = __ballot_sync(0xffffffffu, (w[0] | w[1] | w[2] | w[3]) != 0u);
       }

@@ -37,3 +37,39 @@ def test_forward_mode_derivatives_are_refused():
             torch.autograd.grad(out, qg, forward_ad.make_dual(do, torch.ones_like(do)))
     # Beside a dual level, tensors without a tangent are as ever.
     assert torch.equal(out.detach(), sparse.sparse_attention(q, k, v, idx, causal=True))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_every_call_reads_its_own_selection(d):
+    """The forward starts beside the kernel that writes its bit matrix, into memory that still holds
+    another call's: few and many tiles, lists of one row and of all blocks in turn, eager and in a
+    captured graph."""
+    for B, H, Hkv, nq, nk in ((1, 2, 1, 2, 5000), (2, 16, 16, 700, 900), (1, 8, 2, 3000, 3000)):
+        q, k, v, do = (t.cuda() for t in inputs(B, H, Hkv, nq, nk, d, seed=nq))
+        nb = sparse.num_blocks(nk)
+        g = torch.Generator().manual_seed(d)
+        picks = [torch.rand(B, Hkv, nq, nb, generator=g).argsort(-1)[..., :6].int().cuda()
+                 for _ in range(3)]
+        picks.append(torch.full_like(picks[0], -1))
+        alone = []
+        for idx in picks:
+            alone.append(sparse.streamkl_sparse_attn_fwd(q, k, v, idx, 0.125, True))
+            torch.cuda.synchronize()  # and its workspace goes to the next call
+        assert (alone[3][0] == 0).all() and not torch.equal(alone[0][0], alone[1][0])
+        for _ in range(8):
+            got = [sparse.streamkl_sparse_attn_fwd(q, k, v, idx, 0.125, True) for idx in picks]
+            torch.cuda.synchronize()
+            for want, have in zip(alone, got):
+                assert all(torch.equal(a, b) for a, b in zip(want, have))
+        # One workspace for every replay; the selection changes under it.
+        idx, graph = picks[0].clone(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out, lse = sparse.streamkl_sparse_attn_fwd(q, k, v, idx, 0.125, True)
+            grads = sparse.streamkl_sparse_attn_bwd(q, k, v, out, lse, do, idx, 0.125, True)
+        for want, new in zip(alone * 3, picks * 3):
+            idx.copy_(new)
+            graph.replay()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+            ref = sparse.streamkl_sparse_attn_bwd(q, k, v, *want, do, new, 0.125, True)
+            assert all(torch.equal(a, b) for a, b in zip(grads, ref))
+    assert skl.device_status() == 0

@@ -116,10 +116,28 @@ const int* lens_ptr(const OptTensor& lens, const Tensor& like, int64_t B) {
   return lens->const_data_ptr<int>();
 }
 
-Tensor scratch(long long bytes, const Tensor& like, const char* where) {
+// Workspace sizes that the library gives; -1: sizes that it rejects.
+long long accepted(long long bytes, const char* where) {
   if (bytes < 0) check(STREAMKL_ERR_UNSUPPORTED, where);
+  return bytes;
+}
+
+Tensor scratch(long long bytes, const Tensor& like) {
   return bytes ? at::empty({bytes}, like.options().dtype(at::kByte)) : Tensor();
 }
+
+// Gives up the interpreter lock while it lives, where the caller holds it (autograd's threads do
+// not): allocations, launches and the wait of a status check may take long or depend on work that
+// another Python thread of the process has yet to queue.
+class WithoutPython {
+ public:
+  WithoutPython() {
+    if (PyGILState_Check()) release_.emplace();
+  }
+
+ private:
+  std::optional<py::gil_scoped_release> release_;
+};
 
 void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
@@ -127,28 +145,38 @@ cudaStream_t stream_of(const Tensor& t) {
   return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
 }
 
-void check_device(bool on, const Tensor& t, const char* where) {
-  if (on) check(f_device_status(stream_of(t)), where);
+Tensor contiguous(const Tensor& t) {
+  if (t.is_contiguous()) return t;
+  const WithoutPython free;
+  return t.contiguous();
 }
+
+// The device's status once the stream of t is done, if asked for.
+int device_status(bool on, const Tensor& t) { return on ? f_device_status(stream_of(t)) : 0; }
 
 Tensor block_mass(const Tensor& q, const Tensor& k, double scale, bool causal, const OptTensor& lse,
                   const OptTensor& lens, bool check_status) {
   const Sizes s = qk_sizes(q, k);
-  const c10::cuda::CUDAGuard guard(q.device());
-  Tensor ws;
+  const int* n = lens_ptr(lens, q, s.B);
   if (lse) {
     want("lse", *lse, at::kFloat, q.device());
     want_shape("lse", *lse, {s.B, s.H, s.nq});
-  } else {
-    ws = scratch(f_mass_ws(s.B, s.H, s.Hkv, s.nq, s.nk, s.d), q, "block_mass");
   }
-  Tensor mass = at::empty({s.B, s.Hkv, s.nq, (s.nk + 63ll) / 64}, q.options().dtype(at::kFloat));
-  check(f_mass(q.const_data_ptr(), k.const_data_ptr(), lens_ptr(lens, q, s.B), s.B, s.H, s.Hkv, s.nq,
-               s.nk, s.d, static_cast<float>(scale), causal,
-               lse ? lse->const_data_ptr<float>() : nullptr, ptr(ws), ws.defined() ? ws.numel() : 0,
-               mass.data_ptr<float>(), stream_of(q)),
-        "block_mass");
-  check_device(check_status, q, "block_mass");
+  const c10::cuda::CUDAGuard guard(q.device());
+  const long long bytes =
+      lse ? 0 : accepted(f_mass_ws(s.B, s.H, s.Hkv, s.nq, s.nk, s.d), "block_mass");
+  Tensor mass;
+  int status;
+  {
+    const WithoutPython free;
+    const Tensor ws = scratch(bytes, q);
+    mass = at::empty({s.B, s.Hkv, s.nq, (s.nk + 63ll) / 64}, q.options().dtype(at::kFloat));
+    status = f_mass(q.const_data_ptr(), k.const_data_ptr(), n, s.B, s.H, s.Hkv, s.nq, s.nk, s.d,
+                    static_cast<float>(scale), causal, lse ? lse->const_data_ptr<float>() : nullptr,
+                    ptr(ws), bytes, mass.data_ptr<float>(), stream_of(q));
+    if (status == 0) status = device_status(check_status, q);
+  }
+  check(status, "block_mass");
   return mass;
 }
 
@@ -159,14 +187,20 @@ Tensor select_blocks(const Tensor& mass, int64_t n_k, int64_t topk, bool causal,
                     " blocks, n_k = ", n_k, " keys make ", (n_k + 63) / 64);
   TORCH_CHECK_VALUE(mass.is_cuda(), "mass must be on a CUDA device");
   want("mass", mass, at::kFloat, mass.device());
+  const int* n = lens_ptr(lens, mass, mass.size(0));
+  const int B = narrow(mass.size(0)), Hsel = narrow(mass.size(1)), nq = narrow(mass.size(2)),
+            nk = narrow(n_k), k = narrow(topk), first = narrow(n_first), last = narrow(n_last);
   const c10::cuda::CUDAGuard guard(mass.device());
-  Tensor idx = at::empty({mass.size(0), mass.size(1), mass.size(2), topk > 0 ? topk : 0},
-                         mass.options().dtype(at::kInt));
-  check(f_select(mass.const_data_ptr<float>(), lens_ptr(lens, mass, mass.size(0)),
-                 narrow(mass.size(0)), narrow(mass.size(1)), narrow(mass.size(2)), narrow(n_k), causal,
-                 narrow(topk), narrow(n_first), narrow(n_last), idx.data_ptr<int>(), stream_of(mass)),
-        "select_blocks");
-  check_device(check_status, mass, "select_blocks");
+  Tensor idx;
+  int status;
+  {
+    const WithoutPython free;
+    idx = at::empty({B, Hsel, nq, k > 0 ? k : 0}, mass.options().dtype(at::kInt));
+    status = f_select(mass.const_data_ptr<float>(), n, B, Hsel, nq, nk, causal, k, first, last,
+                      idx.data_ptr<int>(), stream_of(mass));
+    if (status == 0) status = device_status(check_status, mass);
+  }
+  check(status, "select_blocks");
   return idx;
 }
 
@@ -180,17 +214,24 @@ std::tuple<Tensor, Tensor> attn_fwd(const Tensor& q, const Tensor& k, const Tens
   TORCH_CHECK_VALUE(idx.dim() == 4, "block_idx must be [B, H_sel, N_Q, topk]");
   want_shape("block_idx", idx, {s.B, idx.size(1), s.nq, idx.size(3)});
   const int Hsel = narrow(idx.size(1)), topk = narrow(idx.size(3));
+  const int* n = lens_ptr(lens, q, s.B);
   const c10::cuda::CUDAGuard guard(q.device());
-  Tensor out = at::empty_like(q), lse;
-  if (with_lse) lse = at::empty({s.B, s.H, s.nq}, q.options().dtype(at::kFloat));
-  const Tensor ws = scratch(f_attn_ws(s.B, s.H, s.Hkv, Hsel, s.nq, s.nk, s.d, topk, 0), q,
-                            "sparse_attention");
-  check(f_fwd(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), idx.const_data_ptr<int>(),
-              lens_ptr(lens, q, s.B), s.B, s.H, s.Hkv, Hsel, s.nq, s.nk, s.d, topk,
-              static_cast<float>(scale), causal, ptr(ws), ws.defined() ? ws.numel() : 0, out.data_ptr(),
-              with_lse ? lse.data_ptr<float>() : nullptr, stream_of(q)),
-        "sparse_attention");
-  check_device(check_status, q, "sparse_attention forward");
+  const long long bytes =
+      accepted(f_attn_ws(s.B, s.H, s.Hkv, Hsel, s.nq, s.nk, s.d, topk, 0), "sparse_attention");
+  Tensor out, lse;
+  int status;
+  {
+    const WithoutPython free;
+    out = at::empty_like(q);
+    if (with_lse) lse = at::empty({s.B, s.H, s.nq}, q.options().dtype(at::kFloat));
+    const Tensor ws = scratch(bytes, q);
+    status = f_fwd(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(),
+                   idx.const_data_ptr<int>(), n, s.B, s.H, s.Hkv, Hsel, s.nq, s.nk, s.d, topk,
+                   static_cast<float>(scale), causal, ptr(ws), bytes, out.data_ptr(),
+                   with_lse ? lse.data_ptr<float>() : nullptr, stream_of(q));
+    if (status == 0) status = device_status(check_status, q);
+  }
+  check(status, "sparse_attention forward");
   return {out, lse};
 }
 
@@ -222,19 +263,28 @@ struct SparseAttention : torch::autograd::Function<SparseAttention> {
     const OptTensor lens = saved[6].defined() ? OptTensor(saved[6]) : std::nullopt;
     const c10::cuda::CUDAGuard guard(q.device());
     const Sizes s = qk_sizes(q, k);
-    const Tensor dout = grads[0].to(at::kBFloat16).contiguous();
-    Tensor dq = at::empty_like(q), dk = at::empty_like(k), dv = at::empty_like(v);
     const int Hsel = narrow(idx.size(1)), topk = narrow(idx.size(3));
-    const Tensor ws = scratch(f_attn_ws(s.B, s.H, s.Hkv, Hsel, s.nq, s.nk, s.d, topk, 1), q,
-                              "sparse_attention backward");
-    check(f_bwd(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), out.const_data_ptr(),
-                lse.const_data_ptr<float>(), dout.const_data_ptr(), idx.const_data_ptr<int>(),
-                lens_ptr(lens, q, s.B), s.B, s.H, s.Hkv, Hsel, s.nq, s.nk, s.d, topk,
-                static_cast<float>(ctx->saved_data["scale"].toDouble()),
-                ctx->saved_data["causal"].toBool(), ptr(ws), ws.numel(), dq.data_ptr(),
-                dk.data_ptr(), dv.data_ptr(), stream_of(q)),
-          "sparse_attention backward");
-    check_device(ctx->saved_data["check"].toBool(), q, "sparse_attention backward");
+    const int* n = lens_ptr(lens, q, s.B);
+    const long long bytes = accepted(f_attn_ws(s.B, s.H, s.Hkv, Hsel, s.nq, s.nk, s.d, topk, 1),
+                                     "sparse_attention backward");
+    Tensor dq, dk, dv;
+    int status;
+    {
+      const WithoutPython free;
+      const Tensor dout = grads[0].to(at::kBFloat16).contiguous();
+      dq = at::empty_like(q);
+      dk = at::empty_like(k);
+      dv = at::empty_like(v);
+      const Tensor ws = scratch(bytes, q);
+      status = f_bwd(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), out.const_data_ptr(),
+                     lse.const_data_ptr<float>(), dout.const_data_ptr(), idx.const_data_ptr<int>(), n,
+                     s.B, s.H, s.Hkv, Hsel, s.nq, s.nk, s.d, topk,
+                     static_cast<float>(ctx->saved_data["scale"].toDouble()),
+                     ctx->saved_data["causal"].toBool(), ptr(ws), bytes, dq.data_ptr(), dk.data_ptr(),
+                     dv.data_ptr(), stream_of(q));
+      if (status == 0) status = device_status(ctx->saved_data["check"].toBool(), q);
+    }
+    check(status, "sparse_attention backward");
     torch::autograd::variable_list d{dq, dk, dv};
     if (at::GradMode::is_enabled()) {  // create_graph: an error for whoever differentiates these
       for (Tensor& t : d) t.set_requires_grad(true);
@@ -264,7 +314,7 @@ std::tuple<Tensor, Tensor> sparse_attention(const Tensor& q, const Tensor& k, co
   refuse_tangent(q, "q");
   refuse_tangent(k, "k");
   refuse_tangent(v, "v");
-  const Tensor qc = q.contiguous(), kc = k.contiguous(), vc = v.contiguous(), ic = idx.contiguous();
+  const Tensor qc = contiguous(q), kc = contiguous(k), vc = contiguous(v), ic = contiguous(idx);
   if (at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad() || v.requires_grad())) {
     const c10::OptionalDeviceGuard guard(q.device());
     if (q.is_cuda() && c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {

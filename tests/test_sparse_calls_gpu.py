@@ -1,10 +1,13 @@
 """Ways of calling the block-sparse operators (needs a B200)."""
+import ctypes
+
 import pytest
 import torch
 from torch.autograd import forward_ad
 
 import attention_kl_divergence_fwd_b200 as skl
 from attention_kl_divergence_fwd_b200 import sparse
+from attention_kl_divergence_fwd_b200.autograd import set_check_status
 from test_sparse_gpu import inputs, lists
 
 pytestmark = pytest.mark.gpu
@@ -72,4 +75,37 @@ def test_every_call_reads_its_own_selection(d):
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
             ref = sparse.streamkl_sparse_attn_bwd(q, k, v, *want, do, new, 0.125, True)
             assert all(torch.equal(a, b) for a, b in zip(grads, ref))
+    assert skl.device_status() == 0
+
+
+def test_other_python_threads_run_during_a_call():
+    """Launches and the wait of a status check happen without the interpreter lock, which work queued
+    before them may need. The library's functions are replaced by one that says whether its
+    caller holds the lock; as a status, 1 is an error."""
+    q, k, v, do = (t.cuda() for t in inputs(1, 4, 2, 20, 130, 64, seed=43))
+    idx = lists(1, 2, 20, 130, 2, seed=43).cuda()
+    mass = torch.zeros(1, 2, 20, 3, device="cuda")
+    leaf = q.clone().requires_grad_()
+    calls = [lambda: sparse.block_mass(q, k), lambda: sparse.select_blocks(mass, 130, 2),
+             lambda: sparse.sparse_attention(q, k, v, idx),
+             lambda: torch.autograd.grad(sparse.sparse_attention(leaf, k, v, idx), leaf, do)]
+    ext = sparse._ext()
+    at = lambda f: ctypes.cast(f, ctypes.c_void_p).value
+    lib = skl.load_library()
+    real = [at(getattr(lib, "streamkl_" + n)) for n in (
+        "block_mass", "block_mass_workspace", "block_select", "sparse_attn_workspace",
+        "sparse_attn_fwd", "sparse_attn_bwd", "status_string", "device_status")]
+    held = at(ctypes.pythonapi.PyGILState_Check)
+    try:
+        set_check_status(True)
+        # Every launch, then every status check.
+        for fake in ([held if j in (0, 2, 4, 5) else a for j, a in enumerate(real)],
+                     real[:7] + [held]):
+            ext.bind(fake)
+            for call in calls:
+                call()
+    finally:
+        ext.bind(real)
+        set_check_status(False)
+    torch.cuda.synchronize()
     assert skl.device_status() == 0

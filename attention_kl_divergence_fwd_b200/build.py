@@ -17,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -51,11 +52,24 @@ def up_to_date() -> bool:
 
 
 def build_dispatch(force: bool = False, verbose: bool = False) -> str:
+    from .sparse import dispatch_current
     deps = [DISPATCH_SOURCE, os.path.join(ROOT, "include", "streamkl.h")]
-    if not force and os.path.exists(DISPATCH) and all(
-            os.path.getmtime(p) <= os.path.getmtime(DISPATCH) for p in deps):
+    stale = not dispatch_current() or any(
+        os.path.getmtime(p) > os.path.getmtime(DISPATCH) for p in deps)
+    if not force and not stale:
         return DISPATCH
+    try:
+        _compile_dispatch(verbose)
+    except (OSError, RuntimeError):
+        if stale and os.path.exists(DISPATCH):  # of other sources or another PyTorch: better none
+            os.remove(DISPATCH)
+        raise
+    return DISPATCH
+
+
+def _compile_dispatch(verbose: bool) -> None:
     import torch
+    from .sparse import dispatch_marker
     base = os.path.dirname(torch.__file__)
     include = [os.path.join(base, "include"),
                os.path.join(base, "include", "torch", "csrc", "api", "include"),
@@ -69,7 +83,8 @@ def build_dispatch(force: bool = False, verbose: bool = False) -> str:
     # beside PyTorch's, and the two break each other's streams.
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-DTORCH_EXTENSION_NAME=_sparse_dispatch", "-DTORCH_API_INCLUDE_EXTENSION_H",
+           f'-DBUILT_FOR="{dispatch_marker()}"', "-DTORCH_EXTENSION_NAME=_sparse_dispatch",
+           "-DTORCH_API_INCLUDE_EXTENSION_H",
            *(f"-I{p}" for p in include), DISPATCH_SOURCE, "-o", tmp, f"-L{lib}", "-lc10",
            "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     if verbose:
@@ -79,13 +94,21 @@ def build_dispatch(force: bool = False, verbose: bool = False) -> str:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"{cmd[0]} failed with exit code {res.returncode}")
     os.replace(tmp, DISPATCH)
-    return DISPATCH
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_dispatch(force, verbose)
-    if not force and up_to_date():
-        return LIB
+    """The library, and the dispatch module where it can be built: without g++, Python's headers or
+    a CUDA build of PyTorch the block-sparse calls raise OSError and everything else works."""
+    if force or not up_to_date():
+        _compile_library(verbose)
+    try:
+        build_dispatch(force, verbose)
+    except (OSError, RuntimeError) as e:
+        warnings.warn(f"the block-sparse calls are not available: {e}")
+    return LIB
+
+
+def _compile_library(verbose: bool) -> None:
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-I",
@@ -99,7 +122,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"nvcc failed with exit code {res.returncode}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -331,6 +331,7 @@ std::tuple<Tensor, Tensor> sparse_attention(const Tensor& q, const Tensor& k, co
 }  // namespace
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
+  m.attr("built_for") = BUILT_FOR;  // sparse.py looks for this text in the file
   m.def("bind", &bind);
   m.def("block_mass", &block_mass);
   m.def("select_blocks", &select_blocks);

@@ -30,6 +30,7 @@ import importlib.util
 import inspect
 import math
 import os
+import sys
 from typing import Optional
 
 import torch
@@ -240,14 +241,27 @@ def streamkl_sparse_attn_bwd(q, k, v, out, lse, dout, block_idx, scale: float, c
 _dispatch = None
 
 
+def dispatch_marker() -> str:
+    """What a dispatch module has to be built for: its interface to PyTorch and Python is theirs."""
+    return f"block-sparse dispatch for PyTorch {torch.__version__}, Python {sys.version_info[:2]}."
+
+
+def dispatch_current() -> bool:
+    """Whether the dispatch module that is there was built for this PyTorch and Python."""
+    if not os.path.exists(DISPATCH_PATH):
+        return False
+    with open(DISPATCH_PATH, "rb") as f:
+        return dispatch_marker().encode() in f.read()
+
+
 def _ext():
-    """The C++ side of the calls below (raises OSError if it has not been built): checks,
-    allocations and the autograd node without Python's share of a short call."""
+    """The C++ side of the calls below (raises OSError if it has not been built for this PyTorch and
+    Python): checks, allocations and the autograd node without Python's share of a short call."""
     global _dispatch
     if _dispatch is None:
         lib = load_library()
-        if not os.path.exists(DISPATCH_PATH):
-            raise OSError(f"block-sparse dispatch not built: {DISPATCH_PATH} "
+        if not dispatch_current():
+            raise OSError(f"block-sparse dispatch not built for this PyTorch: {DISPATCH_PATH} "
                           "(run python -m attention_kl_divergence_fwd_b200.build)")
         spec = importlib.util.spec_from_file_location("_sparse_dispatch", DISPATCH_PATH)
         ext = importlib.util.module_from_spec(spec)

@@ -145,17 +145,22 @@ cudaStream_t stream_of(const Tensor& t) {
   return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
 }
 
-Tensor contiguous(const Tensor& t) {
-  if (t.is_contiguous()) return t;
+// t as the library takes it: contiguous and at a multiple of 16 bytes, a copy where it is not (a view
+// may begin anywhere in its storage).
+Tensor laid_out(const Tensor& t) {
+  const bool contiguous = t.is_contiguous();
+  if (contiguous && reinterpret_cast<uintptr_t>(t.const_data_ptr()) % 16 == 0) return t;
   const WithoutPython free;
-  return t.contiguous();
+  return contiguous ? t.clone(at::MemoryFormat::Contiguous) : t.contiguous();
 }
 
 // The device's status once the stream of t is done, if asked for.
 int device_status(bool on, const Tensor& t) { return on ? f_device_status(stream_of(t)) : 0; }
 
-Tensor block_mass(const Tensor& q, const Tensor& k, double scale, bool causal, const OptTensor& lse,
-                  const OptTensor& lens, bool check_status) {
+Tensor block_mass(const Tensor& q_in, const Tensor& k_in, double scale, bool causal,
+                  const OptTensor& lse_in, const OptTensor& lens, bool check_status) {
+  const Tensor q = laid_out(q_in), k = laid_out(k_in);
+  const OptTensor lse = lse_in ? OptTensor(laid_out(*lse_in)) : std::nullopt;
   const Sizes s = qk_sizes(q, k);
   const int* n = lens_ptr(lens, q, s.B);
   if (lse) {
@@ -180,8 +185,9 @@ Tensor block_mass(const Tensor& q, const Tensor& k, double scale, bool causal, c
   return mass;
 }
 
-Tensor select_blocks(const Tensor& mass, int64_t n_k, int64_t topk, bool causal, int64_t n_first,
+Tensor select_blocks(const Tensor& mass_in, int64_t n_k, int64_t topk, bool causal, int64_t n_first,
                      int64_t n_last, const OptTensor& lens, bool check_status) {
+  const Tensor mass = laid_out(mass_in);
   TORCH_CHECK_VALUE(mass.dim() == 4, "mass must be [B, H_sel, N_Q, NB]");
   TORCH_CHECK_VALUE(n_k >= 0 && (n_k + 63) / 64 == mass.size(3), "mass has ", mass.size(3),
                     " blocks, n_k = ", n_k, " keys make ", (n_k + 63) / 64);
@@ -271,7 +277,7 @@ struct SparseAttention : torch::autograd::Function<SparseAttention> {
     int status;
     {
       const WithoutPython free;
-      const Tensor dout = grads[0].to(at::kBFloat16).contiguous();
+      const Tensor dout = laid_out(grads[0].to(at::kBFloat16));
       dq = at::empty_like(q);
       dk = at::empty_like(k);
       dv = at::empty_like(v);
@@ -314,7 +320,7 @@ std::tuple<Tensor, Tensor> sparse_attention(const Tensor& q, const Tensor& k, co
   refuse_tangent(q, "q");
   refuse_tangent(k, "k");
   refuse_tangent(v, "v");
-  const Tensor qc = contiguous(q), kc = contiguous(k), vc = contiguous(v), ic = contiguous(idx);
+  const Tensor qc = laid_out(q), kc = laid_out(k), vc = laid_out(v), ic = laid_out(idx);
   if (at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad() || v.requires_grad())) {
     const c10::OptionalDeviceGuard guard(q.device());
     if (q.is_cuda() && c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {

@@ -12,7 +12,9 @@ and, serving one token against a padded cache (``seqlens_k``: keys of each seque
 calls with ``N_Q = 1`` and without ``lse``; ``student_sparse_attention`` makes the three in a row.
 
 Tensors are bf16 [B, heads, N, d] on one CUDA device, d in {64, 128}; K heads may be shared by a
-group of query heads, and one selection may serve several K heads. Calls run on the current (or
+group of query heads, and one selection may serve several K heads. Views that are not contiguous
+or begin at no multiple of 16 bytes are copied by the call (the raw ``streamkl_*`` calls refuse
+them). Calls run on the current (or
 the given) stream and allocate outputs and workspace from PyTorch's allocator, which makes them
 safe to capture into a CUDA graph (a backward through ``torch.autograd.grad``: ``.backward()``
 accumulates into leaves on the stream where eager code first used them; leaves whose eager graph
@@ -292,9 +294,9 @@ def block_mass(q_s, k_s, scale: Optional[float] = None, causal: bool = False, ls
     if scale is None:
         scale = 1.0 / math.sqrt(q_s.shape[-1])
     if lse is not None:
-        lse = lse.detach().contiguous()
-    return _ext().block_mass(q_s.detach().contiguous(), k_s.detach().contiguous(), scale, causal, lse,
-                             _lens_arg(seqlens_k), autograd._check_status)
+        lse = lse.detach()
+    return _ext().block_mass(q_s.detach(), k_s.detach(), scale, causal, lse, _lens_arg(seqlens_k),
+                             autograd._check_status)
 
 
 def select_blocks(mass, n_k: int, topk: int, causal: bool = False, n_first: int = 1,
@@ -302,7 +304,7 @@ def select_blocks(mass, n_k: int, topk: int, causal: bool = False, n_first: int 
     """Of the blocks a query sees: the first ``n_first``, the last ``n_last`` and the heaviest of
     the rest, ``topk`` in all: int32 [B, H_sel, N_Q, topk], ascending, -1 behind the last.
     Equal masses go to the lower index, NaN ranks below every number."""
-    return _ext().select_blocks(mass.contiguous(), n_k, topk, causal, n_first, n_last,
+    return _ext().select_blocks(mass, n_k, topk, causal, n_first, n_last,
                                 _lens_arg(seqlens_k), autograd._check_status)
 
 

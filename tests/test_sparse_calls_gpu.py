@@ -109,3 +109,42 @@ def test_other_python_threads_run_during_a_call():
         set_check_status(False)
     torch.cuda.synchronize()
     assert skl.device_status() == 0
+
+
+def odd(t):
+    """The same values behind one element of the same storage: contiguous, at an address that is no
+    multiple of 16."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    flat[1:] = t.reshape(-1)
+    r = flat[1:].view(t.shape)
+    assert r.is_contiguous() and r.data_ptr() % 16
+    return r
+
+
+def test_contiguous_views_at_any_address():
+    """Laid out by the call, as other strides are."""
+    q, k, v, do = (t.cuda() for t in inputs(2, 4, 2, 70, 300, 64, seed=42))
+    idx = lists(2, 2, 70, 300, 4, seed=42).cuda()
+    lse = sparse.streamkl_sparse_attn_fwd(q, k, torch.zeros_like(k),
+                                          torch.arange(5, dtype=torch.int32, device="cuda")
+                                          .expand(2, 2, 70, 5).contiguous(), 0.125, True)[1]
+    mass = sparse.block_mass(q, k, causal=True, lse=lse)
+    assert torch.equal(sparse.block_mass(odd(q), k, causal=True, lse=odd(lse)), mass)
+    assert torch.equal(sparse.block_mass(q, odd(k), causal=True),
+                       sparse.block_mass(q, k, causal=True))
+    sel = sparse.select_blocks(mass, 300, 3, True)
+    assert torch.equal(sparse.select_blocks(odd(mass), 300, 3, True), sel)
+    leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+    out = sparse.sparse_attention(*leaves, idx, causal=True)
+    ref = torch.autograd.grad(out, leaves, do)
+    moved = [odd(t).requires_grad_() for t in (q, k, v)]
+    got = sparse.sparse_attention(*moved, odd(idx), causal=True)
+    assert torch.equal(got, out)
+    for a, b in zip(torch.autograd.grad(got, moved, odd(do)), ref):
+        assert torch.equal(a, b)
+    # One sequence of a batch of single-token masses: 65 blocks of one head.
+    m = torch.rand(3, 1, 1, 65, device="cuda")
+    for b in range(3):
+        assert torch.equal(sparse.select_blocks(m[b:b + 1], 65 * 64, 4),
+                           sparse.select_blocks(m[b:b + 1].clone(), 65 * 64, 4))
+    assert skl.device_status() == 0

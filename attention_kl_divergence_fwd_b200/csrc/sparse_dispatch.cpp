@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <limits>
+#include <string>
 #include <tuple>
 
 #include "streamkl.h"
@@ -241,18 +242,45 @@ std::tuple<Tensor, Tensor> attn_fwd(const Tensor& q, const Tensor& k, const Tens
   return {out, lse};
 }
 
+bool capturing() {
+  return c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None;
+}
+
+// A gradient goes on to the stream on which the function that made the tensor ran, or, for a leaf, on
+// which the oldest graph that still holds it began. A backward captured meanwhile would make that
+// stream wait for the capture, which for the default stream CUDA takes as an error on a thread of
+// autograd's, and the process ends. So leaves of such a graph are refused while capturing;
+// other tensors are noted (the text for a refusal is returned), because a captured forward alone
+// is sound: their backward is refused.
+std::string check_capture(const Tensor& t, const char* name) {
+  if (!t.requires_grad()) return {};
+  const auto node = t.is_leaf() ? torch::autograd::impl::try_get_grad_accumulator(t)
+                                : torch::autograd::impl::gradient_edge(t).function;
+  if (node == nullptr) return {};
+  const auto stream = node->stream();
+  if (!stream ||
+      c10::cuda::CUDAStream(*stream) != c10::cuda::getDefaultCUDAStream(t.device().index()))
+    return {};
+  const std::string part = std::string("sparse_attention: ") + name +
+                           " is part of a graph made on the default stream; release that graph "
+                           "(or pass " + name + ".detach().requires_grad_()) ";
+  TORCH_CHECK(!t.is_leaf(), part, "before capturing a CUDA graph");
+  return part;
+}
+
 // Attention over selected blocks as an autograd node; gradients flow to q, k and v.
 struct SparseAttention : torch::autograd::Function<SparseAttention> {
   static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx, const Tensor& q,
                                                 const Tensor& k, const Tensor& v, const Tensor& idx,
                                                 const OptTensor& lens, double scale, bool causal,
-                                                bool check_status) {
+                                                bool check_status, const std::string& eager) {
     at::AutoDispatchBelowADInplaceOrView below;
     auto [out, lse] = attn_fwd(q, k, v, idx, lens, scale, causal, true, check_status);
     ctx->save_for_backward({q, k, v, out, lse, idx, lens ? *lens : Tensor()});
     ctx->saved_data["scale"] = scale;
     ctx->saved_data["causal"] = causal;
     ctx->saved_data["check"] = check_status;
+    if (!eager.empty()) ctx->saved_data["eager"] = eager;
     ctx->mark_non_differentiable({lse});
     ctx->set_materialize_grads(false);
     return {out, lse};
@@ -260,9 +288,12 @@ struct SparseAttention : torch::autograd::Function<SparseAttention> {
 
   static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
                                                  torch::autograd::variable_list grads) {
-    torch::autograd::variable_list none(8);
+    torch::autograd::variable_list none(9);
     if (!grads[0].defined()) return none;
     refuse_tangent(grads[0], "dout");
+    const auto eager = ctx->saved_data.find("eager");
+    TORCH_CHECK(eager == ctx->saved_data.end() || !capturing(), eager->second.toStringRef(),
+                "before capturing its backward");
     const auto saved = ctx->get_saved_variables();
     const Tensor &q = saved[0], &k = saved[1], &v = saved[2], &out = saved[3], &lse = saved[4],
                  &idx = saved[5];
@@ -301,19 +332,6 @@ struct SparseAttention : torch::autograd::Function<SparseAttention> {
   }
 };
 
-// While an eager graph of a leaf lives, its gradient goes to the stream that this graph began on. A
-// backward captured meanwhile would make the default stream wait for the capture, which CUDA takes
-// as an error on a thread of autograd's and the process ends: such leaves are refused.
-void check_capture(const Tensor& t, const char* name) {
-  if (!t.requires_grad() || !t.is_leaf()) return;
-  const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
-  if (node == nullptr) return;
-  const auto stream = node->stream();
-  TORCH_CHECK(!stream || c10::cuda::CUDAStream(*stream) != c10::cuda::getDefaultCUDAStream(t.device().index()),
-              "sparse_attention: ", name, " is part of a graph made on the default stream; release "
-              "that graph (or pass ", name, ".detach().requires_grad_()) before capturing a CUDA graph");
-}
-
 std::tuple<Tensor, Tensor> sparse_attention(const Tensor& q, const Tensor& k, const Tensor& v,
                                             const Tensor& idx, const OptTensor& lens, double scale,
                                             bool causal, bool with_lse, bool check_status) {
@@ -323,12 +341,11 @@ std::tuple<Tensor, Tensor> sparse_attention(const Tensor& q, const Tensor& k, co
   const Tensor qc = laid_out(q), kc = laid_out(k), vc = laid_out(v), ic = laid_out(idx);
   if (at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad() || v.requires_grad())) {
     const c10::OptionalDeviceGuard guard(q.device());
-    if (q.is_cuda() && c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
-      check_capture(q, "q");
-      check_capture(k, "k");
-      check_capture(v, "v");
-    }
-    auto r = SparseAttention::apply(qc, kc, vc, ic, lens, scale, causal, check_status);
+    std::string eager;
+    if (q.is_cuda() && capturing())
+      for (const std::string& e : {check_capture(q, "q"), check_capture(k, "k"), check_capture(v, "v")})
+        if (eager.empty()) eager = e;
+    auto r = SparseAttention::apply(qc, kc, vc, ic, lens, scale, causal, check_status, eager);
     return {r[0], r[1]};
   }
   return attn_fwd(qc, kc, vc, ic, lens, scale, causal, with_lse, check_status);

@@ -148,3 +148,40 @@ def test_contiguous_views_at_any_address():
         assert torch.equal(sparse.select_blocks(m[b:b + 1], 65 * 64, 4),
                            sparse.select_blocks(m[b:b + 1].clone(), 65 * 64, 4))
     assert skl.device_status() == 0
+
+
+def test_captured_backward_of_inputs_computed_before():
+    """The captured forward of a tensor that eager code computed is sound, its captured backward would
+    go on into the eager part: refused, and the capture is as good as before."""
+    q, k, v, do = (t.cuda() for t in inputs(1, 4, 2, 70, 300, 64, seed=44))
+    idx = lists(1, 2, 70, 300, 4, seed=44).cuda()
+    leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+    made = [t * 1 for t in leaves]  # on the default stream, with a gradient function
+    plain = [t.clone().requires_grad_() for t in (q, k, v)]
+    out = sparse.sparse_attention(*plain, idx, causal=True)
+    ref = torch.autograd.grad(out, plain, do)
+    want = out.detach().clone()
+    del out
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kept = []
+        for j in range(3):
+            args = [t.detach().requires_grad_() for t in made]
+            args[j] = made[j]
+            kept.append(sparse.sparse_attention(*args, idx, causal=True))
+            for inputs_ in ([leaves[j]], [made[j]]):
+                with pytest.raises(RuntimeError, match="qkv"[j] + " is part of a graph made on the default"):
+                    torch.autograd.grad(kept[j], inputs_, do, retain_graph=True)
+        args = [t.detach().requires_grad_() for t in made]
+        kept.append(sparse.sparse_attention(*args, idx, causal=True))
+        grads = torch.autograd.grad(kept[3], args, do)
+    for t in (*kept, *grads):
+        t.detach().zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want) for t in kept)
+    assert all(torch.equal(a, b) for a, b in zip(grads, ref))
+    # Eager again.
+    eager = torch.autograd.grad(sparse.sparse_attention(*made, idx, causal=True), leaves, do)
+    assert all(torch.equal(a, b) for a, b in zip(eager, ref))
+    assert skl.device_status() == 0

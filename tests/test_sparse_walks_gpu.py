@@ -149,3 +149,44 @@ def test_selection_of_every_width(nq, nk, lens, topk, first, last):
                                None if lt is None else lt.cuda())
     assert torch.equal(got.cpu(), oracle_block_select(mass, nk, topk, True, first, last, lt))
     assert skl.device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradients_of_queries_and_keys_against_differences(d):
+    """Central differences of the kernel's forward, along steps of one query (one key) that bf16
+    holds exactly, against its gradient. Bound: the outputs' and the gradient's own (oracle), and
+    what the oracle says the quotient differs from the derivative by."""
+    nq, nk, scale = 40, 150, 0.25
+    q, k, v, do = inputs(1, 2, 1, nq, nk, d, seed=45)
+    grid = lambda t: (t.float().clamp(-3, 3) * 16).round() / 16  # 7 bits with a step
+    q, k, v = (grid(t).to(torch.bfloat16) for t in (q, k, v))
+    # One output entry, of values of either sign: its derivatives are well above the bound.
+    do = torch.zeros_like(do)
+    do[0, 1, 30, 0] = 1
+    v[..., 0] = torch.where(torch.arange(nk) % 2 == 0, 3, -3)
+    idx = torch.arange(3, dtype=torch.int32).expand(1, 1, nq, 3).contiguous()
+    tol = {}
+    _, _, dq, dk, _ = oracle_sparse_attn(q, k, v, idx, scale, True, None, do, tol)
+    key = int(dk[0, 0].norm(dim=-1).argmax())
+    leaves = [t.cuda().requires_grad_() for t in (q, k, v)]
+    grads = torch.autograd.grad(sparse.sparse_attention(*leaves, idx.cuda(), scale, True), leaves,
+                                do.cuda())
+    for which, at, exact, name in ((0, (0, 1, 30), dq, "dq"), (1, (0, 0, key), dk, "dk")):
+        step = torch.zeros_like((q, k)[which])
+        step[at] = torch.sign(exact[at]).to(torch.bfloat16) / 16
+        value, oracle, bound = [], [], 0.0
+        for s in (1, -1):
+            args = [q, k]
+            args[which] = args[which] + s * step
+            assert torch.equal(args[which].double(), (q, k)[which].double() + s * step.double())
+            t = {}
+            out, _ = oracle_sparse_attn(*args, v, idx, scale, True, bounds=t)
+            oracle.append((out * do.double()).sum().item())
+            bound += (t["out"] * do.double().abs()).sum().item() / 2
+            got = sparse.sparse_attention(*(x.cuda() for x in (*args, v)), idx.cuda(), scale, True)
+            value.append((got.cpu().double() * do.double()).sum().item())
+        along = (grads[which].cpu().double() * step.double()).sum().item()
+        truth = (exact * step.double()).sum().item()
+        bound += abs((oracle[0] - oracle[1]) / 2 - truth) + (tol[name] * step.double().abs()).sum().item()
+        assert abs((value[0] - value[1]) / 2 - along) <= bound
+        assert bound < truth / 2  # the test can tell

@@ -10,8 +10,8 @@
 // narrows to the gap behind the topk-th key in a few steps (6 on average for 256 blocks), and the
 // search ends with the first threshold in that gap, or, with ties, at the topk-th key itself. The
 // selection is then written by ranks in index order, which gives the ascending list and the
-// ties' order without a sort. One warp per row when there are many rows, four or eight when there
-// are few or long ones. Bound by issue slots (89 %) for many rows: 131072 rows of up to 256 blocks
+// ties' order without a sort. One warp per row when there are many rows, eight when there are few
+// or when a row has more than 1024 blocks. Bound by issue slots (89 %) for many rows: 131072 rows of up to 256 blocks
 // 62 us (1.2 TB/s of masses), of which the bisection is 8 us and the stores 10; by latency for few:
 // 512 rows of 1024 blocks 6.4 us.
 #pragma once

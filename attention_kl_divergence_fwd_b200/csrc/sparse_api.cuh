@@ -100,7 +100,9 @@ int sparse_splits(const skl::SparseArgs& a) {
 // first one) has n_tiles steps while the average one has its share of the lists, so with few
 // heads its CTA alone outlasts the rest of the grid. A CTA of a cluster costs about 17 steps
 // (measured: 1024 clusters of two instead of 1024 CTAs take 238 us more at 16384 tokens, 4 K
-// heads), so blocks are split only when the longest one dominates.
+// heads), so blocks are split only when the longest one dominates. That figure, and the 1.3 lists'
+// worth of blocks that a tile is taken to read, come from d = 128 and lists that runs of 128 queries
+// share; they are estimates for d = 64 and for unrelated lists, which only the split depends on.
 int sparse_kv_splits(const skl::SparseArgs& a) {
   const double longest = (double)a.n_tiles * (a.P / a.Hkv), heads = (double)a.B * a.Hkv;
   const double per_tile = a.NB < 1.3 * a.topk ? a.NB : 1.3 * a.topk;

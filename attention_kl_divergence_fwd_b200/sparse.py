@@ -12,17 +12,20 @@ and, serving one token against a padded cache (``seqlens_k``: keys of each seque
 calls with ``N_Q = 1`` and without ``lse``; ``student_sparse_attention`` makes the three in a row.
 
 Tensors are bf16 [B, heads, N, d] on one CUDA device, d in {64, 128}; K heads may be shared by a
-group of query heads, and one selection may serve several K heads. Views that are not contiguous
-or begin at no multiple of 16 bytes are copied by the call (the raw ``streamkl_*`` calls refuse
-them). Calls run on the current (or the given) stream and allocate outputs and workspace from
-PyTorch's allocator, which makes them safe to capture into a CUDA graph (a backward through
-``torch.autograd.grad``: ``.backward()`` accumulates into leaves on the stream where eager code
-first used them; leaves whose eager graph from the default stream still lives are refused while
-capturing, and so is the captured backward of inputs that eager code computed there). With status
-checks on (``autograd.set_check_status``, read by the forward for its backward too) every call waits
-for its kernels and raises their errors. The selection has no gradient, the attention's gradients
-are not differentiable again, and forward-mode derivatives (``torch.autograd.forward_ad``) through
-the attention are refused.
+group of query heads, and one selection may serve several K heads. Views that are not contiguous or
+begin at no multiple of 16 bytes are copied by the call (the raw ``streamkl_*`` calls refuse them).
+The first ``seqlens_k`` (or N_K) keys and values, and all queries and output gradients, have to be
+finite: queries are computed in tiles, and a NaN or infinity in a block that one query of a tile
+lists can reach the tile's others. What a padded cache holds behind them may be anything. Calls run
+on the current (or the given) stream and allocate outputs and workspace from PyTorch's allocator,
+which makes them safe to capture into a CUDA graph (a backward through ``torch.autograd.grad``:
+``.backward()`` accumulates into leaves on the stream where eager code first used them; leaves whose
+eager graph from the default stream still lives are refused while capturing, and so is the captured
+backward of inputs that eager code computed there). With status checks on
+(``autograd.set_check_status``, read by the forward for its backward too) every call waits for its
+kernels and raises their errors. The selection has no gradient, the attention's gradients are not
+differentiable again, and forward-mode derivatives (``torch.autograd.forward_ad``) through the
+attention are refused.
 """
 from __future__ import annotations
 
